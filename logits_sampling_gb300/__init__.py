@@ -5,7 +5,9 @@ current CUDA stream) and calls the C ABI declared in include/ls_sampler.h:
 ``ls_sample``, ``ls_sample_speculative``, ``ls_log_probs``,
 ``ls_sample_log_probs``, ``ls_sample_log_probs_noalloc``, ``ls_sample_device_step``,
 ``ls_argmax``, ``ls_verify_chain``, ``ls_sample_verify``, ``ls_set_split_policy`` and
-``ls_set_log_prob_write_policy``.  Every step of the
+``ls_set_log_prob_write_policy``, and those of include/ls_row_ops.h around the
+sampler: ``ls_process_logits``, ``ls_top_log_probs``, ``ls_distill_loss``,
+``ls_distill_loss_backward`` and ``ls_distill_loss_grad``.  Every step of the
 sampling path runs in the library's CUDA kernels; there is no CPU fallback.
 If the library has not been built (``python -m logits_sampling_gb300.build``)
 or no CUDA device is present, the calls raise.
@@ -34,4 +36,16 @@ from ._binding import (  # noqa: F401
     set_split_policy,
     status_string,
     verify_chain,
+)
+from ._row_ops import (  # noqa: F401
+    LS_ROW_ERR_BAD_MASK,
+    MAX_TOP,
+    LogitsParams,
+    distill,
+    distill_loss,
+    distill_loss_backward,
+    distill_loss_grad,
+    process_logits,
+    row_ops_max_vocab,
+    top_log_probs,
 )

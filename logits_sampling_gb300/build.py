@@ -2,7 +2,7 @@
 
     python -m logits_sampling_gb300.build [--force]
 
-Compiles logits_sampling_gb300/csrc/*.cu into logits_sampling_gb300/libls_sampler.so
+Compiles logits_sampling_gb300/csrc/*.cu and csrc/ops/*.cu into logits_sampling_gb300/libls_sampler.so
 (-gencode arch=compute_103a,code=sm_103a, -O3, -lineinfo, no fast-math).  The
 build is skipped when the library is newer than every source and header.
 
@@ -39,11 +39,11 @@ def _nvcc():
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "ops", "*.cu")))
 
 
 def _inputs():
-    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
+    return sources() + sorted(glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True)) + sorted(
         glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
 
 
