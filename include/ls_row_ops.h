@@ -29,8 +29,9 @@
 extern "C" {
 #endif
 
-/* One more row error: mask_index[i] outside [-1, mask_rows). */
-enum { LS_ROW_ERR_BAD_MASK = 8 };
+/* Further row errors: mask_index[i] outside [-1, mask_rows); a copy that did
+ * not arrive within about two seconds (the row's results are undefined). */
+enum { LS_ROW_ERR_BAD_MASK = 8, LS_ROW_ERR_STALLED = 16 };
 
 /* Per-request parameters of ls_process_logits: device arrays indexed by
  * request, owned by the caller.  Any group may be absent (NULL). */
@@ -131,13 +132,16 @@ typedef struct {
   int32_t k;      /* 1 <= k <= LS_MAX_TOP */
 } ls_teacher;
 
+/* Floats per row that ls_distill_loss leaves for ls_distill_loss_backward. */
+#define LS_DISTILL_STATS 8
+
 /*
  * ls_distill_loss -- loss[i] = weights[i] * KL(teacher || student) of row i.
  *
  * With z = logits / temperature, q = softmax(z), p_k = exp(log_probs[k]) and
  * P = sum p_k:
  *   DROP     sum_k p_k (ln p_k - ln q_k)
- *   RENORM   the same with p_k / P
+ *   RENORM   the same with p_k / P (P below 2^-100: no targets)
  *   BUCKET   DROP plus p_r (ln p_r - ln q_r), p_r = max(0, 1 - P), q_r the
  *            student's mass outside the k ids (the term is left out where
  *            p_r = 0 or no entry above -inf lies outside them)
@@ -147,10 +151,8 @@ typedef struct {
  *
  *   weights    device float[n] or NULL (1)
  *   out_loss   device float[n]
- *   out_stats  device float[4 n], 16-byte aligned, or NULL: what the backward
- *              pass needs of row i: its maximum M, sum exp((x - M) / T), and
- *              the same two over the entries outside the teacher's ids
- *              (-inf and 0 where there is none)
+ *   out_stats  device float[LS_DISTILL_STATS * n], 16-byte aligned, or NULL:
+ *              what the backward pass needs of each row
  * LS_ERR_UNSUPPORTED: vocab above ls_row_ops_max_vocab(dtype).
  */
 ls_status ls_distill_loss(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, int32_t n,

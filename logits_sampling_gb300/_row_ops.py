@@ -6,8 +6,9 @@ from dataclasses import dataclass
 
 from ._binding import LS_OK, LSError, _dptr, _i32, _logits_desc, _on, load_library
 
-LS_ROW_ERR_BAD_MASK = 8
+LS_ROW_ERR_BAD_MASK, LS_ROW_ERR_STALLED = 8, 16
 MAX_TOP = 256  # LS_MAX_TOP
+DISTILL_STATS = 8  # LS_DISTILL_STATS
 TAILS = {"drop": 0, "renorm": 1, "bucket": 2}
 
 _P, _i32t, _i64t, _f32t, _ci = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_int
@@ -258,7 +259,7 @@ def _tail(tail):
 
 def distill_loss(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="bucket", weights=None, out=None,
                  out_stats=None, error_word=None, stream=None):
-    """ls_distill_loss: returns (loss float32 [n], stats float32 [n, 4]); stats
+    """ls_distill_loss: returns (loss float32 [n], stats float32 [n, 8]); stats
     goes to distill_loss_backward."""
     import torch
     lib = _lib()
@@ -269,10 +270,10 @@ def distill_loss(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="
         if out is None:
             out = torch.empty(n, dtype=torch.float32, device=logits.device)
         if out_stats is None:
-            out_stats = torch.empty((n, 4), dtype=torch.float32, device=logits.device)
+            out_stats = torch.empty((n, DISTILL_STATS), dtype=torch.float32, device=logits.device)
         st = lib.ls_distill_loss(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
                                  _f32(weights, "weights", n), _f32(out, "out", n),
-                                 _f32(out_stats, "out_stats", 4 * n), _i32(error_word, "error_word"), s.cuda_stream)
+                                 _f32(out_stats, "out_stats", DISTILL_STATS * n), _i32(error_word, "error_word"), s.cuda_stream)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss")
     return out, out_stats
@@ -292,7 +293,7 @@ def distill_loss_backward(logits, teacher_ids, teacher_log_probs, stats, grad_lo
             out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
         out_stride = _like(out, logits, n, "out")
         st = lib.ls_distill_loss_backward(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
-                                          _f32(weights, "weights", n), _f32(stats, "stats", 4 * n),
+                                          _f32(weights, "weights", n), _f32(stats, "stats", DISTILL_STATS * n),
                                           _f32(grad_loss, "grad_loss", n), out.data_ptr(), out_stride, s.cuda_stream)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss_backward")

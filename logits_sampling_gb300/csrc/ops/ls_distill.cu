@@ -2,14 +2,29 @@
 // its gradient (ls_distill_loss, ls_distill_loss_backward,
 // ls_distill_loss_grad).
 //
-// One CTA per row.  A bitmap in shared memory marks the teacher's ids; maximum
-// and sum of exponentials are taken over the entries outside them, so that the
-// mass outside (q_r) is a sum of its own and not a difference of two sums; the
-// at most 256 entries inside join afterwards.
-#include "ls_row_ops.cuh"
+// Loss, and loss with gradient (distill_kernel): the row lies in the shared
+// memory of a cluster (ls_slice.cuh) and is read from global memory once.  The
+// teacher's entries are taken out of it first (their logits go to every CTA,
+// their places become -inf), so the sums that follow run over the entries
+// outside them, and the mass outside (q_r) is a sum of its own rather than a
+// difference of two.  With R the row's entries outside the ids, of maximum
+// M_r, and e_j = exp((x_j - M_r) / T), the gradient outside the ids is one
+// multiple of e_j:
+//     d_j = g / T * e_j * kappa,   kappa = A exp((M_r - M) / T) / S - p_r / S_r
+// and the at most 256 ids follow one by one: g / T * (alpha exp((x - M) / T) -
+// p), alpha = A / S.  M_r, kappa, M, alpha and the scale of p are the row's
+// `stats`: the backward pass (distill_backward_kernel) reads them and nothing
+// else of the forward pass, and is one sweep over the logits in tiles.
+#include "ls_slice.cuh"
 
 namespace lsg {
 namespace ops {
+
+// What the backward pass needs of a row (LS_DISTILL_STATS floats).
+struct alignas(16) RowStats {
+  float M, alpha, Mr, kappa, scale, pad[3];
+};
+static_assert(sizeof(RowStats) == sizeof(float) * LS_DISTILL_STATS, "the header's size of a row's stats");
 
 struct DistillArgs {
   const void* logits;
@@ -19,143 +34,312 @@ struct DistillArgs {
   int tail;
   const float* weights;
   const float* grad_loss;
-  const float4* stats_in;
+  const RowStats* stats_in;
   float* out_loss;
-  float4* out_stats;
+  RowStats* out_stats;
   void* out_grad;
   int64_t grad_stride;
   int32_t* error_word;
 };
 
-struct OpMaxF {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+// A teacher's mass below this is none to renormalise (its reciprocal would overflow).
+constexpr float kLeastMass = 7.8886e-31f;  // 2^-100
+
+// Gradient of a unit outside the ids: coef * exp((x - m) / T).
+template <typename TIn>
+__device__ __forceinline__ uint4 unit_grad(uint4 w, const ExpAgainst& x, float coef_fast, float coef) {
+  constexpr int kN = Unit<TIn>::kN;
+  w = Unit<TIn>::clean(w);
+  float d[kN];
+  if (x.fast) {
+#pragma unroll
+    for (int q = 0; q < kN / 2; ++q)
+      unpack2(mul2(x.pair_fast(Unit<TIn>::pair(w, q)), pack2(coef_fast, coef_fast)), d[2 * q], d[2 * q + 1]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kN / 2; ++q)
+      unpack2(mul2(x.pair_slow(Unit<TIn>::pair(w, q)), pack2(coef, coef)), d[2 * q], d[2 * q + 1]);
+  }
+  return Unit<TIn>::make(d);
+}
+
+__device__ __forceinline__ void store_unit(void* p, uint4 v) {
+  asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Writes the slice's entries of an output row: unit by unit where the output
+// row starts at the input row's alignment, else entry by entry.  `unit(u)`
+// gives the 16 bytes that belong to the slice's unit u.
+template <typename TIn, typename F>
+__device__ __forceinline__ void write_slice(const Slice<TIn>& s, typename Elem<TIn>::Raw* out, F unit) {
+  using Raw = typename Elem<TIn>::Raw;
+  constexpr int kN = Unit<TIn>::kN;
+  const int f = s.full_first(), l = s.full_last();
+  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(s.row)) & 15u) == 0;
+  for (int u = threadIdx.x; u < s.n; u += kSliceThreads) {
+    const uint4 v = unit(u);
+    const int64_t j = s.index(u * kN);
+    if (same && u >= f && u < l) {
+      store_unit(out + j, v);
+    } else {
+      Raw e[kN];
+      memcpy(e, &v, 16);
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        if (j + q >= 0 && j + q < s.V) out[j + q] = e[q];
+    }
+  }
+}
+
+// Everything of a row but its entries: written by warp 0 of each CTA from the
+// same numbers, so every CTA holds the same bits.
+struct RowShared {
+  uint64_t bars[kChunks];
+  float2 ms[kMaxCluster];  // each CTA's maximum and sum over the entries outside the ids
+  float x[LS_MAX_TOP];     // the student's logits at the ids (-inf where there is none)
+  float p[LS_MAX_TOP];
+  float lp[LS_MAX_TOP];
+  float red[kSliceWarps];
+  RowStats st;
 };
 
-// exp((v - M) / T) for v <= M; entries at an infinite maximum share it.
-__device__ __forceinline__ float rel_exp(float v, float M, float c) { return v == M ? 1.f : ex2((v - M) * c); }
-
-template <typename TIn, bool kLoss, bool kGrad>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a) {
+template <typename TIn, bool kGrad>
+__global__ void __launch_bounds__(kSliceThreads, 3) distill_kernel(const DistillArgs a, int upc) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
-  extern __shared__ uint32_t bits[];  // ceil(vocab / 32)
-  __shared__ float red_f[kWarps];
-  const int tid = threadIdx.x;
-  const int64_t i = blockIdx.x, V = a.vocab;
+  extern __shared__ uint4 slice_smem[];
+  __shared__ RowShared sh;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  const int64_t i = blockIdx.x / (unsigned)C;
   const float w = a.weights ? a.weights[i] : 1.f;
-  const Raw* row = static_cast<const Raw*>(a.logits) + i * a.row_stride;
+  Slice<TIn> s;
+  s.init(slice_smem, a.logits, i, a.row_stride, a.vocab, upc, rank);
   Raw* grad = kGrad ? static_cast<Raw*>(a.out_grad) + i * a.grad_stride : nullptr;
-  if (w == 0.f) {
-    if (kGrad)
-      for (int64_t j = tid; j < V; j += kThreads) grad[j] = E::put(0.f);
-    if (tid == 0 && kLoss) {
+  if (w == 0.f) {  // every CTA of the row leaves here, before any cluster barrier
+    if (kGrad) write_slice<TIn>(s, grad, [](int) { return make_uint4(0u, 0u, 0u, 0u); });
+    if (tid == 0 && rank == 0) {
       a.out_loss[i] = 0.f;
-      if (a.out_stats) a.out_stats[i] = make_float4(0.f, 1.f, 0.f, 1.f);
+      if (a.out_stats) a.out_stats[i] = RowStats{0.f, 0.f, 0.f, 0.f, 1.f, {}};
     }
     return;
   }
+  s.start(sh.bars);
+  if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
   // the teacher's entry of this thread
   int id = -1;
-  float t = kNegInf, p = 0.f, x = kNegInf;
-  if (tid < a.t.k) {
-    id = a.t.ids[i * a.t.stride + tid];
-    t = a.t.log_probs[i * a.t.stride + tid];
-    if (id < 0 || (int64_t)id >= V || !(t > kNegInf)) id = -1;
-    if (id >= 0) {
-      x = guard(E::get(row[id]));
-      p = expf(t);
+  float x = kNegInf, p = 0.f;
+  if (tid < LS_MAX_TOP) {
+    float t = kNegInf;
+    if (tid < a.t.k) {
+      id = a.t.ids[i * a.t.stride + tid];
+      t = a.t.log_probs[i * a.t.stride + tid];
+      if (id < 0 || (int64_t)id >= a.vocab || !(t > kNegInf)) id = -1;
+      if (id >= 0) p = expf(t);
     }
+    sh.lp[tid] = t;
+    sh.p[tid] = p;
+    if (id < 0) sh.x[tid] = kNegInf;
   }
-  const int words = (int)((V + 31) / 32);
-  for (int q = tid; q < words; q += kThreads) bits[q] = 0u;
+  bool stalled = false;
+  for (int k = 0; k < kChunks; ++k)
+    if (!mbar_wait(&sh.bars[k])) stalled = true;
   __syncthreads();
-  if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
-  const float P = block_reduce(p, OpAddF(), red_f);  // the barriers inside order the bitmap too
-  auto listed = [&](int64_t j) { return (bits[j >> 5] >> (j & 31)) & 1u; };
-
+  if (C > 1) cluster_wait();
+  const int mine = id >= 0 ? s.entry(id) : -1;
+  if (mine >= 0) {
+    x = guard(E::get(s.raw()[mine]));
+    if (C > 1) {
+      for (int q = 0; q < C; ++q) peer_store(peer_addr(smem_addr(&sh.x[tid]), q), x);
+    } else {
+      sh.x[tid] = x;
+    }
+    s.raw()[mine] = E::neg_inf();
+  }
+  __syncthreads();
   const float c = kLog2e / a.temperature;
-  float M, S, Mr, Sr;
-  if (kLoss) {
-    float m = kNegInf;
-    for (int64_t j = tid; j < V; j += kThreads)
-      if (!listed(j)) m = fmaxf(m, guard(E::get(row[j])));
-    Mr = block_reduce(m, OpMaxF(), red_f);
-    float s = 0.f;
-    if (Mr > kNegInf)
-      for (int64_t j = tid; j < V; j += kThreads)
-        if (!listed(j)) s += rel_exp(guard(E::get(row[j])), Mr, c);
-    Sr = block_reduce(s, OpAddF(), red_f);
-    M = fmaxf(Mr, block_reduce(x, OpMaxF(), red_f));
-    S = block_reduce(id >= 0 && M > kNegInf ? rel_exp(x, M, c) : 0.f, OpAddF(), red_f);
-    if (Mr > kNegInf) S += Sr * rel_exp(Mr, M, c);
-    if (tid == 0 && a.out_stats) a.out_stats[i] = make_float4(M, S, Mr, Sr);
+  const float m = block_max(slice_max(s, sh.bars, &stalled), sh.red);
+  ExpAgainst against;
+  against.init(m, c);
+  const float sum = block_sum(slice_sum(s, against), sh.red);
+  if (tid < C) {
+    if (C > 1)
+      peer_store2(peer_addr(smem_addr(&sh.ms[rank]), tid), m, sum);
+    else
+      sh.ms[0] = make_float2(m, sum);
+  }
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
   } else {
-    const float4 st = a.stats_in[i];
-    M = st.x;
-    S = st.y;
-    Mr = st.z;
-    Sr = st.w;
+    __syncthreads();
   }
-  if (M == kNegInf) {
-    if (kGrad)
-      for (int64_t j = tid; j < V; j += kThreads) grad[j] = E::put(quiet_nan());
-    if (tid == 0 && kLoss) {
-      a.out_loss[i] = quiet_nan();
-      if (a.error_word) atomicOr(a.error_word, LS_ROW_ERR_NO_FINITE);
+  if (tid < 32) {
+    constexpr int kPer = LS_MAX_TOP / 32;
+    const float2 ms = lane < C ? sh.ms[lane] : make_float2(kNegInf, 0.f);
+    const float Mr = warp_max(ms.x);
+    const float Sr = Mr > kNegInf ? warp_reduce(ms.x > kNegInf ? ms.y * rel_exp(ms.x, Mr, c) : 0.f, OpAddF()) : 0.f;
+    float xk[kPer], mt = kNegInf, P = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      xk[q] = sh.x[lane + 32 * q];
+      mt = fmaxf(mt, xk[q]);
+      P += sh.p[lane + 32 * q];
     }
-    return;
+    const float M = fmaxf(Mr, warp_max(mt));
+    P = warp_reduce(P, OpAddF());
+    float S = 0.f;
+    if (M > kNegInf) {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) S += xk[q] > kNegInf ? rel_exp(xk[q], M, c) : 0.f;
+    }
+    S = warp_reduce(S, OpAddF());
+    const float rest = Mr > kNegInf ? rel_exp(Mr, M, c) : 0.f;
+    S += Sr * rest;
+    float A = P, scale = 1.f, pr = 0.f;
+    if (a.tail == LS_TAIL_RENORM) {
+      const bool some = P >= kLeastMass;
+      A = some ? 1.f : 0.f;
+      scale = some ? 1.f / P : 0.f;
+    } else if (a.tail == LS_TAIL_BUCKET && Mr > kNegInf) {
+      pr = fmaxf(1.f - P, 0.f);
+      A = P + pr;
+    }
+    RowStats st = {M, A / S, Mr, 0.f, scale, {}};
+    if (Mr > kNegInf) st.kappa = st.alpha * rest - (pr > 0.f ? pr / Sr : 0.f);
+    if (M == kNegInf) st.alpha = st.kappa = quiet_nan();
+    if (lane == 0) sh.st = st;
+    __syncwarp();
+    if (rank == 0) {
+      const float lnS = logf(S), lnP = a.tail == LS_TAIL_RENORM ? logf(P) : 0.f;
+      float kl = 0.f;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const float pk = sh.p[lane + 32 * q] * scale;
+        if (pk > 0.f)
+          kl += pk * ((sh.lp[lane + 32 * q] - lnP) - ((xk[q] == M ? 0.f : (xk[q] - M) / a.temperature) - lnS));
+      }
+      if (lane == 0 && pr > 0.f) kl += pr * (logf(pr) - ((Mr == M ? 0.f : (Mr - M) / a.temperature) + logf(Sr / S)));
+      kl = warp_reduce(kl, OpAddF());
+      if (lane == 0) {
+        a.out_loss[i] = M == kNegInf ? quiet_nan() : w * kl;
+        if (a.out_stats) a.out_stats[i] = st;
+        if (a.error_word && M == kNegInf) atomicOr(a.error_word, LS_ROW_ERR_NO_FINITE);
+      }
+    }
   }
-  float lnP = 0.f;
-  float A = P;
-  if (a.tail == LS_TAIL_RENORM) {
-    lnP = logf(P);
-    p = p / P;
-    if (!(P > 0.f)) p = 0.f;
-    A = P > 0.f ? 1.f : 0.f;
-  }
-  float pr = 0.f;
-  if (a.tail == LS_TAIL_BUCKET && Mr > kNegInf) {
-    pr = fmaxf(1.f - P, 0.f);
-    A = P + pr;
-  }
-  if (kLoss) {
-    const float lnS = logf(S);
-    float term = 0.f;
-    if (p > 0.f) term = p * ((t - lnP) - ((x == M ? 0.f : (x - M) / a.temperature) - lnS));
-    if (tid == 0 && pr > 0.f)
-      term += pr * (logf(pr) - ((Mr == M ? 0.f : (Mr - M) / a.temperature) + logf(Sr / S)));
-    const float kl = block_reduce(term, OpAddF(), red_f);
-    if (tid == 0) a.out_loss[i] = w * kl;
-  }
+  if (stalled && a.error_word) atomicOr(a.error_word, LS_ROW_ERR_STALLED);
   if (kGrad) {
-    const float g = w * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
-    const float gA = g * (A / S), gR = pr > 0.f ? g * (pr / Sr) : 0.f;
-    for (int64_t j = tid; j < V; j += kThreads) {
-      if (listed(j)) continue;
-      const float v = guard(E::get(row[j]));
-      float d = gA * rel_exp(v, M, c);
-      if (gR != 0.f) d -= gR * rel_exp(v, Mr, c);
-      grad[j] = E::put(d);
-    }
-    if (id >= 0) grad[id] = E::put(gA * rel_exp(x, M, c) - g * p);
+    __syncthreads();
+    const RowStats st = sh.st;
+    const float g = w / a.temperature;
+    against.init(st.Mr, c);
+    const float coef = g * st.kappa;
+    write_slice<TIn>(s, grad, [&](int u) { return unit_grad<TIn>(s.buf[u], against, coef * against.scale, coef); });
+    __syncthreads();
+    if (mine >= 0) grad[id] = E::put(g * (st.alpha * rel_exp(x, st.M, c) - p * st.scale));
   }
 }
 
-template <typename TIn, bool kLoss, bool kGrad>
-static ls_status launch(const DistillArgs& a, int32_t n, cudaStream_t st) {
-  const size_t smem = (size_t)((a.vocab + 31) / 32) * 4;
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(distill_kernel<TIn, kLoss, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return LS_ERR_CUDA;
-  distill_kernel<TIn, kLoss, kGrad><<<dim3((unsigned)n), dim3(kThreads), smem, st>>>(a);
-  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+// The backward pass alone: a tile of kBackUnits units per thread, loaded to
+// registers before anything is written (the gradient may replace the logits).
+constexpr int kBackThreads = 256;
+constexpr int kBackUnits = 4;
+
+template <typename TIn>
+__global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const DistillArgs a, int tiles) {
+  using E = Elem<TIn>;
+  using Raw = typename E::Raw;
+  constexpr int kN = Unit<TIn>::kN;
+  const int tid = threadIdx.x;
+  const int64_t i = blockIdx.x / (unsigned)tiles;
+  const int tile = (int)(blockIdx.x % (unsigned)tiles);
+  Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
+  const float g = (a.weights ? a.weights[i] : 1.f) * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
+  Slice<TIn> s;  // of this tile, left in global memory
+  s.init(nullptr, a.logits, i, a.row_stride, a.vocab, kBackThreads * kBackUnits, tile);
+  const int f = s.full_first(), l = s.full_last();
+  const RowStats st = a.stats_in[i];
+  const float c = kLog2e / a.temperature;
+  uint4 v[kBackUnits];
+  if (g != 0.f) {
+#pragma unroll
+    for (int k = 0; k < kBackUnits; ++k) {
+      const int u = tid + k * kBackThreads;
+      const int64_t j = s.index(u * kN);
+      if (u >= f && u < l) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                     : "l"(s.row + j));
+      } else if (u < s.n) {
+        Raw e[kN];
+#pragma unroll
+        for (int q = 0; q < kN; ++q) e[q] = j + q >= 0 && j + q < s.V ? s.row[j + q] : E::neg_inf();
+        memcpy(&v[k], e, 16);
+      }
+    }
+  }
+  int id = -1;
+  float x = kNegInf, p = 0.f;
+  if (tid < a.t.k && g != 0.f) {
+    id = a.t.ids[i * a.t.stride + tid];
+    const float t = a.t.log_probs[i * a.t.stride + tid];
+    if (id < 0 || (int64_t)id >= a.vocab || !(t > kNegInf) || s.entry(id) < 0) id = -1;
+    if (id >= 0) {
+      p = expf(t) * st.scale;
+      x = guard(E::get(s.row[id]));
+    }
+  }
+  ExpAgainst against;
+  against.init(st.Mr, c);
+  const float coef = g * st.kappa;
+  const bool same = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(s.row)) & 15u) == 0;
+  __syncthreads();  // every load of the tile is done
+#pragma unroll
+  for (int k = 0; k < kBackUnits; ++k) {
+    const int u = tid + k * kBackThreads;
+    if (u >= s.n) break;
+    const uint4 d = g == 0.f ? make_uint4(0u, 0u, 0u, 0u) : unit_grad<TIn>(v[k], against, coef * against.scale, coef);
+    const int64_t j = s.index(u * kN);
+    if (same && u >= f && u < l) {
+      store_unit(grad + j, d);
+    } else {
+      Raw e[kN];
+      memcpy(e, &d, 16);
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        if (j + q >= 0 && j + q < s.V) grad[j + q] = e[q];
+    }
+  }
+  __syncthreads();
+  if (id >= 0) grad[id] = E::put(g * (st.alpha * rel_exp(x, st.M, c) - p));
 }
 
-template <bool kLoss, bool kGrad>
+template <typename TIn, bool kGrad>
+static ls_status launch(const DistillArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
+  static std::atomic<int> done[kMaxDevices];
+  const SlicePlan plan = plan_slices(n, a.vocab, dtype);
+  return launch_slices(distill_kernel<TIn, kGrad>, a, plan, plan.smem, n, st, done);
+}
+
+template <bool kGrad>
 static ls_status dispatch(const DistillArgs& a, ls_dtype dtype, int32_t n, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == LS_DTYPE_BF16 ? launch<bf16_tag, kLoss, kGrad>(a, n, st) : launch<float, kLoss, kGrad>(a, n, st);
+  return dtype == LS_DTYPE_BF16 ? launch<bf16_tag, kGrad>(a, dtype, n, st) : launch<float, kGrad>(a, dtype, n, st);
+}
+
+static ls_status dispatch_backward(const DistillArgs& a, ls_dtype dtype, int32_t n, void* stream) {
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t e = dtype == LS_DTYPE_F32 ? 4 : 2;
+  const int64_t units = (a.vocab * e + 15 - e) / 16 + 1;
+  const int64_t tiles = (units + kBackThreads * kBackUnits - 1) / (kBackThreads * kBackUnits);
+  if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(tiles * n)), block(kBackThreads);
+  if (dtype == LS_DTYPE_BF16)
+    distill_backward_kernel<bf16_tag><<<grid, block, 0, st>>>(a, (int)tiles);
+  else
+    distill_backward_kernel<float><<<grid, block, 0, st>>>(a, (int)tiles);
+  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
 }
 
 // The checks that the three calls share.
@@ -188,9 +372,9 @@ ls_status ls_distill_loss(const void* logits, ls_dtype dtype, int64_t vocab, int
   if (rc != LS_OK) return rc;
   if (!out_loss || !stats_ok(out_stats)) return LS_ERR_INVALID_ARG;
   const DistillArgs a{logits,  vocab,   row_stride, *teacher, temperature, (int)tail,
-                      weights, nullptr, nullptr,    out_loss, reinterpret_cast<float4*>(out_stats),
+                      weights, nullptr, nullptr,    out_loss, reinterpret_cast<RowStats*>(out_stats),
                       nullptr, 0,       error_word};
-  return dispatch<true, false>(a, dtype, n, stream);
+  return dispatch<false>(a, dtype, n, stream);
 }
 
 ls_status ls_distill_loss_backward(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, int32_t n,
@@ -205,9 +389,9 @@ ls_status ls_distill_loss_backward(const void* logits, ls_dtype dtype, int64_t v
       !overlap_ok(logits, n, row_stride, out_grad, n, grad_stride, vocab, dtype, true))
     return LS_ERR_INVALID_ARG;
   const DistillArgs a{logits,   vocab,     row_stride,  *teacher, temperature, (int)tail,
-                      weights,  grad_loss, reinterpret_cast<const float4*>(stats), nullptr, nullptr,
+                      weights,  grad_loss, reinterpret_cast<const RowStats*>(stats), nullptr, nullptr,
                       out_grad, grad_stride, nullptr};
-  return dispatch<false, true>(a, dtype, n, stream);
+  return dispatch_backward(a, dtype, n, stream);
 }
 
 ls_status ls_distill_loss_grad(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, int32_t n,
@@ -223,7 +407,7 @@ ls_status ls_distill_loss_grad(const void* logits, ls_dtype dtype, int64_t vocab
     return LS_ERR_INVALID_ARG;
   const DistillArgs a{logits,  vocab,   row_stride, *teacher, temperature, (int)tail,   weights,
                       nullptr, nullptr, out_loss,   nullptr,  out_grad,    grad_stride, error_word};
-  return dispatch<true, true>(a, dtype, n, stream);
+  return dispatch<true>(a, dtype, n, stream);
 }
 
 }  // extern "C"

@@ -59,9 +59,9 @@ static int device_attr() {
   return v;
 }
 
-// Largest vocab of the calls that take a whole row at once: eight slices of at
-// most 192 KB of shared memory.
-static inline int64_t max_row(ls_dtype dtype) { return 8 * (int64_t)(192 * 1024) / (dtype == LS_DTYPE_F32 ? 4 : 2); }
+// Largest vocab of the calls that hold a whole row in shared memory: sixteen
+// slices of at most 160 KB.
+static inline int64_t max_row(ls_dtype dtype) { return 16 * (int64_t)(160 * 1024) / (dtype == LS_DTYPE_F32 ? 4 : 2); }
 
 static inline bool matrix_ok(const void* p, ls_dtype dtype, int64_t vocab, int64_t row_stride) {
   if (!p || (dtype != LS_DTYPE_F32 && dtype != LS_DTYPE_BF16)) return false;
