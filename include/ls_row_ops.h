@@ -29,9 +29,8 @@
 extern "C" {
 #endif
 
-/* Further row errors: mask_index[i] outside [-1, mask_rows); a copy that did
- * not arrive within about two seconds (the row's results are undefined). */
-enum { LS_ROW_ERR_BAD_MASK = 8, LS_ROW_ERR_STALLED = 16 };
+/* One more row error: mask_index[i] outside [-1, mask_rows). */
+enum { LS_ROW_ERR_BAD_MASK = 8 };
 
 /* Per-request parameters of ls_process_logits: device arrays indexed by
  * request, owned by the caller.  Any group may be absent (NULL). */

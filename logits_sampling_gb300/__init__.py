@@ -39,7 +39,6 @@ from ._binding import (  # noqa: F401
 )
 from ._row_ops import (  # noqa: F401
     LS_ROW_ERR_BAD_MASK,
-    LS_ROW_ERR_STALLED,
     MAX_TOP,
     LogitsParams,
     distill,

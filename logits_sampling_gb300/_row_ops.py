@@ -2,11 +2,15 @@
 biases and masks before sampling, top log-probs beside it, the distillation
 loss and its gradient."""
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass
 
-from ._binding import LS_OK, LSError, _dptr, _i32, _logits_desc, _on, load_library
+from ._binding import LS_DTYPE_BF16, LS_DTYPE_F32, LS_OK, LSError, load_library
 
-LS_ROW_ERR_BAD_MASK, LS_ROW_ERR_STALLED = 8, 16
+torch = None  # imported by the first call: building the library needs no torch
+_DTYPES = {}
+
+LS_ROW_ERR_BAD_MASK = 8
 MAX_TOP = 256  # LS_MAX_TOP
 DISTILL_STATS = 8  # LS_DISTILL_STATS
 TAILS = {"drop": 0, "renorm": 1, "bucket": 2}
@@ -44,10 +48,19 @@ def configure(lib):
 _ready = None
 
 
+def _need_torch():
+    global torch
+    if torch is None:
+        import torch as t
+        torch = t
+        _DTYPES.update({t.float32: LS_DTYPE_F32, t.bfloat16: LS_DTYPE_BF16})
+
+
 def _lib():
     global _ready
     lib = load_library()
     if _ready is not lib:
+        _need_torch()
         _ready = configure(lib)
     return lib
 
@@ -57,21 +70,54 @@ def row_ops_max_vocab(dtype):
     return int(_lib().ls_row_ops_max_vocab(int(dtype)))
 
 
-def _f32(t, what, n=None):
-    import torch
+_HERE = nullcontext()
+
+
+def _where(stream):
+    """The raw stream that a call runs on, and a context in which outputs are
+    allocated on it (the current stream needs none)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), _HERE
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _matrix(logits):
+    """(pointer, dtype, rows, vocab, row stride) of a logits matrix."""
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [rows, vocab]")
+    stride, inner = logits.stride()
+    if inner != 1:
+        raise ValueError("logits rows must be contiguous (stride(1) == 1)")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    rows, vocab = logits.shape
+    return logits.data_ptr(), dt, rows, vocab, stride if rows > 1 else max(stride, vocab)
+
+
+def _vec(t, dtype, what, n=None):
+    """The pointer of an optional contiguous device tensor of at least n entries."""
     if t is None:
         return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{what} must be float32")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {str(dtype)[6:]}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
     if n is not None and t.numel() < n:
         raise ValueError(f"{what} has {t.numel()} entries, {n} are needed")
-    return _dptr(t)
+    return t.data_ptr()
 
 
-def _ints(t, what, n=None):
-    if t is not None and n is not None and t.numel() < n:
-        raise ValueError(f"{what} has {t.numel()} entries, {n} are needed")
-    return _i32(t, what)
+def _f32(t, what, n=None):
+    return _vec(t, torch.float32, what, n)
+
+
+def _i32(t, what, n=None):
+    return _vec(t, torch.int32, what, n)
 
 
 def _like(t, logits, n, what):
@@ -82,7 +128,7 @@ def _like(t, logits, n, what):
         raise ValueError(f"{what}'s rows must be contiguous (stride(1) == 1)")
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    return t.stride(0)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 @dataclass(frozen=True, eq=False)
@@ -109,6 +155,7 @@ class LogitsParams:
         object.__setattr__(self, "_struct", self._marshal())
 
     def _marshal(self):
+        _need_torch()
         per_request = {"prompt_lens": self.prompt_lens, "seq_lens": self.seq_lens,
                        "repetition_penalty": self.repetition_penalty, "presence_penalty": self.presence_penalty,
                        "frequency_penalty": self.frequency_penalty}
@@ -117,7 +164,6 @@ class LogitsParams:
         if self.tokens is not None:
             if self.tokens.dim() != 2 or (self.tokens.shape[1] > 1 and self.tokens.stride(1) != 1):
                 raise ValueError("tokens must be [requests, capacity] with contiguous rows")
-            import torch
             if self.tokens.dtype != torch.int32:
                 raise TypeError("tokens must be int32")
             if not self.tokens.is_cuda:
@@ -152,7 +198,6 @@ class LogitsParams:
         """Builds the tensors from host lists: `histories` a list of id lists
         (with room for `capacity` ids each), `biases` a list of {id: bias} dicts."""
         import numpy as np
-        import torch
 
         def dev(v, dtype):
             return None if v is None else torch.from_numpy(np.ascontiguousarray(v, dtype)).to(device)
@@ -181,9 +226,8 @@ def process_logits(logits, n=None, params=None, gather_indices=None, token_to_re
     """ls_process_logits: returns out ([n, vocab] of the logits' type).  out may
     be the logits themselves (no gather_indices).  allowed_mask int32
     [mask_rows, >= ceil(vocab / 32)]."""
-    import torch
     lib = _lib()
-    ptr, dt, rows, V, stride = _logits_desc(logits)
+    ptr, dt, rows, V, stride = _matrix(logits)
     if n is None:
         n = len(gather_indices) if gather_indices is not None else rows
     n = int(n)
@@ -195,17 +239,17 @@ def process_logits(logits, n=None, params=None, gather_indices=None, token_to_re
             raise ValueError("expected a CUDA tensor")
         mask_ptr, mask_rows = allowed_mask.data_ptr(), allowed_mask.shape[0]
         mask_stride = allowed_mask.stride(0) if mask_rows > 1 else allowed_mask.shape[1]
-    s, ctx = _on(stream)
+    s, ctx = _where(stream)
     with ctx:
         if out is None:
             out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
         out_stride = _like(out, logits, n, "out")
         st = lib.ls_process_logits(
-            ptr, dt, rows, V, stride, n, _ints(gather_indices, "gather_indices", n),
-            _ints(token_to_request_index, "token_to_request_index", n),
-            None if params is None else ctypes.byref(params._struct), _ints(row_lens, "row_lens", n), mask_ptr,
-            mask_rows, mask_stride, _ints(mask_index, "mask_index", n), out.data_ptr(), out_stride,
-            _i32(error_word, "error_word"), s.cuda_stream)
+            ptr, dt, rows, V, stride, n, _i32(gather_indices, "gather_indices", n),
+            _i32(token_to_request_index, "token_to_request_index", n),
+            None if params is None else ctypes.byref(params._struct), _i32(row_lens, "row_lens", n), mask_ptr,
+            mask_rows, mask_stride, _i32(mask_index, "mask_index", n), out.data_ptr(), out_stride,
+            _i32(error_word, "error_word"), s)
     if st != LS_OK:
         raise LSError(st, "ls_process_logits")
     return out
@@ -214,13 +258,12 @@ def process_logits(logits, n=None, params=None, gather_indices=None, token_to_re
 def top_log_probs(logits, k, n=None, temperature=1.0, gather_indices=None, out_ids=None, out_log_probs=None,
                   out_lse=None, error_word=None, stream=None):
     """ls_top_log_probs: returns (ids int32 [n, k], log_probs float32 [n, k], lse float32 [n])."""
-    import torch
     lib = _lib()
-    ptr, dt, rows, V, stride = _logits_desc(logits)
+    ptr, dt, rows, V, stride = _matrix(logits)
     if n is None:
         n = len(gather_indices) if gather_indices is not None else rows
     n, k = int(n), int(k)
-    s, ctx = _on(stream)
+    s, ctx = _where(stream)
     with ctx:
         if out_ids is None:
             out_ids = torch.empty((n, k), dtype=torch.int32, device=logits.device)
@@ -228,17 +271,16 @@ def top_log_probs(logits, k, n=None, temperature=1.0, gather_indices=None, out_i
             out_log_probs = torch.empty((n, k), dtype=torch.float32, device=logits.device)
         if out_lse is None:
             out_lse = torch.empty(n, dtype=torch.float32, device=logits.device)
-        st = lib.ls_top_log_probs(ptr, dt, rows, V, stride, n, _ints(gather_indices, "gather_indices", n), k,
-                                  float(temperature), _ints(out_ids, "out_ids", n * k),
+        st = lib.ls_top_log_probs(ptr, dt, rows, V, stride, n, _i32(gather_indices, "gather_indices", n), k,
+                                  float(temperature), _i32(out_ids, "out_ids", n * k),
                                   _f32(out_log_probs, "out_log_probs", n * k), _f32(out_lse, "out_lse", n),
-                                  _i32(error_word, "error_word"), s.cuda_stream)
+                                  _i32(error_word, "error_word"), s)
     if st != LS_OK:
         raise LSError(st, f"ls_top_log_probs (k = {k}; at most {MAX_TOP})")
     return out_ids, out_log_probs, out_lse
 
 
 def _teacher(ids, log_probs, n):
-    import torch
     if ids.dim() != 2 or ids.shape != log_probs.shape or ids.shape[0] != n:
         raise ValueError(f"teacher_ids and teacher_log_probs must both be [{n}, k]")
     if ids.dtype != torch.int32 or log_probs.dtype != torch.float32:
@@ -261,11 +303,10 @@ def distill_loss(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="
                  out_stats=None, error_word=None, stream=None):
     """ls_distill_loss: returns (loss float32 [n], stats float32 [n, 8]); stats
     goes to distill_loss_backward."""
-    import torch
     lib = _lib()
-    ptr, dt, n, V, stride = _logits_desc(logits)
+    ptr, dt, n, V, stride = _matrix(logits)
     t = _teacher(teacher_ids, teacher_log_probs, n)
-    s, ctx = _on(stream)
+    s, ctx = _where(stream)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.float32, device=logits.device)
@@ -273,7 +314,7 @@ def distill_loss(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="
             out_stats = torch.empty((n, DISTILL_STATS), dtype=torch.float32, device=logits.device)
         st = lib.ls_distill_loss(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
                                  _f32(weights, "weights", n), _f32(out, "out", n),
-                                 _f32(out_stats, "out_stats", DISTILL_STATS * n), _i32(error_word, "error_word"), s.cuda_stream)
+                                 _f32(out_stats, "out_stats", DISTILL_STATS * n), _i32(error_word, "error_word"), s)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss")
     return out, out_stats
@@ -283,18 +324,17 @@ def distill_loss_backward(logits, teacher_ids, teacher_log_probs, stats, grad_lo
                           tail="bucket", weights=None, out=None, stream=None):
     """ls_distill_loss_backward: returns out, the gradient ([n, vocab] of the
     logits' type; out may be the logits themselves)."""
-    import torch
     lib = _lib()
-    ptr, dt, n, V, stride = _logits_desc(logits)
+    ptr, dt, n, V, stride = _matrix(logits)
     t = _teacher(teacher_ids, teacher_log_probs, n)
-    s, ctx = _on(stream)
+    s, ctx = _where(stream)
     with ctx:
         if out is None:
             out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
         out_stride = _like(out, logits, n, "out")
         st = lib.ls_distill_loss_backward(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
                                           _f32(weights, "weights", n), _f32(stats, "stats", DISTILL_STATS * n),
-                                          _f32(grad_loss, "grad_loss", n), out.data_ptr(), out_stride, s.cuda_stream)
+                                          _f32(grad_loss, "grad_loss", n), out.data_ptr(), out_stride, s)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss_backward")
     return out
@@ -305,11 +345,10 @@ def distill_loss_grad(logits, teacher_ids, teacher_log_probs, temperature=1.0, t
     """ls_distill_loss_grad: returns (loss float32 [n], gradient [n, vocab] of
     the logits' type) from one read of the logits; out_grad may be the logits
     themselves."""
-    import torch
     lib = _lib()
-    ptr, dt, n, V, stride = _logits_desc(logits)
+    ptr, dt, n, V, stride = _matrix(logits)
     t = _teacher(teacher_ids, teacher_log_probs, n)
-    s, ctx = _on(stream)
+    s, ctx = _where(stream)
     with ctx:
         if out_loss is None:
             out_loss = torch.empty(n, dtype=torch.float32, device=logits.device)
@@ -318,7 +357,7 @@ def distill_loss_grad(logits, teacher_ids, teacher_log_probs, temperature=1.0, t
         out_stride = _like(out_grad, logits, n, "out_grad")
         st = lib.ls_distill_loss_grad(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
                                       _f32(weights, "weights", n), _f32(out_loss, "out_loss", n),
-                                      out_grad.data_ptr(), out_stride, _i32(error_word, "error_word"), s.cuda_stream)
+                                      out_grad.data_ptr(), out_stride, _i32(error_word, "error_word"), s)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss_grad")
     return out_loss, out_grad
@@ -329,7 +368,7 @@ def distill(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="bucke
     the logits: distill_loss forward, distill_loss_backward backward."""
     global _Distill
     if _Distill is None:
-        import torch
+        _need_torch()
 
         class Distill(torch.autograd.Function):
             @staticmethod

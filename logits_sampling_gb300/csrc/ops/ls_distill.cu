@@ -2,20 +2,20 @@
 // its gradient (ls_distill_loss, ls_distill_loss_backward,
 // ls_distill_loss_grad).
 //
-// Loss, and loss with gradient (distill_kernel): the row lies in the shared
-// memory of a cluster (ls_slice.cuh) and is read from global memory once.  The
-// teacher's entries are taken out of it first (their logits go to every CTA,
-// their places become -inf), so the sums that follow run over the entries
-// outside them, and the mass outside (q_r) is a sum of its own rather than a
-// difference of two.  With R the row's entries outside the ids, of maximum
-// M_r, and e_j = exp((x_j - M_r) / T), the gradient outside the ids is one
-// multiple of e_j:
+// Loss, and loss with gradient (distill_kernel): a row over the CTAs of a
+// cluster (ls_stream.cuh).  A bitmap in shared memory marks the teacher's ids;
+// the running maximum and sum skip them, so that the mass outside them (q_r) is
+// a sum of its own rather than a difference of two.  With the entries outside
+// of maximum M_r and e_j = exp((x_j - M_r) / T), the gradient outside the ids
+// is one multiple of e_j:
 //     d_j = g / T * e_j * kappa,   kappa = A exp((M_r - M) / T) / S - p_r / S_r
 // and the at most 256 ids follow one by one: g / T * (alpha exp((x - M) / T) -
 // p), alpha = A / S.  M_r, kappa, M, alpha and the scale of p are the row's
 // `stats`: the backward pass (distill_backward_kernel) reads them and nothing
-// else of the forward pass, and is one sweep over the logits in tiles.
-#include "ls_slice.cuh"
+// else of the forward pass, and is one sweep over the logits in tiles.  In the
+// call that gives both, each CTA reads its run a second time for the gradient;
+// runs are short enough that what is in flight stays in L2.
+#include "ls_stream.cuh"
 
 namespace lsg {
 namespace ops {
@@ -45,87 +45,65 @@ struct DistillArgs {
 // A teacher's mass below this is none to renormalise (its reciprocal would overflow).
 constexpr float kLeastMass = 7.8886e-31f;  // 2^-100
 
-// Gradient of a unit outside the ids: coef * exp((x - m) / T).
+// Gradient of a unit outside the ids: coef * exp((x - m) / T), coef over
+// x.scale where x is fast.
 template <typename TIn>
-__device__ __forceinline__ uint4 unit_grad(uint4 w, const ExpAgainst& x, float coef_fast, float coef) {
+__device__ __forceinline__ void unit_grad(uint32_t (&w)[8], const ExpAgainst& x, float coef) {
   constexpr int kN = Unit<TIn>::kN;
-  w = Unit<TIn>::clean(w);
-  float d[kN];
-  if (x.fast) {
+  Unit<TIn>::clean(w);
+  uint32_t o[8];
 #pragma unroll
-    for (int q = 0; q < kN / 2; ++q)
-      unpack2(mul2(x.pair_fast(Unit<TIn>::pair(w, q)), pack2(coef_fast, coef_fast)), d[2 * q], d[2 * q + 1]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < kN / 2; ++q)
-      unpack2(mul2(x.pair_slow(Unit<TIn>::pair(w, q)), pack2(coef, coef)), d[2 * q], d[2 * q + 1]);
+  for (int q = 0; q < kN / 2; ++q) {
+    float a, b;
+    unpack2(mul2(x.fast ? x.pair_fast(Unit<TIn>::pair(w, q)) : x.pair_slow(Unit<TIn>::pair(w, q)), pack2(coef, coef)), a,
+            b);
+    Unit<TIn>::set_pair(o, q, a, b);
   }
-  return Unit<TIn>::make(d);
-}
-
-__device__ __forceinline__ void store_unit(void* p, uint4 v) {
-  asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-// Writes the slice's entries of an output row: unit by unit where the output
-// row starts at the input row's alignment, else entry by entry.  `unit(u)`
-// gives the 16 bytes that belong to the slice's unit u.
-template <typename TIn, typename F>
-__device__ __forceinline__ void write_slice(const Slice<TIn>& s, typename Elem<TIn>::Raw* out, F unit) {
-  using Raw = typename Elem<TIn>::Raw;
-  constexpr int kN = Unit<TIn>::kN;
-  const int f = s.full_first(), l = s.full_last();
-  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(s.row)) & 15u) == 0;
-  for (int u = threadIdx.x; u < s.n; u += kSliceThreads) {
-    const uint4 v = unit(u);
-    const int64_t j = s.index(u * kN);
-    if (same && u >= f && u < l) {
-      store_unit(out + j, v);
-    } else {
-      Raw e[kN];
-      memcpy(e, &v, 16);
 #pragma unroll
-      for (int q = 0; q < kN; ++q)
-        if (j + q >= 0 && j + q < s.V) out[j + q] = e[q];
-    }
-  }
+  for (int q = 0; q < 8; ++q) w[q] = o[q];
 }
 
-// Everything of a row but its entries: written by warp 0 of each CTA from the
-// same numbers, so every CTA holds the same bits.
-struct RowShared {
-  uint64_t bars[kChunks];
+struct DistillShared {
   float2 ms[kMaxCluster];  // each CTA's maximum and sum over the entries outside the ids
+  float2 red[kStreamWarps];
   float x[LS_MAX_TOP];     // the student's logits at the ids (-inf where there is none)
   float p[LS_MAX_TOP];
   float lp[LS_MAX_TOP];
-  float red[kSliceWarps];
   RowStats st;
 };
 
 template <typename TIn, bool kGrad>
-__global__ void __launch_bounds__(kSliceThreads, 3) distill_kernel(const DistillArgs a, int upc) {
+__global__ void __launch_bounds__(kStreamThreads, 2) distill_kernel(const DistillArgs a, int upc) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
-  extern __shared__ uint4 slice_smem[];
-  __shared__ RowShared sh;
+  constexpr int kN = Unit<TIn>::kN;
+  extern __shared__ uint4 dyn_smem[];
+  __shared__ DistillShared sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t i = blockIdx.x / (unsigned)C;
-  const float w = a.weights ? a.weights[i] : 1.f;
-  Slice<TIn> s;
-  s.init(slice_smem, a.logits, i, a.row_stride, a.vocab, upc, rank);
+  Run<TIn> run;
+  run.init(a.logits, i, a.row_stride, a.vocab, upc, rank);
   Raw* grad = kGrad ? static_cast<Raw*>(a.out_grad) + i * a.grad_stride : nullptr;
+  const float w = a.weights ? a.weights[i] : 1.f;
   if (w == 0.f) {  // every CTA of the row leaves here, before any cluster barrier
-    if (kGrad) write_slice<TIn>(s, grad, [](int) { return make_uint4(0u, 0u, 0u, 0u); });
+    if (kGrad) {
+      const bool same = run.aligned_with(grad);
+      uint32_t z[8] = {};
+      for (int u = tid; u < run.n; u += kStreamThreads) run.store(grad, same, u, z);
+    }
     if (tid == 0 && rank == 0) {
       a.out_loss[i] = 0.f;
       if (a.out_stats) a.out_stats[i] = RowStats{0.f, 0.f, 0.f, 0.f, 1.f, {}};
     }
     return;
   }
-  s.start(sh.bars);
+  typename Run<TIn>::Stage first;
+  run.template prefetch<kGrad>(tid, first);
   if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
+  // one bit per place of the run
+  uint32_t* bits = reinterpret_cast<uint32_t*>(dyn_smem);
+  for (int q = tid; q < (run.n * kN + 127) / 128; q += kStreamThreads) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
   // the teacher's entry of this thread
   int id = -1;
   float x = kNegInf, p = 0.f;
@@ -135,46 +113,47 @@ __global__ void __launch_bounds__(kSliceThreads, 3) distill_kernel(const Distill
       id = a.t.ids[i * a.t.stride + tid];
       t = a.t.log_probs[i * a.t.stride + tid];
       if (id < 0 || (int64_t)id >= a.vocab || !(t > kNegInf)) id = -1;
-      if (id >= 0) p = expf(t);
+      if (id >= 0) {
+        p = expf(t);
+        x = guard(E::get(run.row[id]));
+      }
     }
     sh.lp[tid] = t;
     sh.p[tid] = p;
-    if (id < 0) sh.x[tid] = kNegInf;
+    sh.x[tid] = x;
   }
-  bool stalled = false;
-  for (int k = 0; k < kChunks; ++k)
-    if (!mbar_wait(&sh.bars[k])) stalled = true;
   __syncthreads();
-  if (C > 1) cluster_wait();
-  const int mine = id >= 0 ? s.entry(id) : -1;
-  if (mine >= 0) {
-    x = guard(E::get(s.raw()[mine]));
-    if (C > 1) {
-      for (int q = 0; q < C; ++q) peer_store(peer_addr(smem_addr(&sh.x[tid]), q), x);
-    } else {
-      sh.x[tid] = x;
-    }
-    s.raw()[mine] = E::neg_inf();
-  }
+  const int mine = id >= 0 ? run.place(id) : -1;
+  if (mine >= 0) atomicOr(&bits[mine >> 5], 1u << (mine & 31));
   __syncthreads();
   const float c = kLog2e / a.temperature;
-  const float m = block_max(slice_max(s, sh.bars, &stalled), sh.red);
-  ExpAgainst against;
-  against.init(m, c);
-  const float sum = block_sum(slice_sum(s, against), sh.red);
-  if (tid < C) {
-    if (C > 1)
-      peer_store2(peer_addr(smem_addr(&sh.ms[rank]), tid), m, sum);
-    else
-      sh.ms[0] = make_float2(m, sum);
-  }
+  OnlineSum acc;
+  acc.init(c);
+  run.template stream<kGrad>(first, [&](int u, typename Run<TIn>::Stage& v) {
+    float um = kNegInf;
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      const int uk = min(u + k * kStreamThreads, run.n - 1);
+      const uint32_t listed = kN == 16 ? reinterpret_cast<const uint16_t*>(bits)[uk] : reinterpret_cast<const uint8_t*>(bits)[uk];
+      if (listed) Unit<TIn>::drop(v[k], listed);
+      Unit<TIn>::clean(v[k]);
+      um = fmaxf(um, Unit<TIn>::max(v[k]));
+    }
+    acc.raise(um);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) acc.template add<TIn>(v[k]);
+  });
+  const float2 mine_ms = block_lse(acc.x.m, acc.sum(), c, sh.red);
   if (C > 1) {
+    cluster_wait();
+    if (tid < C) peer_store2(peer_addr(smem_addr(&sh.ms[rank]), tid), mine_ms.x, mine_ms.y);
     cluster_arrive();
     cluster_wait();
-  } else {
-    __syncthreads();
+  } else if (tid == 0) {
+    sh.ms[0] = mine_ms;
   }
-  if (tid < 32) {
+  if (tid < 32) {  // the row's scalars, in each CTA from the same numbers
+    __syncwarp();
     constexpr int kPer = LS_MAX_TOP / 32;
     const float2 ms = lane < C ? sh.ms[lane] : make_float2(kNegInf, 0.f);
     const float Mr = warp_max(ms.x);
@@ -209,7 +188,6 @@ __global__ void __launch_bounds__(kSliceThreads, 3) distill_kernel(const Distill
     if (Mr > kNegInf) st.kappa = st.alpha * rest - (pr > 0.f ? pr / Sr : 0.f);
     if (M == kNegInf) st.alpha = st.kappa = quiet_nan();
     if (lane == 0) sh.st = st;
-    __syncwarp();
     if (rank == 0) {
       const float lnS = logf(S), lnP = a.tail == LS_TAIL_RENORM ? logf(P) : 0.f;
       float kl = 0.f;
@@ -228,98 +206,95 @@ __global__ void __launch_bounds__(kSliceThreads, 3) distill_kernel(const Distill
       }
     }
   }
-  if (stalled && a.error_word) atomicOr(a.error_word, LS_ROW_ERR_STALLED);
   if (kGrad) {
+    run.template prefetch<true>(tid, first);
     __syncthreads();
     const RowStats st = sh.st;
     const float g = w / a.temperature;
+    ExpAgainst against;
     against.init(st.Mr, c);
-    const float coef = g * st.kappa;
-    write_slice<TIn>(s, grad, [&](int u) { return unit_grad<TIn>(s.buf[u], against, coef * against.scale, coef); });
+    const float coef = g * st.kappa * against.scale;
+    const bool same = run.aligned_with(grad);
+    run.template stream<true>(first, [&](int u, typename Run<TIn>::Stage& v) {
+#pragma unroll
+      for (int k = 0; k < kStage; ++k) {
+        const int uk = u + k * kStreamThreads;
+        if (uk < run.n) {
+          unit_grad<TIn>(v[k], against, coef);
+          run.store(grad, same, uk, v[k]);
+        }
+      }
+    });
     __syncthreads();
     if (mine >= 0) grad[id] = E::put(g * (st.alpha * rel_exp(x, st.M, c) - p * st.scale));
   }
 }
 
-// The backward pass alone: a tile of kBackUnits units per thread, loaded to
-// registers before anything is written (the gradient may replace the logits).
+// The backward pass alone: kBackUnits units per thread, loaded to registers
+// before anything is written (the gradient may replace the logits).
 constexpr int kBackThreads = 256;
-constexpr int kBackUnits = 4;
+constexpr int kBackUnits = 2;
 
 template <typename TIn>
 __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const DistillArgs a, int tiles) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
-  constexpr int kN = Unit<TIn>::kN;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)tiles;
-  const int tile = (int)(blockIdx.x % (unsigned)tiles);
+  Run<TIn> run;
+  run.init(a.logits, i, a.row_stride, a.vocab, kBackThreads * kBackUnits, (int)(blockIdx.x % (unsigned)tiles));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
   const float g = (a.weights ? a.weights[i] : 1.f) * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
-  Slice<TIn> s;  // of this tile, left in global memory
-  s.init(nullptr, a.logits, i, a.row_stride, a.vocab, kBackThreads * kBackUnits, tile);
-  const int f = s.full_first(), l = s.full_last();
+  const bool same = run.aligned_with(grad);
+  if (g == 0.f) {
+    uint32_t z[8] = {};
+    for (int u = tid; u < run.n; u += kBackThreads) run.store(grad, same, u, z);
+    return;
+  }
+  uint32_t v[kBackUnits][8];
+#pragma unroll
+  for (int k = 0; k < kBackUnits; ++k)
+    if (tid + k * kBackThreads < run.n) run.template load<true>(tid + k * kBackThreads, v[k]);
   const RowStats st = a.stats_in[i];
   const float c = kLog2e / a.temperature;
-  uint4 v[kBackUnits];
-  if (g != 0.f) {
-#pragma unroll
-    for (int k = 0; k < kBackUnits; ++k) {
-      const int u = tid + k * kBackThreads;
-      const int64_t j = s.index(u * kN);
-      if (u >= f && u < l) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
-                     : "l"(s.row + j));
-      } else if (u < s.n) {
-        Raw e[kN];
-#pragma unroll
-        for (int q = 0; q < kN; ++q) e[q] = j + q >= 0 && j + q < s.V ? s.row[j + q] : E::neg_inf();
-        memcpy(&v[k], e, 16);
-      }
-    }
-  }
   int id = -1;
   float x = kNegInf, p = 0.f;
-  if (tid < a.t.k && g != 0.f) {
+  if (tid < a.t.k) {
     id = a.t.ids[i * a.t.stride + tid];
     const float t = a.t.log_probs[i * a.t.stride + tid];
-    if (id < 0 || (int64_t)id >= a.vocab || !(t > kNegInf) || s.entry(id) < 0) id = -1;
+    if (id < 0 || (int64_t)id >= a.vocab || !(t > kNegInf) || run.place(id) < 0) id = -1;
     if (id >= 0) {
       p = expf(t) * st.scale;
-      x = guard(E::get(s.row[id]));
+      x = guard(E::get(run.row[id]));
     }
   }
+  const float top = g * (st.alpha * rel_exp(x, st.M, c) - p);
   ExpAgainst against;
   against.init(st.Mr, c);
-  const float coef = g * st.kappa;
-  const bool same = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(s.row)) & 15u) == 0;
+  const float coef = g * st.kappa * against.scale;
   __syncthreads();  // every load of the tile is done
 #pragma unroll
-  for (int k = 0; k < kBackUnits; ++k) {
-    const int u = tid + k * kBackThreads;
-    if (u >= s.n) break;
-    const uint4 d = g == 0.f ? make_uint4(0u, 0u, 0u, 0u) : unit_grad<TIn>(v[k], against, coef * against.scale, coef);
-    const int64_t j = s.index(u * kN);
-    if (same && u >= f && u < l) {
-      store_unit(grad + j, d);
-    } else {
-      Raw e[kN];
-      memcpy(e, &d, 16);
-#pragma unroll
-      for (int q = 0; q < kN; ++q)
-        if (j + q >= 0 && j + q < s.V) grad[j + q] = e[q];
+  for (int k = 0; k < kBackUnits; ++k)
+    if (tid + k * kBackThreads < run.n) {
+      unit_grad<TIn>(v[k], against, coef);
+      run.store(grad, same, tid + k * kBackThreads, v[k]);
     }
-  }
   __syncthreads();
-  if (id >= 0) grad[id] = E::put(g * (st.alpha * rel_exp(x, st.M, c) - p));
+  if (id >= 0) grad[id] = E::put(top);
 }
+
+// Bytes of a CTA's run in the call that reads it twice: two CTAs on each of 152
+// SMs then have at most 38 MB of logits in flight, and as much of gradient, in
+// a 129 MB L2.
+constexpr int64_t kRunTwice = 128 * 1024;
+constexpr int64_t kRunOnce = 1024 * 1024;
 
 template <typename TIn, bool kGrad>
 static ls_status launch(const DistillArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
-  const SlicePlan plan = plan_slices(n, a.vocab, dtype);
-  return launch_slices(distill_kernel<TIn, kGrad>, a, plan, plan.smem, n, st, done);
+  const StreamPlan plan = plan_stream(n, a.vocab, dtype, kGrad ? kRunTwice : kRunOnce);
+  const size_t smem = ((size_t)plan.upc * Unit<TIn>::kN + 127) / 128 * 16;
+  return launch_rows(distill_kernel<TIn, kGrad>, a, plan, smem, n, st, done);
 }
 
 template <bool kGrad>
@@ -330,9 +305,7 @@ static ls_status dispatch(const DistillArgs& a, ls_dtype dtype, int32_t n, void*
 
 static ls_status dispatch_backward(const DistillArgs& a, ls_dtype dtype, int32_t n, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t e = dtype == LS_DTYPE_F32 ? 4 : 2;
-  const int64_t units = (a.vocab * e + 15 - e) / 16 + 1;
-  const int64_t tiles = (units + kBackThreads * kBackUnits - 1) / (kBackThreads * kBackUnits);
+  const int64_t tiles = (row_units(a.vocab, dtype) + kBackThreads * kBackUnits - 1) / (kBackThreads * kBackUnits);
   if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)(tiles * n)), block(kBackThreads);
   if (dtype == LS_DTYPE_BF16)

@@ -59,9 +59,8 @@ static int device_attr() {
   return v;
 }
 
-// Largest vocab of the calls that hold a whole row in shared memory: sixteen
-// slices of at most 160 KB.
-static inline int64_t max_row(ls_dtype dtype) { return 16 * (int64_t)(160 * 1024) / (dtype == LS_DTYPE_F32 ? 4 : 2); }
+// Largest vocab of the calls that keep a few bits per entry in shared memory.
+static inline int64_t max_row(ls_dtype) { return int64_t(1) << 22; }
 
 static inline bool matrix_ok(const void* p, ls_dtype dtype, int64_t vocab, int64_t row_stride) {
   if (!p || (dtype != LS_DTYPE_F32 && dtype != LS_DTYPE_BF16)) return false;

@@ -1,0 +1,392 @@
+// ls_stream.cuh -- a logits row streamed through registers, split over the
+// CTAs of a cluster where one CTA would be too slow or its share too large.
+//
+// The row is seen as 32-byte units aligned in global memory (16 bf16 or 8 fp32
+// entries).  CTA q of C owns a contiguous run of units; its threads take them
+// in turn, kStage at a time, with the next stage's loads in flight while one
+// is computed.  The units that lie wholly in the row are one 256-bit load, the
+// row's first and last partial unit are read entry by entry, with -inf in the
+// places outside the row.
+#pragma once
+
+#include "ls_row_ops.cuh"
+
+namespace lsg {
+namespace ops {
+
+constexpr int kStreamThreads = 512;
+constexpr int kStreamWarps = kStreamThreads / 32;
+constexpr int kStage = 2;  // units of a thread per stage
+constexpr int kMaxCluster = 8;
+
+// ---------------------------------------------------------------------------
+// Cluster primitives
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
+  uint32_t d;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store2(uint32_t a, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void peer_store(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t peer_add(uint32_t a, uint32_t v) {
+  uint32_t o;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(o) : "r"(a), "r"(v) : "memory");
+  return o;
+}
+
+// ---------------------------------------------------------------------------
+// 32-byte units by type
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+// The same as an ordinary load, for memory that the kernel itself writes later
+// (a gradient over its logits).
+__device__ __forceinline__ void load32_plain(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+template <typename TIn>
+struct Unit;
+
+template <>
+struct Unit<bf16_tag> {
+  static constexpr int kN = 16;
+  // The unit with its NaNs read as -inf (max with -inf drops a NaN).
+  __device__ __forceinline__ static void clean(uint32_t (&w)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = bmax2(w[q], 0xFF80FF80u);
+  }
+  // Maximum of a clean unit.
+  __device__ __forceinline__ static float max(const uint32_t (&w)[8]) {
+    const uint32_t m = bmax2(bmax2(bmax2(w[0], w[1]), bmax2(w[2], w[3])), bmax2(bmax2(w[4], w[5]), bmax2(w[6], w[7])));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ static f32x2 pair(const uint32_t (&w)[8], int q) {
+    return pack2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ static void set_pair(uint32_t (&w)[8], int q, float lo, float hi) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[q]) : "f"(hi), "f"(lo));
+  }
+  // -inf in the entries whose bit is set.
+  __device__ __forceinline__ static void drop(uint32_t (&w)[8], uint32_t bits) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (bits & (1u << (2 * q))) w[q] = (w[q] & 0xFFFF0000u) | 0xFF80u;
+      if (bits & (2u << (2 * q))) w[q] = (w[q] & 0xFFFFu) | 0xFF800000u;
+    }
+  }
+};
+
+template <>
+struct Unit<float> {
+  static constexpr int kN = 8;
+  __device__ __forceinline__ static void clean(uint32_t (&w)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(fmaxf(__uint_as_float(w[q]), kNegInf));
+  }
+  __device__ __forceinline__ static float max(const uint32_t (&w)[8]) {
+    return fmax3(fmax3(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2])),
+                 fmax3(__uint_as_float(w[3]), __uint_as_float(w[4]), __uint_as_float(w[5])),
+                 fmaxf(__uint_as_float(w[6]), __uint_as_float(w[7])));
+  }
+  __device__ __forceinline__ static f32x2 pair(const uint32_t (&w)[8], int q) {
+    return pack2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+  }
+  __device__ __forceinline__ static void set_pair(uint32_t (&w)[8], int q, float lo, float hi) {
+    w[2 * q] = __float_as_uint(lo);
+    w[2 * q + 1] = __float_as_uint(hi);
+  }
+  __device__ __forceinline__ static void drop(uint32_t (&w)[8], uint32_t bits) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (bits & (1u << q)) w[q] = 0xFF800000u;
+  }
+};
+
+// exp((v - M) / T), c = log2(e) / T, for v <= M; entries at an infinite
+// maximum share it.
+__device__ __forceinline__ float rel_exp(float v, float M, float c) { return v == M ? 1.f : ex2((v - M) * c); }
+
+// exp((v - m) / T) for many v against one m.  fma(v, c, -r) with r = RN(m c)
+// is one instruction for two entries and exact up to its last rounding; the
+// common factor 2^(m c - r) that r's rounding leaves is known (`scale` takes
+// it out).  For |m c| of 2^16 and above that factor would matter, and for an
+// infinite m the difference is undefined: there each entry is subtracted first.
+struct ExpAgainst {
+  float m, c, r, scale;
+  bool fast;
+  __device__ __forceinline__ void init(float m_, float c_) {
+    m = m_;
+    c = c_;
+    r = m * c;
+    fast = fabsf(r) < 65536.f;
+    scale = fast ? ex2(-fmaf(m, c, -r)) : 1.f;
+  }
+  // The exponentials of a pair over `scale`.
+  __device__ __forceinline__ f32x2 pair_fast(f32x2 v) const {
+    float a, b;
+    unpack2(fma2(v, pack2(c, c), pack2(-r, -r)), a, b);
+    return pack2(ex2(a), ex2(b));
+  }
+  __device__ __forceinline__ f32x2 pair_slow(f32x2 v) const {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(rel_exp(a, m, c), rel_exp(b, m, c));
+  }
+};
+
+// A thread's running maximum and sum of exp((v - m) / T).
+struct OnlineSum {
+  ExpAgainst x;
+  f32x2 s0, s1;
+  __device__ __forceinline__ void init(float c) {
+    x.init(kNegInf, c);
+    s0 = s1 = 0ull;
+  }
+  // Takes units of maximum at most um.
+  __device__ __forceinline__ void raise(float um) {
+    if (um > x.m) {
+      const float f = x.m > kNegInf ? x.scale * rel_exp(x.m, um, x.c) : 0.f;
+      x.init(um, x.c);
+      const float g = f / x.scale;
+      s0 = mul2(s0, pack2(g, g));
+      s1 = mul2(s1, pack2(g, g));
+    }
+  }
+  template <typename TIn>
+  __device__ __forceinline__ void add(const uint32_t (&w)[8]) {
+    if (x.fast) {
+#pragma unroll
+      for (int q = 0; q < Unit<TIn>::kN / 2; q += 2) {
+        s0 = add2(s0, x.pair_fast(Unit<TIn>::pair(w, q)));
+        s1 = add2(s1, x.pair_fast(Unit<TIn>::pair(w, q + 1)));
+      }
+    } else if (x.m > kNegInf) {
+#pragma unroll
+      for (int q = 0; q < Unit<TIn>::kN / 2; ++q) s0 = add2(s0, x.pair_slow(Unit<TIn>::pair(w, q)));
+    }
+  }
+  __device__ __forceinline__ float sum() const {
+    float a, b;
+    unpack2(add2(s0, s1), a, b);
+    return (a + b) * x.scale;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// One CTA's run of a row's units
+// ---------------------------------------------------------------------------
+template <typename TIn>
+struct Run {
+  using E = Elem<TIn>;
+  using Raw = typename E::Raw;
+  static constexpr int kN = Unit<TIn>::kN;
+  const Raw* row;
+  const char* base;  // unit 0 of the run
+  int64_t V;
+  int64_t j0;        // vocabulary index of the run's first place (negative in the row's first unit)
+  int n;             // units
+  int f, l;          // units [f, l) lie wholly in the row
+
+  __device__ __forceinline__ void init(const void* matrix, int64_t src, int64_t stride, int64_t vocab, int upc, int rank) {
+    row = static_cast<const Raw*>(matrix) + src * stride;
+    V = vocab;
+    const int off = (int)((reinterpret_cast<uintptr_t>(row) & 31u) / E::kBytes);
+    const int units = (int)((off + V + kN - 1) / kN), u0 = rank * upc;
+    j0 = (int64_t)u0 * kN - off;
+    base = reinterpret_cast<const char*>(row) + j0 * E::kBytes;
+    n = max(min(upc, units - u0), 0);
+    f = u0 == 0 && off > 0 ? 1 : 0;
+    l = min(n, (int)((off + V) / kN) - u0);
+  }
+  __device__ __forceinline__ int64_t index(int u) const { return j0 + (int64_t)u * kN; }
+  __device__ __forceinline__ bool full(int u) const { return u >= f && u < l; }
+  // Place of a vocabulary index in the run, -1 when another CTA holds it.
+  __device__ __forceinline__ int place(int64_t j) const {
+    const int64_t e = j - j0;
+    return e >= 0 && e < (int64_t)n * kN ? (int)e : -1;
+  }
+  // A unit's words (u < n); kPlain: see load32_plain.
+  template <bool kPlain = false>
+  __device__ __forceinline__ void load(int u, uint32_t (&w)[8]) const {
+    if (full(u)) {
+      if (kPlain)
+        load32_plain(base + (int64_t)u * 32, w);
+      else
+        load32(base + (int64_t)u * 32, w);
+    } else {
+      Raw e[kN];
+      const int64_t j = index(u);
+#pragma unroll
+      for (int q = 0; q < kN; ++q) e[q] = j + q >= 0 && j + q < V ? row[j + q] : E::neg_inf();
+      memcpy(w, e, 32);
+    }
+  }
+  // Writes unit u of an output row with this row's indices (`same`: and its alignment).
+  __device__ __forceinline__ void store(Raw* out, bool same, int u, const uint32_t (&w)[8]) const {
+    const int64_t j = index(u);
+    if (same && full(u)) {
+      store32(out + j, w);
+    } else {
+      Raw e[kN];
+      memcpy(e, w, 32);
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        if (j + q >= 0 && j + q < V) out[j + q] = e[q];
+    }
+  }
+  __device__ __forceinline__ bool aligned_with(const Raw* out) const {
+    return ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 31u) == 0;
+  }
+  // Visits this thread's units in order, kStage at a time: visit(u, w) with the
+  // words of units u and u + kStreamThreads (units past n as -inf).  `first`
+  // has been loaded by prefetch().
+  typedef uint32_t Stage[kStage][8];
+  template <bool kPlain = false>
+  __device__ __forceinline__ void prefetch(int u, Stage& w) const {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      const int uk = u + k * kStreamThreads;
+      if (uk < n) {
+        load<kPlain>(uk, w[k]);
+      } else {
+        const uint32_t none = E::kBytes == 2 ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[k][q] = none;
+      }
+    }
+  }
+  template <bool kPlain = false, typename F>
+  __device__ __forceinline__ void stream(Stage& first, F visit) const {
+    for (int u = threadIdx.x; u < n; u += 2 * kStage * kStreamThreads) {
+      Stage next;
+      const int u1 = u + kStage * kStreamThreads;
+      prefetch<kPlain>(u1, next);
+      visit(u, first);
+      prefetch<kPlain>(u1 + kStage * kStreamThreads, first);
+      if (u1 < n) visit(u1, next);
+    }
+  }
+};
+
+// Block-wide maximum, and sum, of one value per thread (all threads call;
+// `red` holds kStreamWarps floats; the sum's order is fixed).
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = warp_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_max(red[threadIdx.x & (kStreamWarps - 1)]);
+}
+// (maximum, sum) of the block from each thread's, in every thread.
+__device__ __forceinline__ float2 block_lse(float m, float s, float c, float2* red) {
+  const float wm = warp_max(m);
+  const float ws = warp_reduce(m > kNegInf ? s * rel_exp(m, wm, c) : 0.f, OpAddF());
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(wm, ws);
+  __syncthreads();
+  const float2 r = red[threadIdx.x & (kStreamWarps - 1)];
+  const float bm = warp_max(r.x);
+  float bs = r.x > kNegInf ? r.y * rel_exp(r.x, bm, c) : 0.f;
+#pragma unroll
+  for (int o = kStreamWarps / 2; o > 0; o >>= 1) bs += __shfl_xor_sync(0xFFFFFFFFu, bs, o);
+  return make_float2(bm, bs);
+}
+
+// ---------------------------------------------------------------------------
+// Host: cluster size and launch
+// ---------------------------------------------------------------------------
+struct StreamPlan {
+  int ctas;  // per row
+  int upc;   // units per CTA
+};
+
+static inline int64_t row_units(int64_t vocab, ls_dtype dtype) {  // at the worst alignment
+  const int64_t e = dtype == LS_DTYPE_F32 ? 4 : 2;
+  return (vocab * e + 31 - e) / 32 + 1;
+}
+
+// The fewest CTAs per row that keep a CTA's run within `most` bytes and, while
+// runs stay above kRunLeast bytes, give each SM kRowsPerSm CTAs' worth of work.
+constexpr int64_t kRunLeast = 16 * 1024;
+constexpr int kCtasPerSm = 4;
+
+static inline StreamPlan plan_stream(int32_t n, int64_t vocab, ls_dtype dtype, int64_t most) {
+  const int64_t units = row_units(vocab, dtype), sms = device_attr<cudaDevAttrMultiProcessorCount>();
+  int c = 1;
+  while (c < kMaxCluster && (units + c - 1) / c * 32 > most) c *= 2;
+  while (c < kMaxCluster && (int64_t)n * c < kCtasPerSm * sms && units * 32 / (2 * c) >= kRunLeast) c *= 2;
+  return StreamPlan{c, (int)((units + c - 1) / c)};
+}
+
+// Lets a kernel use the device's whole shared memory per CTA (once per device; `done` belongs to the kernel).
+template <typename Kernel>
+static bool open_limits(Kernel kernel, std::atomic<int>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return true;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return false;
+  const int most = device_attr<cudaDevAttrMaxSharedMemoryPerBlockOptin>() - (int)fa.sharedSizeBytes;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+    return false;
+  if (dev >= 0 && dev < kMaxDevices) done[dev].store(1, std::memory_order_relaxed);
+  return true;
+}
+
+// Launches one cluster of p.ctas CTAs per row.
+template <typename Kernel, typename Args>
+static ls_status launch_rows(Kernel kernel, const Args& a, const StreamPlan& p, size_t smem, int32_t n,
+                               cudaStream_t stream, std::atomic<int>* done) {
+  if ((int64_t)n * p.ctas > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  if (!open_limits(kernel, done)) return LS_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)n * p.ctas));
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, a, p.upc) != cudaSuccess) return LS_ERR_CUDA;
+  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+}
+
+}  // namespace ops
+}  // namespace lsg

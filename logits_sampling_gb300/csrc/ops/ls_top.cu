@@ -1,27 +1,29 @@
 // ls_top.cu -- the k best entries of each logits row, their log-probs and the
 // row's log-sum-exp (ls_top_log_probs).
 //
-// The row lies in the shared memory of a cluster (ls_slice.cuh), read from
-// global memory once.  Per row:
-//  1. Each thread's maximum and the CTA's sum of exponentials.  In each of the w
-//     warps that hold entries, the ceil(k / w)-th largest lane maximum: at least
-//     k entries of the slice are at or above the least of these, so that is a
-//     lower bound of the k-th largest entry, and the largest such bound over
-//     the cluster's CTAs is one too.
-//  2. (max, sum, bound) are exchanged over the cluster; each CTA collects its
-//     entries at or above the bound as 64-bit keys (value, then lower index).
-//     More than kLocal of them -- ties in the main: constant rows, rows masked
-//     with one low value -- are cut to the slice's own k best (select_ties).
-//  3. The keys go to the first CTA's shared memory (over its slice, which every
-//     CTA is done with), which ranks them and writes the k best.
-#include "ls_slice.cuh"
+// A row over the CTAs of a cluster (ls_stream.cuh).  Per row:
+//  1. One pass: each thread's running maximum and sum of exponentials, and in
+//     shared memory the maximum of each stage (kStage units of a thread).
+//  2. In each of the w warps that hold units, the ceil(k / w)-th largest lane
+//     maximum: at least k entries of the run are at or above the least of
+//     these, so that is a lower bound of the k-th largest entry, and the
+//     largest such bound over the cluster's CTAs is one too.  (max, sum,
+//     bound) are exchanged over the cluster.
+//  3. The stages whose maximum reaches the bound are read again (from L2) and
+//     their entries at or above it collected as 64-bit keys (value, then lower
+//     index).  More than kLocal of them -- ties in the main: constant rows,
+//     rows masked with one low value -- are cut to the run's own k best
+//     (select_ties).
+//  4. The keys go to the first CTA's shared memory (over its stage maxima, which
+//     every CTA is done with), which ranks them and writes the k best.
+#include "ls_stream.cuh"
 
 namespace lsg {
 namespace ops {
 
 constexpr int kLocal = 512;      // keys that a CTA sends at most
 constexpr int kRankMost = 384;   // keys placed by counting; more are sorted
-static_assert(kLocal >= LS_MAX_TOP, "a slice's own k best must fit");
+static_assert(kLocal >= LS_MAX_TOP, "a run's own k best must fit");
 
 struct TopArgs {
   const void* logits;
@@ -36,11 +38,11 @@ struct TopArgs {
 };
 
 struct TopShared {
-  uint64_t bars[kChunks];
   float2 ms[kMaxCluster];
+  float2 red[kStreamWarps];
   float bound[kMaxCluster];
-  float red[kSliceWarps];
-  int warp_n[kSliceWarps];
+  float redf[kStreamWarps];
+  int warp_n[kStreamWarps];
   unsigned int total;  // keys sent to this CTA
   int count;           // keys of this CTA
   int base;            // their place among those sent
@@ -53,78 +55,79 @@ __device__ __forceinline__ int block_count(int v, int* red) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  return __reduce_add_sync(0xFFFFFFFFu, (threadIdx.x & 31) < kSliceWarps ? red[threadIdx.x & 31] : 0);
+  return __reduce_add_sync(0xFFFFFFFFu, (threadIdx.x & 31) < kStreamWarps ? red[threadIdx.x & 31] : 0);
 }
 
-// The slice's entries of a predicate on (key, index), counted.
+// Visits the run's entries whose stage maximum is at least `least`: f(value, place in the run).
 template <typename TIn, typename F>
-__device__ __forceinline__ int count_entries(const Slice<TIn>& s, int* red, F test) {
+__device__ __forceinline__ void visit_stages(const Run<TIn>& run, const float* stage_max, float least, F f) {
   constexpr int kN = Unit<TIn>::kN;
-  int n = 0;
-  for (int u = threadIdx.x; u < s.n; u += kSliceThreads) {
-    const uint4 w = Unit<TIn>::clean(s.buf[u]);
+  for (int b = threadIdx.x, u = threadIdx.x; u < run.n; b += kStreamThreads, u += kStage * kStreamThreads) {
+    if (!(stage_max[b] >= least)) continue;
+    typename Run<TIn>::Stage w;
+    run.prefetch(u, w);
 #pragma unroll
-    for (int q = 0; q < kN / 2; ++q) {
-      float a, b;
-      unpack2(Unit<TIn>::pair(w, q), a, b);
-      n += (test(f32_key(a)) ? 1 : 0) + (test(f32_key(b)) ? 1 : 0);
+    for (int k = 0; k < kStage; ++k) {
+#pragma unroll
+      for (int q = 0; q < kN / 2; ++q) {
+        float x, y;
+        unpack2(Unit<TIn>::pair(w[k], q), x, y);
+        f(x, (u + k * kStreamThreads) * kN + 2 * q);
+        f(y, (u + k * kStreamThreads) * kN + 2 * q + 1);
+      }
     }
   }
-  return block_count(n, red);
 }
 
-// The slice's k best exactly, for any number of ties: `bound` has at least k
+// The run's k best exactly, for any number of ties: `bound` has at least k
 // entries at or above it.  If fewer than k lie above it, it is the k-th largest
 // value; else that is found by bisection of the keys above it.  Entries above
 // the cut all belong to the answer, and of those equal to it the lowest
-// indices, taken in order of the slice.
+// indices, taken in order of the run.
 template <typename TIn>
-__device__ void select_ties(const Slice<TIn>& s, int k, float bound, TopShared& sh) {
+__device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage_max, int k, float bound, TopShared& sh) {
   constexpr int kN = Unit<TIn>::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t low = f32_key(kNegInf);
-  uint32_t cut = max(f32_key(bound), low + 1u);  // -inf is never listed
-  uint32_t hi = 0xFFFFFFFFu;                     // fewer than k keys are above hi
-  if (count_entries(s, sh.warp_n, [&](uint32_t key) { return key > cut; }) >= k) {
-    uint32_t lo = cut;  // at least k keys are above lo
+  auto above = [&](uint32_t key) {  // entries whose key is above `key`
+    int n = 0;
+    visit_stages<TIn>(run, stage_max, f32_from_key(key), [&](float v, int) { n += guard(v) == v && f32_key(v) > key; });
+    return block_count(n, sh.warp_n);
+  };
+  uint32_t cut = max(f32_key(bound), f32_key(kNegInf) + 1u);  // -inf is never listed
+  if (above(cut) >= k) {
+    uint32_t lo = cut, hi = f32_key(kPosInf);  // at least k keys are above lo, fewer than k above hi
     while (hi - lo > 1u) {
       const uint32_t mid = lo + (hi - lo) / 2u;
-      if (count_entries(s, sh.warp_n, [&](uint32_t key) { return key > mid; }) >= k)
+      if (above(mid) >= k)
         lo = mid;
       else
         hi = mid;
     }
     cut = hi;
   }
+  const float cut_value = f32_from_key(cut);
   __syncthreads();
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  for (int u = tid; u < s.n; u += kSliceThreads) {
-    const uint4 w = Unit<TIn>::clean(s.buf[u]);
-#pragma unroll
-    for (int q = 0; q < kN / 2; ++q) {
-      float v[2];
-      unpack2(Unit<TIn>::pair(w, q), v[0], v[1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (f32_key(v[e]) > cut) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kLocal) sh.keys[at] = argmax_key(v[e], s.index(u * kN + 2 * q + e));
-        }
+  visit_stages<TIn>(run, stage_max, cut_value, [&](float v, int place) {
+    if (v > cut_value) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kLocal) sh.keys[at] = argmax_key(v, run.j0 + place);
     }
-  }
+  });
   __syncthreads();
   int have = sh.count;  // fewer than k
-  for (int u0 = 0; u0 < s.n && have < k; u0 += kSliceThreads) {
+  for (int u0 = 0; u0 < run.n && have < k; u0 += kStreamThreads) {
     const int u = u0 + tid;
     float v[kN];
     int n = 0;
-    if (u < s.n) {
-      const uint4 w = Unit<TIn>::clean(s.buf[u]);
+    if (u < run.n) {
+      uint32_t w[8];
+      run.load(u, w);
 #pragma unroll
       for (int q = 0; q < kN / 2; ++q) unpack2(Unit<TIn>::pair(w, q), v[2 * q], v[2 * q + 1]);
 #pragma unroll
-      for (int e = 0; e < kN; ++e) n += f32_key(v[e]) == cut;
+      for (int e = 0; e < kN; ++e) n += v[e] == cut_value;
     }
     int before = n;  // ties up to and with this lane
 #pragma unroll
@@ -137,15 +140,15 @@ __device__ void select_ties(const Slice<TIn>& s, int k, float bound, TopShared& 
     __syncthreads();
     int at = have + before - n, all = 0;
 #pragma unroll
-    for (int q = 0; q < kSliceWarps; ++q) {
+    for (int q = 0; q < kStreamWarps; ++q) {
       if (q < warp) at += sh.warp_n[q];
       all += sh.warp_n[q];
     }
     if (n > 0) {
 #pragma unroll
       for (int e = 0; e < kN; ++e)
-        if (f32_key(v[e]) == cut) {
-          if (at < k) sh.keys[at] = argmax_key(v[e], s.index(u * kN + e));
+        if (v[e] == cut_value) {
+          if (at < k) sh.keys[at] = argmax_key(v[e], run.index(u) + e);
           ++at;
         }
     }
@@ -157,11 +160,11 @@ __device__ void select_ties(const Slice<TIn>& s, int k, float bound, TopShared& 
 }
 
 // Descending sort of n keys in shared memory (n a power of two).
-__device__ void sort_keys(unsigned long long* keys, int n) {
+__device__ __noinline__ void sort_keys(unsigned long long* keys, int n) {
   for (int size = 2; size <= n; size <<= 1)
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
       __syncthreads();
-      for (int t = threadIdx.x; t < n / 2; t += kSliceThreads) {
+      for (int t = threadIdx.x; t < n / 2; t += kStreamThreads) {
         const int a = 2 * t - (t & (stride - 1)), b = a + stride;
         const unsigned long long x = keys[a], y = keys[b];
         if ((x < y) == ((a & size) == 0)) {
@@ -174,10 +177,10 @@ __device__ void sort_keys(unsigned long long* keys, int n) {
 }
 
 template <typename TIn>
-__global__ void __launch_bounds__(kSliceThreads, 3) top_kernel(const TopArgs a, int upc) {
-  constexpr int kN = Unit<TIn>::kN;
-  extern __shared__ uint4 slice_smem[];
+__global__ void __launch_bounds__(kStreamThreads, 2) top_kernel(const TopArgs a, int upc) {
+  extern __shared__ uint4 dyn_smem[];  // stage maxima, then the keys sent to the first CTA
   __shared__ TopShared sh;
+  float* stage_max = reinterpret_cast<float*>(dyn_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t i = blockIdx.x / (unsigned)C;
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kSliceThreads, 3) top_kernel(const TopArgs a, 
   int32_t* ids = a.out_ids + i * k;
   float* lp = a.out_lp + i * k;
   auto fail = [&](int32_t bit) {
-    for (int q = tid; q < k; q += kSliceThreads) {
+    for (int q = tid; q < k; q += kStreamThreads) {
       ids[q] = -1;
       lp[q] = quiet_nan();
     }
@@ -199,18 +202,34 @@ __global__ void __launch_bounds__(kSliceThreads, 3) top_kernel(const TopArgs a, 
     if (rank == 0) fail(LS_ROW_ERR_BAD_GATHER);
     return;
   }
-  Slice<TIn> s;
-  s.init(slice_smem, a.logits, src, a.row_stride, a.vocab, upc, rank);
+  Run<TIn> run;
+  run.init(a.logits, src, a.row_stride, a.vocab, upc, rank);
+  typename Run<TIn>::Stage first;
+  run.prefetch(tid, first);
+  if (C > 1) cluster_arrive();
   if (tid == 0) {
     sh.count = 0;
     sh.total = 0u;
   }
-  s.start(sh.bars);
-  if (C > 1) cluster_arrive();
-  bool stalled = false;
-  const float mine = slice_max(s, sh.bars, &stalled);
+  const float c = kLog2e / a.temperature;
+  OnlineSum acc;
+  acc.init(c);
+  run.stream(first, [&](int u, typename Run<TIn>::Stage& v) {
+    float um = kNegInf;
+#pragma unroll
+    for (int q = 0; q < kStage; ++q) {
+      Unit<TIn>::clean(v[q]);
+      um = fmaxf(um, Unit<TIn>::max(v[q]));
+    }
+    // u = tid + stage * kStage * kStreamThreads
+    stage_max[(u - tid) / kStage + tid] = um;
+    acc.raise(um);
+#pragma unroll
+    for (int q = 0; q < kStage; ++q) acc.template add<TIn>(v[q]);
+  });
   // the j-th largest lane maximum of each warp that holds units (ties ranked by lane)
-  const int warps = min(kSliceWarps, (s.n + 31) / 32);
+  const float mine = acc.x.m;
+  const int warps = min(kStreamWarps, (run.n + 31) / 32);
   float bound = kPosInf;
   if (warp < warps) {
     const int j = (k + warps - 1) / warps;
@@ -222,26 +241,20 @@ __global__ void __launch_bounds__(kSliceThreads, 3) top_kernel(const TopArgs a, 
     }
     bound = j > 32 ? kNegInf : warp_max(above == j - 1 ? mine : kNegInf);
   }
-  const float c = kLog2e / a.temperature;
-  const float m = block_max(mine, sh.red);
-  __syncthreads();
-  if (lane == 0) sh.red[warp] = bound;
-  __syncthreads();
-  bound = s.n > 0 ? warp_min(sh.red[tid & (kSliceWarps - 1)]) : kNegInf;
-  ExpAgainst against;
-  against.init(m, c);
-  const float sum = block_sum(slice_sum(s, against), sh.red);
+  if (lane == 0) sh.redf[warp] = bound;
+  const float2 mine_ms = block_lse(mine, acc.sum(), c, sh.red);  // its barriers order redf too
+  bound = run.n > 0 ? warp_min(sh.redf[tid & (kStreamWarps - 1)]) : kNegInf;
   if (C > 1) {
     cluster_wait();  // every CTA of the cluster runs
     if (tid < C) {
-      peer_store2(peer_addr(smem_addr(&sh.ms[rank]), tid), m, sum);
+      peer_store2(peer_addr(smem_addr(&sh.ms[rank]), tid), mine_ms.x, mine_ms.y);
       peer_store(peer_addr(smem_addr(&sh.bound[rank]), tid), bound);
     }
     cluster_arrive();
     cluster_wait();
   } else {
     if (tid == 0) {
-      sh.ms[0] = make_float2(m, sum);
+      sh.ms[0] = mine_ms;
       sh.bound[0] = bound;
     }
     __syncthreads();
@@ -253,80 +266,71 @@ __global__ void __launch_bounds__(kSliceThreads, 3) top_kernel(const TopArgs a, 
     return;
   }
   bound = warp_max(lane < C ? sh.bound[lane] : kNegInf);
-  // entries at or above the bound
-  for (int u = tid; u < s.n; u += kSliceThreads) {
-    const uint4 w = s.buf[u];
-    if (Unit<TIn>::max(w) < bound) continue;
-#pragma unroll
-    for (int q = 0; q < kN / 2; ++q) {
-      float v[2];
-      unpack2(Unit<TIn>::pair(w, q), v[0], v[1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (v[e] >= bound && v[e] > kNegInf) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kLocal) sh.keys[at] = argmax_key(v[e], s.index(u * kN + 2 * q + e));
-        }
+  visit_stages<TIn>(run, stage_max, bound, [&](float v, int place) {
+    if (v >= bound && v > kNegInf) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kLocal) sh.keys[at] = argmax_key(v, run.j0 + place);
     }
-  }
+  });
   __syncthreads();
-  if (sh.count > kLocal) select_ties(s, k, bound, sh);
+  if (sh.count > kLocal) select_ties<TIn>(run, stage_max, k, bound, sh);
   const int n_local = sh.count;
-  // to the first CTA, over its slice
-  unsigned long long* all = reinterpret_cast<unsigned long long*>(slice_smem);
+  // to the first CTA, over its stage maxima
+  unsigned long long* all = reinterpret_cast<unsigned long long*>(dyn_smem);
   int n = n_local;
   if (C > 1) {
     if (tid == 0) sh.base = (int)peer_add(peer_addr(smem_addr(&sh.total), 0), (uint32_t)n_local);
     cluster_arrive();
-    cluster_wait();  // every CTA is done with its slice
+    cluster_wait();  // every CTA is done with its stage maxima
     const int base = sh.base;
-    for (int q = tid; q < n_local; q += kSliceThreads) peer_store(peer_addr(smem_addr(&all[base + q]), 0), sh.keys[q]);
+    for (int q = tid; q < n_local; q += kStreamThreads) peer_store(peer_addr(smem_addr(&all[base + q]), 0), sh.keys[q]);
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;
     n = (int)sh.total;
   } else {
-    for (int q = tid; q < n; q += kSliceThreads) all[q] = sh.keys[q];
+    for (int q = tid; q < n; q += kStreamThreads) all[q] = sh.keys[q];
     __syncthreads();
   }
   const float S = warp_reduce(ms.x > kNegInf ? ms.y * rel_exp(ms.x, M, c) : 0.f, OpAddF());
   const float lnS = logf(S);
-  auto put = [&](int place, unsigned long long key) {
+  auto put = [&](int at, unsigned long long key) {
     const float v = f32_from_key((uint32_t)(key >> 32));
-    ids[place] = argmax_index(key);
-    lp[place] = (v == M ? 0.f : (v - M) / a.temperature) - lnS;
+    ids[at] = argmax_index(key);
+    lp[at] = (v == M ? 0.f : (v - M) / a.temperature) - lnS;
   };
   if (n <= kRankMost) {
-    for (int q = tid; q < n; q += kSliceThreads) {
+    for (int q = tid; q < n; q += kStreamThreads) {
       const unsigned long long key = all[q];
-      int place = 0;
-      for (int o = 0; o < n; ++o) place += all[o] > key;
-      if (place < k) put(place, key);
+      int at = 0;
+      for (int o = 0; o < n; ++o) at += all[o] > key;
+      if (at < k) put(at, key);
     }
   } else {
     int size = 1;
     while (size < n) size <<= 1;
-    for (int q = n + tid; q < size; q += kSliceThreads) all[q] = 0ull;  // below every key
+    for (int q = n + tid; q < size; q += kStreamThreads) all[q] = 0ull;  // below every key
     sort_keys(all, size);
-    for (int q = tid; q < min(n, k); q += kSliceThreads) put(q, all[q]);
+    for (int q = tid; q < min(n, k); q += kStreamThreads) put(q, all[q]);
   }
-  for (int q = n + tid; q < k; q += kSliceThreads) {
+  for (int q = n + tid; q < k; q += kStreamThreads) {
     ids[q] = -1;
     lp[q] = kNegInf;
   }
-  if (tid == 0) {
-    if (a.out_lse) a.out_lse[i] = M / a.temperature + lnS;
-  }
-  if (stalled && a.error_word) atomicOr(a.error_word, LS_ROW_ERR_STALLED);
+  if (tid == 0 && a.out_lse) a.out_lse[i] = M / a.temperature + lnS;
 }
+
+constexpr int64_t kRunTop = 1024 * 1024;  // bytes of a CTA's run at most
 
 template <typename TIn>
 static ls_status launch_top(const TopArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
-  const SlicePlan plan = plan_slices(n, a.vocab, dtype);
-  // the first CTA takes every CTA's keys, padded to a power of two
+  const StreamPlan plan = plan_stream(n, a.vocab, dtype, kRunTop);
+  // stage maxima of every thread; the keys of every CTA, padded to a power of two
+  const size_t stages = ((size_t)plan.upc + kStage * kStreamThreads - 1) / (kStage * kStreamThreads);
+  const size_t maxima = stages * kStreamThreads * sizeof(float);
   const size_t keys = (size_t)plan.ctas * kLocal * sizeof(unsigned long long);
-  return launch_slices(top_kernel<TIn>, a, plan, plan.smem > keys ? plan.smem : keys, n, st, done);
+  return launch_rows(top_kernel<TIn>, a, plan, maxima > keys ? maxima : keys, n, st, done);
 }
 
 }  // namespace ops
