@@ -1,19 +1,31 @@
 // ls_process.cu -- penalties, biases and masks of allowed tokens on logits
 // rows (ls_process_logits).
 //
-// A row is cut into tiles of kTile entries, one CTA each.  The CTA keeps one
-// word per entry of its tile in shared memory: bit 0 says that the id occurs in
-// the request's history, the bits above count its occurrences past the
-// prompt.  It reads the whole history once (each tile of the row does), marks
-// the ids of its own tile, adds the row's biases and then passes over its
-// entries.
-#include "ls_row_ops.cuh"
+// A row is cut into tiles, one CTA each: kProcUnits 32-byte units per thread,
+// loaded to registers at the start and written at the end.  In between, the few
+// entries that the history or a bias touches are worked out on the side:
+//  1. The CTA reads the request's history (every tile of the row does: at the
+//     lengths that occur it is small against the row) and keeps the ids of its
+//     own tile in a table with one slot per entry: bit 0 says that the id
+//     occurs, the bits above count its occurrences past the prompt.
+//  2. Each touched entry is claimed by one thread (a bit per entry; biased
+//     entries belong to the thread of their bias), which reads the logit and
+//     the slot, works out the new value in fp32 and leaves it in the slot,
+//     rounded to the logits' type.
+//  3. Each unit takes the slots of its claimed entries and -inf where the mask
+//     says so, and is written: entries that nothing touches keep their bits.
+// The slot is as wide as it has to be: 16 bits hold a bf16 result and the
+// counts of a history of fewer than 2^15 ids; fp32 logits and longer histories
+// take 32.
+#include "ls_stream.cuh"
 
 namespace lsg {
 namespace ops {
 
 constexpr int kProcThreads = 256;
-constexpr int kTile = 4096;
+constexpr int kProcUnits = 4;   // units per thread
+constexpr int kHeldTokens = 4;  // history ids of a thread kept in registers between steps 1 and 2
+constexpr int kTileUnits = kProcThreads * kProcUnits;
 
 struct ProcessArgs {
   const void* logits;
@@ -31,88 +43,177 @@ struct ProcessArgs {
   int32_t* error_word;
 };
 
-template <typename TIn>
-__global__ void __launch_bounds__(kProcThreads) process_kernel(const ProcessArgs a, int tiles) {
+// A table slot in shared memory: an atomic update of 16-bit slots works on the
+// 32-bit word that holds two (no carry crosses: see the widths above).
+template <typename Slot>
+__device__ __forceinline__ void mark(Slot* table, int e, bool prompt) {
+  uint32_t* word = reinterpret_cast<uint32_t*>(table) + (sizeof(Slot) == 2 ? e >> 1 : e);
+  const int shift = sizeof(Slot) == 2 ? (e & 1) * 16 : 0;
+  if (prompt)
+    atomicOr(word, 1u << shift);
+  else
+    atomicAdd(word, 2u << shift);
+}
+
+// Bits [j, j + N) of a mask row, 1 outside [0, vocab) (j may lie before the row).
+template <int N>
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int64_t j, int64_t vocab) {
+  const int64_t last = (vocab - 1) >> 5, w = j >> 5;  // arithmetic: -1 for a negative j
+  const uint32_t lo = w >= 0 && w <= last ? __ldg(mask + w) : 0xFFFFFFFFu;
+  const int shift = (int)(j & 31);
+  uint32_t hi = 0xFFFFFFFFu;
+  if (shift > 32 - N && w + 1 <= last) hi = __ldg(mask + w + 1);
+  return __funnelshift_r(lo, hi, shift) & ((1u << N) - 1u);
+}
+
+template <typename TIn, typename Slot>
+__global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessArgs a, int tiles) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
-  __shared__ uint32_t marks[kTile];
-  __shared__ float bias[kTile];
+  constexpr int kN = Unit<TIn>::kN;
+  constexpr int kEntries = kTileUnits * kN;
+  extern __shared__ uint4 dyn_smem[];
+  Slot* table = reinterpret_cast<Slot*>(dyn_smem);
+  uint32_t* claimed = reinterpret_cast<uint32_t*>(table + kEntries);  // a bit per entry
+  uint32_t* biased = claimed + kEntries / 32;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)tiles;
-  const int64_t j0 = (int64_t)(blockIdx.x % (unsigned)tiles) * kTile;
-  const int len = (int)min((int64_t)kTile, a.vocab - j0);
-  Raw* out = static_cast<Raw*>(a.out) + i * a.out_stride + j0;
+  const int tile = (int)(blockIdx.x % (unsigned)tiles);
+  Raw* out = static_cast<Raw*>(a.out) + i * a.out_stride;
 
   int32_t bad = 0;
   const int64_t src = a.gather ? a.gather[i] : i;
+  const int64_t r = a.has_params ? (a.t2r ? a.t2r[i] : i) : 0;
+  const int64_t mrow = a.mask ? (a.mask_index ? a.mask_index[i] : i) : -1;
   if (src < 0 || src >= a.logits_rows) bad |= LS_ROW_ERR_BAD_GATHER;
-  int64_t r = 0;
-  if (a.has_params) {
-    r = a.t2r ? a.t2r[i] : i;
-    if (r < 0 || r >= a.p.num_requests) bad |= LS_ROW_ERR_BAD_REQUEST;
-  }
-  int64_t mrow = -1;
-  if (a.mask) {
-    mrow = a.mask_index ? a.mask_index[i] : i;
-    if (mrow < -1 || mrow >= a.mask_rows) bad |= LS_ROW_ERR_BAD_MASK;
-  }
+  if (a.has_params && (r < 0 || r >= a.p.num_requests)) bad |= LS_ROW_ERR_BAD_REQUEST;
+  if (mrow < -1 || mrow >= a.mask_rows) bad |= a.mask ? LS_ROW_ERR_BAD_MASK : 0;
+  Run<TIn> run;
+  run.init(a.logits, bad & LS_ROW_ERR_BAD_GATHER ? 0 : src, a.row_stride, a.vocab, kTileUnits, tile);
+  const bool same = run.aligned_with(out);
+  uint32_t v[kProcUnits][8];
   if (bad) {
-    for (int e = tid; e < len; e += kProcThreads) out[e] = E::put(quiet_nan());
-    if (tid == 0 && j0 == 0 && a.error_word) atomicOr(a.error_word, bad);
+    const Raw nan = E::put(quiet_nan());
+    Raw e[kN];
+#pragma unroll
+    for (int q = 0; q < kN; ++q) e[q] = nan;
+    memcpy(v[0], e, 32);
+    for (int u = tid; u < run.n; u += kProcThreads) run.store(out, same, u, v[0]);
+    if (tid == 0 && tile == 0 && a.error_word) atomicOr(a.error_word, bad);
     return;
   }
-  const Raw* in = static_cast<const Raw*>(a.logits) + src * a.row_stride + j0;
+#pragma unroll
+  for (int q = 0; q < kProcUnits; ++q)
+    if (tid + q * kProcThreads < run.n) run.template load<true>(tid + q * kProcThreads, v[q]);
 
-  for (int e = tid; e < kTile; e += kProcThreads) {
-    marks[e] = 0u;
-    bias[e] = 0.f;
-  }
-  __syncthreads();
+  // The request's penalties; neutral ones leave the history unread.
   float rho = 1.f, pres = 0.f, freq = 0.f;
-  if (a.has_params && a.p.tokens) {
-    if (a.p.repetition) rho = a.p.repetition[r];
-    if (a.p.presence) pres = a.p.presence[r];
-    if (a.p.frequency) freq = a.p.frequency[r];
-    const int32_t L = min(max(a.row_lens ? a.row_lens[i] : a.p.seq_lens[r], 0), a.p.token_capacity);
-    const int32_t prompt = a.p.prompt_lens ? a.p.prompt_lens[r] : 0;
-    const int32_t* t = a.p.tokens + r * a.p.token_stride;
-    for (int32_t q = tid; q < L; q += kProcThreads) {
-      const int64_t e = (int64_t)t[q] - j0;
-      if (e >= 0 && e < len) {
-        if (q < prompt)
-          atomicOr(&marks[e], 1u);
-        else
-          atomicAdd(&marks[e], 2u);
+  int32_t L = 0, prompt = 0;
+  const int32_t* history = nullptr;
+  int32_t b_lo = 0, b_hi = 0;
+  if (a.has_params) {
+    if (a.p.tokens) {
+      if (a.p.repetition) rho = a.p.repetition[r];
+      if (a.p.presence) pres = a.p.presence[r];
+      if (a.p.frequency) freq = a.p.frequency[r];
+      L = a.row_lens ? a.row_lens[i] : a.p.seq_lens[r];
+      prompt = a.p.prompt_lens ? a.p.prompt_lens[r] : 0;
+      L = min(max(L, 0), a.p.token_capacity);
+      if (rho == 1.f && pres == 0.f && freq == 0.f) L = 0;
+      history = a.p.tokens + r * a.p.token_stride;
+    }
+    if (a.p.bias_offsets) {
+      b_lo = max(a.p.bias_offsets[r], 0);
+      b_hi = min(a.p.bias_offsets[r + 1], a.p.bias_count);
+    }
+  }
+  const bool touched = L > 0 || b_lo < b_hi;  // the same in every thread
+  const uint32_t* mask = mrow >= 0 ? a.mask + mrow * a.mask_stride : nullptr;
+  if (touched) {
+    // table, claimed and biased bits
+    constexpr int kWords = (kEntries * (int)sizeof(Slot) + kEntries / 4) / 16;
+    for (int q = tid; q < kWords; q += kProcThreads) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
+    int32_t held[kHeldTokens];
+#pragma unroll
+    for (int q = 0; q < kHeldTokens; ++q) {
+      const int32_t at = tid + q * kProcThreads;
+      held[q] = at < L ? run.place(history[at]) : -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kHeldTokens; ++q)
+      if (held[q] >= 0) mark(table, held[q], tid + q * kProcThreads < prompt);
+    for (int32_t at = tid + kHeldTokens * kProcThreads; at < L; at += kProcThreads) {
+      const int e = run.place(history[at]);
+      if (e >= 0) mark(table, e, at < prompt);
+    }
+    for (int32_t q = b_lo + tid; q < b_hi; q += kProcThreads) {
+      const int e = run.place(a.p.bias_ids[q]);
+      if (e >= 0) atomicOr(&biased[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    // the new value of entry e (called by its one thread)
+    auto settle = [&](int e, float b, bool has_bias) {
+      const int64_t j = run.j0 + e;
+      if (j < 0 || j >= run.V) return;  // an id out of range falls into an edge unit's padding
+      const uint32_t bit = 1u << (e & 31);
+      if (!has_bias && (biased[e >> 5] & bit)) return;
+      if (atomicOr(&claimed[e >> 5], bit) & bit) return;
+      const uint32_t m = table[e];
+      const float x = E::get(run.row[j]);
+      const float n = (float)(m >> 1);
+      float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
+      y = __fsub_rn(y, __fmul_rn(freq, n));
+      if (n > 0.f) y -= pres;
+      if (has_bias) y += b;
+      const Raw raw = E::put(guard(y));
+      if (sizeof(Slot) == sizeof(Raw))
+        memcpy(&table[e], &raw, sizeof(Raw));
+      else
+        table[e] = (Slot) * reinterpret_cast<const uint16_t*>(&raw);
+    };
+#pragma unroll
+    for (int q = 0; q < kHeldTokens; ++q)
+      if (held[q] >= 0) settle(held[q], 0.f, false);
+    for (int32_t at = tid + kHeldTokens * kProcThreads; at < L; at += kProcThreads) {
+      const int e = run.place(history[at]);
+      if (e >= 0) settle(e, 0.f, false);
+    }
+    for (int32_t q = b_lo + tid; q < b_hi; q += kProcThreads) {
+      const int e = run.place(a.p.bias_ids[q]);
+      if (e >= 0) settle(e, a.p.bias_values[q], true);
+    }
+    __syncthreads();  // and every read of the logits is done: the output may replace them
+  }
+#pragma unroll
+  for (int q = 0; q < kProcUnits; ++q) {
+    const int u = tid + q * kProcThreads;
+    if (u >= run.n) break;
+    if (touched) {
+      const uint32_t take = kN == 16 ? reinterpret_cast<const uint16_t*>(claimed)[u] : reinterpret_cast<const uint8_t*>(claimed)[u];
+      if (take) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+          if (take >> k & 1u) Unit<TIn>::set(v[q], k, (uint32_t)table[u * kN + k]);
       }
     }
-  }
-  bool biased = false;
-  if (a.has_params && a.p.bias_offsets) {
-    const int32_t lo = max(a.p.bias_offsets[r], 0), hi = min(a.p.bias_offsets[r + 1], a.p.bias_count);
-    biased = lo < hi;
-    for (int32_t q = lo + tid; q < hi; q += kProcThreads) {
-      const int64_t e = (int64_t)a.p.bias_ids[q] - j0;
-      if (e >= 0 && e < len) bias[e] = a.p.bias_values[q];
+    if (mask) {
+      const uint32_t forbidden = ~mask_bits<kN>(mask, run.index(u), run.V) & ((1u << kN) - 1u);
+      if (forbidden) Unit<TIn>::drop(v[q], forbidden);
     }
+    run.store(out, same, u, v[q]);
   }
-  __syncthreads();
-  const uint32_t* mask = mrow >= 0 ? a.mask + mrow * a.mask_stride : nullptr;
-  for (int e = tid; e < len; e += kProcThreads) {
-    Raw raw = in[e];
-    const uint32_t m = marks[e];
-    const float b = biased ? bias[e] : 0.f;
-    if (m != 0u || b != 0.f) {
-      const float x = E::get(raw);
-      const float c = (float)(m >> 1);
-      float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
-      y = __fsub_rn(y, __fmul_rn(freq, c));
-      if (c > 0.f) y -= pres;
-      y += b;
-      raw = E::put(guard(y));
-    }
-    if (mask && !((mask[(j0 + e) >> 5] >> ((j0 + e) & 31)) & 1u)) raw = E::neg_inf();
-    out[e] = raw;
-  }
+}
+
+template <typename TIn, typename Slot>
+static ls_status launch(const ProcessArgs& a, int64_t tiles, int32_t n, cudaStream_t st) {
+  static std::atomic<int> done[kMaxDevices];
+  constexpr int kEntries = kTileUnits * Unit<TIn>::kN;
+  const bool side = a.has_params && (a.p.tokens || a.p.bias_offsets);
+  const size_t smem = side ? (size_t)kEntries * sizeof(Slot) + kEntries / 4 : 0;
+  if (!open_limits(process_kernel<TIn, Slot>, done)) return LS_ERR_CUDA;
+  process_kernel<TIn, Slot><<<dim3((unsigned)(tiles * n)), dim3(kProcThreads), smem, st>>>(a, (int)tiles);
+  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
 }
 
 }  // namespace ops
@@ -148,7 +249,7 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
   if (allowed_mask &&
       (mask_rows < 1 || mask_stride < (vocab + 31) / 32 || (!mask_index && (int64_t)n > mask_rows)))
     return LS_ERR_INVALID_ARG;
-  const int64_t tiles = (vocab + kTile - 1) / kTile;
+  const int64_t tiles = (row_units(vocab, dtype) + kTileUnits - 1) / kTileUnits;
   if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   a.logits = logits;
   a.logits_rows = logits_rows;
@@ -165,10 +266,8 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
   a.out_stride = out_stride;
   a.error_word = error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)(tiles * n)), block(kProcThreads);
-  if (dtype == LS_DTYPE_BF16)
-    process_kernel<bf16_tag><<<grid, block, 0, st>>>(a, (int)tiles);
-  else
-    process_kernel<float><<<grid, block, 0, st>>>(a, (int)tiles);
-  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+  if (dtype == LS_DTYPE_F32) return launch<float, uint32_t>(a, tiles, n, st);
+  // counts of a history that fits 15 bits leave a 16-bit slot
+  if (!a.has_params || !a.p.tokens || a.p.token_capacity < (1 << 15)) return launch<bf16_tag, uint16_t>(a, tiles, n, st);
+  return launch<bf16_tag, uint32_t>(a, tiles, n, st);
 }

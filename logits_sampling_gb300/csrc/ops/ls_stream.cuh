@@ -99,6 +99,10 @@ struct Unit<bf16_tag> {
   __device__ __forceinline__ static void set_pair(uint32_t (&w)[8], int q, float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[q]) : "f"(hi), "f"(lo));
   }
+  // Entry e becomes the value with these bits.
+  __device__ __forceinline__ static void set(uint32_t (&w)[8], int e, uint32_t raw) {
+    w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | raw << 16 : (w[e >> 1] & 0xFFFF0000u) | (raw & 0xFFFFu);
+  }
   // -inf in the entries whose bit is set.
   __device__ __forceinline__ static void drop(uint32_t (&w)[8], uint32_t bits) {
 #pragma unroll
@@ -128,6 +132,7 @@ struct Unit<float> {
     w[2 * q] = __float_as_uint(lo);
     w[2 * q + 1] = __float_as_uint(hi);
   }
+  __device__ __forceinline__ static void set(uint32_t (&w)[8], int e, uint32_t raw) { w[e] = raw; }
   __device__ __forceinline__ static void drop(uint32_t (&w)[8], uint32_t bits) {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
