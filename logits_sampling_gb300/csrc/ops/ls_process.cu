@@ -1,18 +1,19 @@
 // ls_process.cu -- penalties, biases and masks of allowed tokens on logits
 // rows (ls_process_logits).
 //
-// A row is cut into tiles, one CTA each: kProcUnits 32-byte units per thread,
-// loaded to registers at the start and written at the end.  In between, the few
+// A row is cut into tiles, one CTA each: kUnits 32-byte units per thread,
+// loaded to registers at the start and written at the end (four, or one where
+// that leaves SMs without a CTA).  In between, the few
 // entries that the history or a bias touches are worked out on the side:
 //  1. The CTA reads the request's history (every tile of the row does: at the
 //     lengths that occur it is small against the row) and keeps the ids of its
 //     own tile in a table with one slot per entry: bit 0 says that the id
-//     occurs, the bits above count its occurrences past the prompt.
-//  2. Each touched entry is claimed by one thread (a bit per entry; biased
-//     entries belong to the thread of their bias), which reads the logit and
-//     the slot, works out the new value in fp32 and leaves it in the slot,
-//     rounded to the logits' type.
-//  3. Each unit takes the slots of its claimed entries and -inf where the mask
+//     occurs, the bits above count its occurrences past the prompt.  The first
+//     occurrence of an id sets the entry's touched bit and lists the entry.
+//  2. One thread per listed entry, and one per bias, reads the logit and the
+//     slot, works out the new value in fp32 and leaves it in the slot, rounded
+//     to the logits' type.
+//  3. Each unit takes the slots of its touched entries and -inf where the mask
 //     says so, and is written: entries that nothing touches keep their bits.
 // The slot is as wide as it has to be: 16 bits hold a bf16 result and the
 // counts of a history of fewer than 2^15 ids; fp32 logits and longer histories
@@ -23,9 +24,8 @@ namespace lsg {
 namespace ops {
 
 constexpr int kProcThreads = 256;
-constexpr int kProcUnits = 4;   // units per thread
-constexpr int kHeldTokens = 4;  // history ids of a thread kept in registers between steps 1 and 2
-constexpr int kTileUnits = kProcThreads * kProcUnits;
+constexpr int kHistoryBatch = 8;  // history ids of a thread in flight
+constexpr int kListed = 2048;     // touched entries listed; past it step 2 walks the touched bits
 
 struct ProcessArgs {
   const void* logits;
@@ -66,16 +66,19 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int64_t j, i
   return __funnelshift_r(lo, hi, shift) & ((1u << N) - 1u);
 }
 
-template <typename TIn, typename Slot>
+template <typename TIn, typename Slot, int kUnits>
 __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessArgs a, int tiles) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
   constexpr int kN = Unit<TIn>::kN;
-  constexpr int kEntries = kTileUnits * kN;
+  constexpr int kTileUnits = kProcThreads * kUnits, kEntries = kTileUnits * kN;
   extern __shared__ uint4 dyn_smem[];
   Slot* table = reinterpret_cast<Slot*>(dyn_smem);
-  uint32_t* claimed = reinterpret_cast<uint32_t*>(table + kEntries);  // a bit per entry
-  uint32_t* biased = claimed + kEntries / 32;
+  uint32_t* touched = reinterpret_cast<uint32_t*>(table + kEntries);  // a bit per entry
+  uint32_t* biased = touched + kEntries / 32;                         // entries of a bias
+  uint32_t* settled = biased + kEntries / 32;                         // those whose bias is applied
+  __shared__ uint16_t list[kListed];
+  __shared__ int listed;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)tiles;
   const int tile = (int)(blockIdx.x % (unsigned)tiles);
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   Run<TIn> run;
   run.init(a.logits, bad & LS_ROW_ERR_BAD_GATHER ? 0 : src, a.row_stride, a.vocab, kTileUnits, tile);
   const bool same = run.aligned_with(out);
-  uint32_t v[kProcUnits][8];
+  uint32_t v[kUnits][8];
   if (bad) {
     const Raw nan = E::put(quiet_nan());
     Raw e[kN];
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
     return;
   }
 #pragma unroll
-  for (int q = 0; q < kProcUnits; ++q)
+  for (int q = 0; q < kUnits; ++q)
     if (tid + q * kProcThreads < run.n) run.template load<true>(tid + q * kProcThreads, v[q]);
 
   // The request's penalties; neutral ones leave the history unread.
@@ -127,40 +130,47 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
       b_hi = min(a.p.bias_offsets[r + 1], a.p.bias_count);
     }
   }
-  const bool touched = L > 0 || b_lo < b_hi;  // the same in every thread
+  const bool any = L > 0 || b_lo < b_hi;  // the same in every thread
   const uint32_t* mask = mrow >= 0 ? a.mask + mrow * a.mask_stride : nullptr;
-  if (touched) {
-    // table, claimed and biased bits
-    constexpr int kWords = (kEntries * (int)sizeof(Slot) + kEntries / 4) / 16;
+  if (any) {
+    constexpr int kWords = (kEntries * (int)sizeof(Slot) + 3 * (kEntries / 8)) / 16;  // table and bits
     for (int q = tid; q < kWords; q += kProcThreads) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
-    int32_t held[kHeldTokens];
+    if (tid == 0) listed = 0;
+    int32_t held[kHistoryBatch];
+    auto fetch = [&](int32_t at) {
 #pragma unroll
-    for (int q = 0; q < kHeldTokens; ++q) {
-      const int32_t at = tid + q * kProcThreads;
-      held[q] = at < L ? run.place(history[at]) : -1;
-    }
+      for (int q = 0; q < kHistoryBatch; ++q) {
+        const int32_t t = at + q * kProcThreads;
+        held[q] = t < L ? history[t] : -1;
+      }
+    };
+    fetch(tid);
     __syncthreads();
+    for (int32_t at = tid; at - tid < L; at += kHistoryBatch * kProcThreads) {
+      if (at != tid) fetch(at);
 #pragma unroll
-    for (int q = 0; q < kHeldTokens; ++q)
-      if (held[q] >= 0) mark(table, held[q], tid + q * kProcThreads < prompt);
-    for (int32_t at = tid + kHeldTokens * kProcThreads; at < L; at += kProcThreads) {
-      const int e = run.place(history[at]);
-      if (e >= 0) mark(table, e, at < prompt);
+      for (int q = 0; q < kHistoryBatch; ++q) {
+        const int e = held[q] >= 0 && held[q] < run.V ? run.place(held[q]) : -1;
+        if (e >= 0) {
+          mark(table, e, at + q * kProcThreads < prompt);
+          const uint32_t bit = 1u << (e & 31);
+          if (!(atomicOr(&touched[e >> 5], bit) & bit)) {
+            const int n = atomicAdd(&listed, 1);
+            if (n < kListed) list[n] = (uint16_t)e;
+          }
+        }
+      }
     }
     for (int32_t q = b_lo + tid; q < b_hi; q += kProcThreads) {
-      const int e = run.place(a.p.bias_ids[q]);
+      const int32_t id = a.p.bias_ids[q];
+      const int e = id >= 0 && id < run.V ? run.place(id) : -1;
       if (e >= 0) atomicOr(&biased[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    // the new value of entry e (called by its one thread)
+    // the new value of entry e (called by one thread per entry)
     auto settle = [&](int e, float b, bool has_bias) {
-      const int64_t j = run.j0 + e;
-      if (j < 0 || j >= run.V) return;  // an id out of range falls into an edge unit's padding
-      const uint32_t bit = 1u << (e & 31);
-      if (!has_bias && (biased[e >> 5] & bit)) return;
-      if (atomicOr(&claimed[e >> 5], bit) & bit) return;
       const uint32_t m = table[e];
-      const float x = E::get(run.row[j]);
+      const float x = E::get(run.row[run.j0 + e]);
       const float n = (float)(m >> 1);
       float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
       y = __fsub_rn(y, __fmul_rn(freq, n));
@@ -172,25 +182,32 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
       else
         table[e] = (Slot) * reinterpret_cast<const uint16_t*>(&raw);
     };
-#pragma unroll
-    for (int q = 0; q < kHeldTokens; ++q)
-      if (held[q] >= 0) settle(held[q], 0.f, false);
-    for (int32_t at = tid + kHeldTokens * kProcThreads; at < L; at += kProcThreads) {
-      const int e = run.place(history[at]);
-      if (e >= 0) settle(e, 0.f, false);
+    const int n_listed = listed;
+    if (n_listed <= kListed) {
+      for (int q = tid; q < n_listed; q += kProcThreads) {
+        const int e = list[q];
+        if (!(biased[e >> 5] >> (e & 31) & 1u)) settle(e, 0.f, false);
+      }
+    } else {
+      for (int q = tid; q < kEntries / 32; q += kProcThreads)
+        for (uint32_t w = touched[q] & ~biased[q]; w; w &= w - 1) settle(q * 32 + __ffs((int)w) - 1, 0.f, false);
     }
     for (int32_t q = b_lo + tid; q < b_hi; q += kProcThreads) {
-      const int e = run.place(a.p.bias_ids[q]);
-      if (e >= 0) settle(e, a.p.bias_values[q], true);
+      const int32_t id = a.p.bias_ids[q];
+      const int e = id >= 0 && id < run.V ? run.place(id) : -1;
+      if (e < 0) continue;
+      const uint32_t bit = 1u << (e & 31);
+      if (!(atomicOr(&settled[e >> 5], bit) & bit)) settle(e, a.p.bias_values[q], true);
     }
     __syncthreads();  // and every read of the logits is done: the output may replace them
   }
 #pragma unroll
-  for (int q = 0; q < kProcUnits; ++q) {
+  for (int q = 0; q < kUnits; ++q) {
     const int u = tid + q * kProcThreads;
     if (u >= run.n) break;
-    if (touched) {
-      const uint32_t take = kN == 16 ? reinterpret_cast<const uint16_t*>(claimed)[u] : reinterpret_cast<const uint8_t*>(claimed)[u];
+    if (any) {
+      const uint32_t take = kN == 16 ? reinterpret_cast<const uint16_t*>(touched)[u] | reinterpret_cast<const uint16_t*>(biased)[u]
+                                     : reinterpret_cast<const uint8_t*>(touched)[u] | reinterpret_cast<const uint8_t*>(biased)[u];
       if (take) {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
@@ -205,15 +222,24 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   }
 }
 
-template <typename TIn, typename Slot>
-static ls_status launch(const ProcessArgs& a, int64_t tiles, int32_t n, cudaStream_t st) {
+template <typename TIn, typename Slot, int kUnits>
+static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
-  constexpr int kEntries = kTileUnits * Unit<TIn>::kN;
+  constexpr int kTileUnits = kProcThreads * kUnits, kEntries = kTileUnits * Unit<TIn>::kN;
+  const int64_t tiles = (row_units(a.vocab, dtype) + kTileUnits - 1) / kTileUnits;
+  if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   const bool side = a.has_params && (a.p.tokens || a.p.bias_offsets);
-  const size_t smem = side ? (size_t)kEntries * sizeof(Slot) + kEntries / 4 : 0;
-  if (!open_limits(process_kernel<TIn, Slot>, done)) return LS_ERR_CUDA;
-  process_kernel<TIn, Slot><<<dim3((unsigned)(tiles * n)), dim3(kProcThreads), smem, st>>>(a, (int)tiles);
+  const size_t smem = side ? (size_t)kEntries * sizeof(Slot) + 3 * (kEntries / 8) : 0;
+  if (!open_limits(process_kernel<TIn, Slot, kUnits>, done)) return LS_ERR_CUDA;
+  process_kernel<TIn, Slot, kUnits><<<dim3((unsigned)(tiles * n)), dim3(kProcThreads), smem, st>>>(a, (int)tiles);
   return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+}
+
+template <typename TIn, typename Slot>
+static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
+  const int64_t wide = (row_units(a.vocab, dtype) + 4 * kProcThreads - 1) / (4 * kProcThreads) * n;
+  return wide < 2 * device_attr<cudaDevAttrMultiProcessorCount>() ? launch<TIn, Slot, 1>(a, dtype, n, st)
+                                                                  : launch<TIn, Slot, 4>(a, dtype, n, st);
 }
 
 }  // namespace ops
@@ -249,8 +275,6 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
   if (allowed_mask &&
       (mask_rows < 1 || mask_stride < (vocab + 31) / 32 || (!mask_index && (int64_t)n > mask_rows)))
     return LS_ERR_INVALID_ARG;
-  const int64_t tiles = (row_units(vocab, dtype) + kTileUnits - 1) / kTileUnits;
-  if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   a.logits = logits;
   a.logits_rows = logits_rows;
   a.vocab = vocab;
@@ -266,8 +290,8 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
   a.out_stride = out_stride;
   a.error_word = error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == LS_DTYPE_F32) return launch<float, uint32_t>(a, tiles, n, st);
+  if (dtype == LS_DTYPE_F32) return launch<float, uint32_t>(a, dtype, n, st);
   // counts of a history that fits 15 bits leave a 16-bit slot
-  if (!a.has_params || !a.p.tokens || a.p.token_capacity < (1 << 15)) return launch<bf16_tag, uint16_t>(a, tiles, n, st);
-  return launch<bf16_tag, uint32_t>(a, tiles, n, st);
+  if (!a.has_params || !a.p.tokens || a.p.token_capacity < (1 << 15)) return launch<bf16_tag, uint16_t>(a, dtype, n, st);
+  return launch<bf16_tag, uint32_t>(a, dtype, n, st);
 }
