@@ -24,6 +24,7 @@ namespace ops {
 struct alignas(16) RowStats {
   float M, alpha, Mr, kappa, scale, pad[3];
 };
+static_assert(kStreamThreads >= LS_MAX_TOP, "a thread per teacher entry");
 static_assert(sizeof(RowStats) == sizeof(float) * LS_DISTILL_STATS, "the header's size of a row's stats");
 
 struct DistillArgs {
@@ -73,7 +74,7 @@ struct DistillShared {
 };
 
 template <typename TIn, bool kGrad>
-__global__ void __launch_bounds__(kStreamThreads, 2) distill_kernel(const DistillArgs a, int upc) {
+__global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const DistillArgs a, int upc) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
   constexpr int kN = Unit<TIn>::kN;

@@ -10,14 +10,13 @@
 //     own tile in a table with one slot per entry: bit 0 says that the id
 //     occurs, the bits above count its occurrences past the prompt.  The first
 //     occurrence of an id sets the entry's touched bit and lists the entry.
-//  2. One thread per listed entry, and one per bias, reads the logit and the
-//     slot, works out the new value in fp32 and leaves it in the slot, rounded
-//     to the logits' type.
-//  3. Each unit takes the slots of its touched entries and -inf where the mask
-//     says so, and is written: entries that nothing touches keep their bits.
-// The slot is as wide as it has to be: 16 bits hold a bf16 result and the
-// counts of a history of fewer than 2^15 ids; fp32 logits and longer histories
-// take 32.
+//  2. Each unit takes -inf where the mask says so and is written: entries that
+//     nothing touches keep their bits.
+//  3. One thread per listed entry, and one per bias, reads the logit and the
+//     slot, works out the new value in fp32 and writes it over the copy, unless
+//     the mask forbids the id.  (In place the logit is still there: step 2
+//     wrote the same bits, or -inf where the mask forbids it.)
+// A slot of 16 bits holds the counts of a history of fewer than 2^15 ids.
 #include "ls_stream.cuh"
 
 namespace lsg {
@@ -57,12 +56,18 @@ __device__ __forceinline__ void mark(Slot* table, int e, bool prompt) {
 
 // Bits [j, j + N) of a mask row, 1 outside [0, vocab) (j may lie before the row).
 template <int N>
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int64_t j, int64_t vocab) {
-  const int64_t last = (vocab - 1) >> 5, w = j >> 5;  // arithmetic: -1 for a negative j
-  const uint32_t lo = w >= 0 && w <= last ? __ldg(mask + w) : 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int64_t j, int64_t vocab, bool full) {
+  const int64_t w = j >> 5;  // arithmetic: -1 for a negative j
   const int shift = (int)(j & 31);
-  uint32_t hi = 0xFFFFFFFFu;
-  if (shift > 32 - N && w + 1 <= last) hi = __ldg(mask + w + 1);
+  uint32_t lo, hi = 0xFFFFFFFFu;
+  if (full) {  // all N entries lie in the row: so do their words
+    lo = __ldg(mask + w);
+    if (shift > 32 - N) hi = __ldg(mask + w + 1);
+  } else {
+    const int64_t last = (vocab - 1) >> 5;
+    lo = w >= 0 && w <= last ? __ldg(mask + w) : 0xFFFFFFFFu;
+    if (shift > 32 - N && w + 1 <= last) hi = __ldg(mask + w + 1);
+  }
   return __funnelshift_r(lo, hi, shift) & ((1u << N) - 1u);
 }
 
@@ -167,20 +172,32 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
       if (e >= 0) atomicOr(&biased[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
+  }
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    const int u = tid + q * kProcThreads;
+    if (u >= run.n) break;
+    if (mask) {
+      const uint32_t all = (1u << kN) - 1u;
+      const uint32_t forbidden = ~mask_bits<kN>(mask, run.index(u), run.V, run.full(u)) & all;
+      if (forbidden) Unit<TIn>::drop(v[q], forbidden);
+    }
+    run.store(out, same, u, v[q]);
+  }
+  if (any) {
+    __syncthreads();  // the unit's copies are written before their touched entries are
     // the new value of entry e (called by one thread per entry)
     auto settle = [&](int e, float b, bool has_bias) {
+      const int64_t j = run.j0 + e;
+      if (mask && !(__ldg(mask + (j >> 5)) >> (j & 31) & 1u)) return;
       const uint32_t m = table[e];
-      const float x = E::get(run.row[run.j0 + e]);
+      const float x = E::get(run.row[j]);
       const float n = (float)(m >> 1);
       float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
       y = __fsub_rn(y, __fmul_rn(freq, n));
       if (n > 0.f) y -= pres;
       if (has_bias) y += b;
-      const Raw raw = E::put(guard(y));
-      if (sizeof(Slot) == sizeof(Raw))
-        memcpy(&table[e], &raw, sizeof(Raw));
-      else
-        table[e] = (Slot) * reinterpret_cast<const uint16_t*>(&raw);
+      out[j] = E::put(guard(y));
     };
     const int n_listed = listed;
     if (n_listed <= kListed) {
@@ -199,26 +216,6 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
       const uint32_t bit = 1u << (e & 31);
       if (!(atomicOr(&settled[e >> 5], bit) & bit)) settle(e, a.p.bias_values[q], true);
     }
-    __syncthreads();  // and every read of the logits is done: the output may replace them
-  }
-#pragma unroll
-  for (int q = 0; q < kUnits; ++q) {
-    const int u = tid + q * kProcThreads;
-    if (u >= run.n) break;
-    if (any) {
-      const uint32_t take = kN == 16 ? reinterpret_cast<const uint16_t*>(touched)[u] | reinterpret_cast<const uint16_t*>(biased)[u]
-                                     : reinterpret_cast<const uint8_t*>(touched)[u] | reinterpret_cast<const uint8_t*>(biased)[u];
-      if (take) {
-#pragma unroll
-        for (int k = 0; k < kN; ++k)
-          if (take >> k & 1u) Unit<TIn>::set(v[q], k, (uint32_t)table[u * kN + k]);
-      }
-    }
-    if (mask) {
-      const uint32_t forbidden = ~mask_bits<kN>(mask, run.index(u), run.V) & ((1u << kN) - 1u);
-      if (forbidden) Unit<TIn>::drop(v[q], forbidden);
-    }
-    run.store(out, same, u, v[q]);
   }
 }
 
@@ -290,8 +287,7 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
   a.out_stride = out_stride;
   a.error_word = error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == LS_DTYPE_F32) return launch<float, uint32_t>(a, dtype, n, st);
-  // counts of a history that fits 15 bits leave a 16-bit slot
-  if (!a.has_params || !a.p.tokens || a.p.token_capacity < (1 << 15)) return launch<bf16_tag, uint16_t>(a, dtype, n, st);
-  return launch<bf16_tag, uint32_t>(a, dtype, n, st);
+  const bool narrow = !a.has_params || !a.p.tokens || a.p.token_capacity < (1 << 15);
+  if (dtype == LS_DTYPE_F32) return narrow ? launch<float, uint16_t>(a, dtype, n, st) : launch<float, uint32_t>(a, dtype, n, st);
+  return narrow ? launch<bf16_tag, uint16_t>(a, dtype, n, st) : launch<bf16_tag, uint32_t>(a, dtype, n, st);
 }

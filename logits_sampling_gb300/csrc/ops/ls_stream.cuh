@@ -14,7 +14,7 @@
 namespace lsg {
 namespace ops {
 
-constexpr int kStreamThreads = 512;
+constexpr int kStreamThreads = 256;
 constexpr int kStreamWarps = kStreamThreads / 32;
 constexpr int kStage = 2;  // units of a thread per stage
 constexpr int kMaxCluster = 8;
@@ -99,16 +99,12 @@ struct Unit<bf16_tag> {
   __device__ __forceinline__ static void set_pair(uint32_t (&w)[8], int q, float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[q]) : "f"(hi), "f"(lo));
   }
-  // Entry e becomes the value with these bits.
-  __device__ __forceinline__ static void set(uint32_t (&w)[8], int e, uint32_t raw) {
-    w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | raw << 16 : (w[e >> 1] & 0xFFFF0000u) | (raw & 0xFFFFu);
-  }
   // -inf in the entries whose bit is set.
   __device__ __forceinline__ static void drop(uint32_t (&w)[8], uint32_t bits) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (bits & (1u << (2 * q))) w[q] = (w[q] & 0xFFFF0000u) | 0xFF80u;
-      if (bits & (2u << (2 * q))) w[q] = (w[q] & 0xFFFFu) | 0xFF800000u;
+    for (int q = 0; q < 8; ++q) {  // bytes 0-1 and 2-3 of the word, or of the replacement
+      const uint32_t two = bits >> (2 * q) & 3u;
+      w[q] = __byte_perm(w[q], 0xFF80FF80u, 0x3210u | (two & 1u) * 0x44u | (two & 2u) * 0x2200u);
     }
   }
 };
@@ -132,7 +128,6 @@ struct Unit<float> {
     w[2 * q] = __float_as_uint(lo);
     w[2 * q + 1] = __float_as_uint(hi);
   }
-  __device__ __forceinline__ static void set(uint32_t (&w)[8], int e, uint32_t raw) { w[e] = raw; }
   __device__ __forceinline__ static void drop(uint32_t (&w)[8], uint32_t bits) {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -172,7 +167,9 @@ struct ExpAgainst {
   }
 };
 
-// A thread's running maximum and sum of exp((v - m) / T).
+// A warp's running maximum m and each thread's sum of exp((v - m) / T).  The
+// maximum is the warp's, so raising it is one branch for all lanes and rare
+// after the first stages.
 struct OnlineSum {
   ExpAgainst x;
   f32x2 s0, s1;
@@ -180,8 +177,9 @@ struct OnlineSum {
     x.init(kNegInf, c);
     s0 = s1 = 0ull;
   }
-  // Takes units of maximum at most um.
+  // Before units of maximum um in this lane are added (all lanes call).
   __device__ __forceinline__ void raise(float um) {
+    um = warp_max(um);
     if (um > x.m) {
       const float f = x.m > kNegInf ? x.scale * rel_exp(x.m, um, x.c) : 0.f;
       x.init(um, x.c);
@@ -293,33 +291,26 @@ struct Run {
       }
     }
   }
+  // The trip count is the warp's: every lane of a warp visits the same stages.
   template <bool kPlain = false, typename F>
   __device__ __forceinline__ void stream(Stage& first, F visit) const {
-    for (int u = threadIdx.x; u < n; u += 2 * kStage * kStreamThreads) {
+    const int lane = threadIdx.x & 31;
+    for (int u = threadIdx.x; u - lane < n; u += 2 * kStage * kStreamThreads) {
       Stage next;
       const int u1 = u + kStage * kStreamThreads;
       prefetch<kPlain>(u1, next);
       visit(u, first);
+      if (u1 - lane >= n) break;
       prefetch<kPlain>(u1 + kStage * kStreamThreads, first);
-      if (u1 < n) visit(u1, next);
+      visit(u1, next);
     }
   }
 };
 
-// Block-wide maximum, and sum, of one value per thread (all threads call;
-// `red` holds kStreamWarps floats; the sum's order is fixed).
-__device__ __forceinline__ float block_max(float v, float* red) {
-  v = warp_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_max(red[threadIdx.x & (kStreamWarps - 1)]);
-}
-// (maximum, sum) of the block from each thread's, in every thread.
-__device__ __forceinline__ float2 block_lse(float m, float s, float c, float2* red) {
-  const float wm = warp_max(m);
-  const float ws = warp_reduce(m > kNegInf ? s * rel_exp(m, wm, c) : 0.f, OpAddF());
-  __syncthreads();
+// (maximum, sum) of the block from each warp's maximum and thread's sum, in
+// every thread; the sum's order is fixed.  `red` holds kStreamWarps pairs.
+__device__ __forceinline__ float2 block_lse(float wm, float s, float c, float2* red) {
+  const float ws = warp_reduce(s, OpAddF());
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(wm, ws);
   __syncthreads();
   const float2 r = red[threadIdx.x & (kStreamWarps - 1)];

@@ -4,11 +4,13 @@
 // A row over the CTAs of a cluster (ls_stream.cuh).  Per row:
 //  1. One pass: each thread's running maximum and sum of exponentials, and in
 //     shared memory the maximum of each stage (kStage units of a thread).
-//  2. In each of the w warps that hold units, the ceil(k / w)-th largest lane
-//     maximum: at least k entries of the run are at or above the least of
-//     these, so that is a lower bound of the k-th largest entry, and the
-//     largest such bound over the cluster's CTAs is one too.  (max, sum,
-//     bound) are exchanged over the cluster.
+//  2. A lower bound of the k-th largest entry.  In each of the w warps that hold
+//     units, the ceil(k / w)-th largest lane maximum: at least k entries of the
+//     run are at or above the least of these.  For large k that is far below
+//     the k-th entry (k = 256: the least of all lane maxima), so the bound is
+//     raised to about the k-th largest stage maximum (tighten).  The largest
+//     bound over the cluster's CTAs is one too: (max, sum, bound) are exchanged
+//     over the cluster.
 //  3. The stages whose maximum reaches the bound are read again (from L2) and
 //     their entries at or above it collected as 64-bit keys (value, then lower
 //     index).  More than kLocal of them -- ties in the main: constant rows,
@@ -22,6 +24,7 @@ namespace lsg {
 namespace ops {
 
 constexpr int kLocal = 512;      // keys that a CTA sends at most
+constexpr int kTakeMost = 8;      // lane maxima of a warp taken away one by one
 constexpr int kRankMost = 384;   // keys placed by counting; more are sorted
 static_assert(kLocal >= LS_MAX_TOP, "a run's own k best must fit");
 
@@ -159,6 +162,28 @@ __device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage
   __syncthreads();
 }
 
+// A value with at least k stage maxima at or above it and, where values allow,
+// at most k / 8 more (-inf where there are fewer than k): bisection of the
+// keys up to the run's maximum.
+__device__ __noinline__ float tighten(int units, const float* stage_max, int k, float most, TopShared& sh) {
+  uint32_t lo = f32_key(kNegInf), hi = f32_key(most) + 1u;
+  while (hi - lo > 1u) {
+    const uint32_t mid = lo + (hi - lo) / 2u;
+    const float t = f32_from_key(mid);
+    int n = 0;
+    for (int b = threadIdx.x, u = threadIdx.x; u < units; b += kStreamThreads, u += kStage * kStreamThreads)
+      n += stage_max[b] >= t;
+    n = block_count(n, sh.warp_n);
+    if (n >= k) {
+      lo = mid;
+      if (n <= k + k / 8) break;
+    } else {
+      hi = mid;
+    }
+  }
+  return f32_from_key(lo);
+}
+
 // Descending sort of n keys in shared memory (n a power of two).
 __device__ __noinline__ void sort_keys(unsigned long long* keys, int n) {
   for (int size = 2; size <= n; size <<= 1)
@@ -177,7 +202,7 @@ __device__ __noinline__ void sort_keys(unsigned long long* keys, int n) {
 }
 
 template <typename TIn>
-__global__ void __launch_bounds__(kStreamThreads, 2) top_kernel(const TopArgs a, int upc) {
+__global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a, int upc) {
   extern __shared__ uint4 dyn_smem[];  // stage maxima, then the keys sent to the first CTA
   __shared__ TopShared sh;
   float* stage_max = reinterpret_cast<float*>(dyn_smem);
@@ -214,6 +239,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) top_kernel(const TopArgs a,
   const float c = kLog2e / a.temperature;
   OnlineSum acc;
   acc.init(c);
+  float mine = kNegInf;  // this thread's maximum
   run.stream(first, [&](int u, typename Run<TIn>::Stage& v) {
     float um = kNegInf;
 #pragma unroll
@@ -223,27 +249,31 @@ __global__ void __launch_bounds__(kStreamThreads, 2) top_kernel(const TopArgs a,
     }
     // u = tid + stage * kStage * kStreamThreads
     stage_max[(u - tid) / kStage + tid] = um;
+    mine = fmaxf(mine, um);
     acc.raise(um);
 #pragma unroll
     for (int q = 0; q < kStage; ++q) acc.template add<TIn>(v[q]);
   });
   // the j-th largest lane maximum of each warp that holds units (ties ranked by lane)
-  const float mine = acc.x.m;
   const int warps = min(kStreamWarps, (run.n + 31) / 32);
   float bound = kPosInf;
   if (warp < warps) {
     const int j = (k + warps - 1) / warps;
-    int above = 0;
-#pragma unroll
-    for (int o = 0; o < 32; ++o) {
-      const float v = __shfl_sync(0xFFFFFFFFu, mine, o);
-      above += v > mine || (v == mine && o < lane);
+    if (j <= kTakeMost) {  // take the largest away j - 1 times
+      float left = mine;
+      for (int q = 1; q < j; ++q) {
+        const unsigned int at = __ballot_sync(0xFFFFFFFFu, left == warp_max(left));
+        if (lane == __ffs((int)at) - 1) left = kNegInf;
+      }
+      bound = warp_max(left);
+    } else {
+      bound = kNegInf;  // tighten() starts from nothing
     }
-    bound = j > 32 ? kNegInf : warp_max(above == j - 1 ? mine : kNegInf);
   }
   if (lane == 0) sh.redf[warp] = bound;
-  const float2 mine_ms = block_lse(mine, acc.sum(), c, sh.red);  // its barriers order redf too
+  const float2 mine_ms = block_lse(acc.x.m, acc.sum(), c, sh.red);  // its barriers order redf too
   bound = run.n > 0 ? warp_min(sh.redf[tid & (kStreamWarps - 1)]) : kNegInf;
+  if (run.n > 0 && (k + warps - 1) / warps > kTakeMost) bound = tighten(run.n, stage_max, k, mine_ms.x, sh);
   if (C > 1) {
     cluster_wait();  // every CTA of the cluster runs
     if (tid < C) {
