@@ -2,7 +2,7 @@
 biases and masks before sampling, top log-probs beside it, the distillation
 loss and its gradient."""
 import ctypes
-from contextlib import nullcontext
+import functools
 from dataclasses import dataclass
 
 from ._binding import LS_DTYPE_BF16, LS_DTYPE_F32, LS_OK, LSError, load_library
@@ -70,19 +70,8 @@ def row_ops_max_vocab(dtype):
     return int(_lib().ls_row_ops_max_vocab(int(dtype)))
 
 
-_HERE = nullcontext()
-
-
-def _where(stream):
-    """The raw stream that a call runs on, and a context in which outputs are
-    allocated on it (the current stream needs none)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), _HERE
-    return stream.cuda_stream, torch.cuda.stream(stream)
-
-
 def _matrix(logits):
-    """(pointer, dtype, rows, vocab, row stride) of a logits matrix."""
+    """(pointer, dtype, rows, vocab, row stride, raw current stream) of a logits matrix."""
     dt = _DTYPES.get(logits.dtype)
     if dt is None:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
@@ -94,14 +83,27 @@ def _matrix(logits):
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
     rows, vocab = logits.shape
-    return logits.data_ptr(), dt, rows, vocab, stride if rows > 1 else max(stride, vocab)
+    if rows <= 1 and stride < vocab:
+        stride = vocab
+    return logits.data_ptr(), dt, rows, vocab, stride, torch._C._cuda_getCurrentRawStream(logits.get_device())
+
+
+def _on_stream(f):
+    """A call's `stream` argument: the call runs with that stream current, so
+    that its outputs are allocated on it.  Without one nothing is entered."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        _need_torch()
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
 def _vec(t, dtype, what, n=None):
-    """The pointer of an optional contiguous device tensor of at least n entries."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+    """The pointer of a contiguous device tensor of at least n entries."""
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {str(dtype)[6:]}")
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
@@ -113,11 +115,11 @@ def _vec(t, dtype, what, n=None):
 
 
 def _f32(t, what, n=None):
-    return _vec(t, torch.float32, what, n)
+    return None if t is None else _vec(t, torch.float32, what, n)
 
 
 def _i32(t, what, n=None):
-    return _vec(t, torch.int32, what, n)
+    return None if t is None else _vec(t, torch.int32, what, n)
 
 
 def _like(t, logits, n, what):
@@ -152,7 +154,9 @@ class LogitsParams:
     bias_values: object = None
 
     def __post_init__(self):
-        object.__setattr__(self, "_struct", self._marshal())
+        struct = self._marshal()  # its pointers stay valid with the tensors that the fields hold
+        object.__setattr__(self, "_struct", struct)
+        object.__setattr__(self, "_ref", ctypes.byref(struct))
 
     def _marshal(self):
         _need_torch()
@@ -221,143 +225,160 @@ class LogitsParams:
                             dev(values, np.float32))
 
 
+@_on_stream
 def process_logits(logits, n=None, params=None, gather_indices=None, token_to_request_index=None, row_lens=None,
-                   allowed_mask=None, mask_index=None, out=None, error_word=None, stream=None):
+                   allowed_mask=None, mask_index=None, out=None, error_word=None):
     """ls_process_logits: returns out ([n, vocab] of the logits' type).  out may
     be the logits themselves (no gather_indices).  allowed_mask int32
-    [mask_rows, >= ceil(vocab / 32)]."""
-    lib = _lib()
-    ptr, dt, rows, V, stride = _matrix(logits)
+    [mask_rows, >= ceil(vocab / 32)].  `stream`: the current one by default."""
+    lib = _ready or _lib()
+    ptr, dt, rows, V, stride, raw = _matrix(logits)
     if n is None:
         n = len(gather_indices) if gather_indices is not None else rows
-    n = int(n)
     mask_ptr, mask_rows, mask_stride = None, 0, 0
     if allowed_mask is not None:
-        if allowed_mask.dim() != 2 or allowed_mask.stride(1) != 1 or allowed_mask.dtype != torch.int32:
+        if allowed_mask.dim() != 2 or allowed_mask.stride(1) != 1 or allowed_mask.dtype is not torch.int32:
             raise ValueError("allowed_mask must be int32 [mask_rows, words] with contiguous rows")
         if not allowed_mask.is_cuda:
             raise ValueError("expected a CUDA tensor")
-        mask_ptr, mask_rows = allowed_mask.data_ptr(), allowed_mask.shape[0]
-        mask_stride = allowed_mask.stride(0) if mask_rows > 1 else allowed_mask.shape[1]
-    s, ctx = _where(stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        mask_ptr, (mask_rows, words) = allowed_mask.data_ptr(), allowed_mask.shape
+        mask_stride = allowed_mask.stride(0) if mask_rows > 1 else words
+    if out is None:
+        out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        out_stride = V
+    else:
         out_stride = _like(out, logits, n, "out")
-        st = lib.ls_process_logits(
-            ptr, dt, rows, V, stride, n, _i32(gather_indices, "gather_indices", n),
-            _i32(token_to_request_index, "token_to_request_index", n),
-            None if params is None else ctypes.byref(params._struct), _i32(row_lens, "row_lens", n), mask_ptr,
-            mask_rows, mask_stride, _i32(mask_index, "mask_index", n), out.data_ptr(), out_stride,
-            _i32(error_word, "error_word"), s)
+    st = lib.ls_process_logits(
+        ptr, dt, rows, V, stride, n, _i32(gather_indices, "gather_indices", n),
+        _i32(token_to_request_index, "token_to_request_index", n), None if params is None else params._ref,
+        _i32(row_lens, "row_lens", n), mask_ptr, mask_rows, mask_stride, _i32(mask_index, "mask_index", n),
+        out.data_ptr(), out_stride, _i32(error_word, "error_word"), raw)
     if st != LS_OK:
         raise LSError(st, "ls_process_logits")
     return out
 
 
+@_on_stream
 def top_log_probs(logits, k, n=None, temperature=1.0, gather_indices=None, out_ids=None, out_log_probs=None,
-                  out_lse=None, error_word=None, stream=None):
-    """ls_top_log_probs: returns (ids int32 [n, k], log_probs float32 [n, k], lse float32 [n])."""
-    lib = _lib()
-    ptr, dt, rows, V, stride = _matrix(logits)
+                  out_lse=None, error_word=None):
+    """ls_top_log_probs: returns (ids int32 [n, k], log_probs float32 [n, k], lse
+    float32 [n]).  `stream`: the current one by default."""
+    lib = _ready or _lib()
+    ptr, dt, rows, V, stride, raw = _matrix(logits)
     if n is None:
         n = len(gather_indices) if gather_indices is not None else rows
-    n, k = int(n), int(k)
-    s, ctx = _where(stream)
-    with ctx:
-        if out_ids is None:
-            out_ids = torch.empty((n, k), dtype=torch.int32, device=logits.device)
-        if out_log_probs is None:
-            out_log_probs = torch.empty((n, k), dtype=torch.float32, device=logits.device)
-        if out_lse is None:
-            out_lse = torch.empty(n, dtype=torch.float32, device=logits.device)
-        st = lib.ls_top_log_probs(ptr, dt, rows, V, stride, n, _i32(gather_indices, "gather_indices", n), k,
-                                  float(temperature), _i32(out_ids, "out_ids", n * k),
-                                  _f32(out_log_probs, "out_log_probs", n * k), _f32(out_lse, "out_lse", n),
-                                  _i32(error_word, "error_word"), s)
+    dev = logits.device
+    if out_ids is None:
+        out_ids = torch.empty((n, k), dtype=torch.int32, device=dev)
+    else:
+        _i32(out_ids, "out_ids", n * k)
+    if out_log_probs is None:
+        out_log_probs = torch.empty((n, k), dtype=torch.float32, device=dev)
+    else:
+        _f32(out_log_probs, "out_log_probs", n * k)
+    if out_lse is None:
+        out_lse = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _f32(out_lse, "out_lse", n)
+    st = lib.ls_top_log_probs(ptr, dt, rows, V, stride, n, _i32(gather_indices, "gather_indices", n), k, temperature,
+                              out_ids.data_ptr(), out_log_probs.data_ptr(), out_lse.data_ptr(),
+                              _i32(error_word, "error_word"), raw)
     if st != LS_OK:
         raise LSError(st, f"ls_top_log_probs (k = {k}; at most {MAX_TOP})")
     return out_ids, out_log_probs, out_lse
 
 
 def _teacher(ids, log_probs, n):
-    if ids.dim() != 2 or ids.shape != log_probs.shape or ids.shape[0] != n:
+    k = ids.shape[-1]
+    if ids.shape != (n, k) or log_probs.shape != (n, k):
         raise ValueError(f"teacher_ids and teacher_log_probs must both be [{n}, k]")
-    if ids.dtype != torch.int32 or log_probs.dtype != torch.float32:
+    if ids.dtype is not torch.int32 or log_probs.dtype is not torch.float32:
         raise TypeError("teacher_ids must be int32, teacher_log_probs float32")
-    if ids.stride(1) != 1 or log_probs.stride(1) != 1 or (n > 1 and ids.stride(0) != log_probs.stride(0)):
-        raise ValueError("teacher_ids and teacher_log_probs must have contiguous rows and one row stride")
+    stride, inner = ids.stride()
+    if n <= 1:
+        stride = k
+    elif log_probs.stride(0) != stride:
+        raise ValueError("teacher_ids and teacher_log_probs must have one row stride")
+    if k > 1 and (inner != 1 or log_probs.stride(1) != 1):
+        raise ValueError("teacher_ids and teacher_log_probs must have contiguous rows")
     if not (ids.is_cuda and log_probs.is_cuda):
         raise ValueError("expected a CUDA tensor")
-    k = ids.shape[1]
-    return _Teacher(ids.data_ptr(), log_probs.data_ptr(), ids.stride(0) if n > 1 else k, k)
+    return ctypes.byref(_Teacher(ids.data_ptr(), log_probs.data_ptr(), stride, k))
 
 
 def _tail(tail):
-    if tail not in TAILS:
+    code = TAILS.get(tail)
+    if code is None:
         raise ValueError(f"tail must be one of {sorted(TAILS)}")
-    return TAILS[tail]
+    return code
 
 
+@_on_stream
 def distill_loss(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="bucket", weights=None, out=None,
-                 out_stats=None, error_word=None, stream=None):
+                 out_stats=None, error_word=None):
     """ls_distill_loss: returns (loss float32 [n], stats float32 [n, 8]); stats
-    goes to distill_loss_backward."""
-    lib = _lib()
-    ptr, dt, n, V, stride = _matrix(logits)
-    t = _teacher(teacher_ids, teacher_log_probs, n)
-    s, ctx = _where(stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(n, dtype=torch.float32, device=logits.device)
-        if out_stats is None:
-            out_stats = torch.empty((n, DISTILL_STATS), dtype=torch.float32, device=logits.device)
-        st = lib.ls_distill_loss(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
-                                 _f32(weights, "weights", n), _f32(out, "out", n),
-                                 _f32(out_stats, "out_stats", DISTILL_STATS * n), _i32(error_word, "error_word"), s)
+    goes to distill_loss_backward.  `stream`: the current one by default."""
+    lib = _ready or _lib()
+    ptr, dt, n, V, stride, raw = _matrix(logits)
+    teacher = _teacher(teacher_ids, teacher_log_probs, n)
+    if out is None:
+        out = torch.empty(n, dtype=torch.float32, device=logits.device)
+    else:
+        _f32(out, "out", n)
+    if out_stats is None:
+        out_stats = torch.empty((n, DISTILL_STATS), dtype=torch.float32, device=logits.device)
+    else:
+        _f32(out_stats, "out_stats", DISTILL_STATS * n)
+    st = lib.ls_distill_loss(ptr, dt, V, stride, n, teacher, temperature, _tail(tail), _f32(weights, "weights", n),
+                             out.data_ptr(), out_stats.data_ptr(), _i32(error_word, "error_word"), raw)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss")
     return out, out_stats
 
 
+@_on_stream
 def distill_loss_backward(logits, teacher_ids, teacher_log_probs, stats, grad_loss=None, temperature=1.0,
-                          tail="bucket", weights=None, out=None, stream=None):
+                          tail="bucket", weights=None, out=None):
     """ls_distill_loss_backward: returns out, the gradient ([n, vocab] of the
-    logits' type; out may be the logits themselves)."""
-    lib = _lib()
-    ptr, dt, n, V, stride = _matrix(logits)
-    t = _teacher(teacher_ids, teacher_log_probs, n)
-    s, ctx = _where(stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+    logits' type; out may be the logits themselves).  `stream`: the current one
+    by default."""
+    lib = _ready or _lib()
+    ptr, dt, n, V, stride, raw = _matrix(logits)
+    teacher = _teacher(teacher_ids, teacher_log_probs, n)
+    if out is None:
+        out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        out_stride = V
+    else:
         out_stride = _like(out, logits, n, "out")
-        st = lib.ls_distill_loss_backward(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
-                                          _f32(weights, "weights", n), _f32(stats, "stats", DISTILL_STATS * n),
-                                          _f32(grad_loss, "grad_loss", n), out.data_ptr(), out_stride, s)
+    st = lib.ls_distill_loss_backward(ptr, dt, V, stride, n, teacher, temperature, _tail(tail),
+                                      _f32(weights, "weights", n), _f32(stats, "stats", DISTILL_STATS * n),
+                                      _f32(grad_loss, "grad_loss", n), out.data_ptr(), out_stride, raw)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss_backward")
     return out
 
 
+@_on_stream
 def distill_loss_grad(logits, teacher_ids, teacher_log_probs, temperature=1.0, tail="bucket", weights=None,
-                      out_loss=None, out_grad=None, error_word=None, stream=None):
+                      out_loss=None, out_grad=None, error_word=None):
     """ls_distill_loss_grad: returns (loss float32 [n], gradient [n, vocab] of
-    the logits' type) from one read of the logits; out_grad may be the logits
-    themselves."""
-    lib = _lib()
-    ptr, dt, n, V, stride = _matrix(logits)
-    t = _teacher(teacher_ids, teacher_log_probs, n)
-    s, ctx = _where(stream)
-    with ctx:
-        if out_loss is None:
-            out_loss = torch.empty(n, dtype=torch.float32, device=logits.device)
-        if out_grad is None:
-            out_grad = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+    the logits' type) from one call; out_grad may be the logits themselves.
+    `stream`: the current one by default."""
+    lib = _ready or _lib()
+    ptr, dt, n, V, stride, raw = _matrix(logits)
+    teacher = _teacher(teacher_ids, teacher_log_probs, n)
+    if out_loss is None:
+        out_loss = torch.empty(n, dtype=torch.float32, device=logits.device)
+    else:
+        _f32(out_loss, "out_loss", n)
+    if out_grad is None:
+        out_grad = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        out_stride = V
+    else:
         out_stride = _like(out_grad, logits, n, "out_grad")
-        st = lib.ls_distill_loss_grad(ptr, dt, V, stride, n, ctypes.byref(t), float(temperature), _tail(tail),
-                                      _f32(weights, "weights", n), _f32(out_loss, "out_loss", n),
-                                      out_grad.data_ptr(), out_stride, _i32(error_word, "error_word"), s)
+    st = lib.ls_distill_loss_grad(ptr, dt, V, stride, n, teacher, temperature, _tail(tail),
+                                  _f32(weights, "weights", n), out_loss.data_ptr(), out_grad.data_ptr(), out_stride,
+                                  _i32(error_word, "error_word"), raw)
     if st != LS_OK:
         raise LSError(st, "ls_distill_loss_grad")
     return out_loss, out_grad

@@ -5,16 +5,16 @@
 // loaded to registers at the start and written at the end (four, or one where
 // that leaves SMs without a CTA).  In between, the few
 // entries that the history or a bias touches are worked out on the side:
-//  1. The CTA reads the request's history (every tile of the row does: at the
-//     lengths that occur it is small against the row) and keeps the ids of its
-//     own tile in a table with one slot per entry: bit 0 says that the id
-//     occurs, the bits above count its occurrences past the prompt.  The first
-//     occurrence of an id sets the entry's touched bit and lists the entry.
-//  2. Each unit takes -inf where the mask says so and is written: entries that
+//  1. Each unit takes -inf where the mask says so and is written: entries that
 //     nothing touches keep their bits.
+//  2. Meanwhile the request's history arrives (every tile of the row reads all
+//     of it: at the lengths that occur it is small against the row).  The ids of
+//     the CTA's own tile go to a table with one slot per entry: bit 0 says that
+//     the id occurs, the bits above count its occurrences past the prompt.  An
+//     id's first occurrence lists the entry.
 //  3. One thread per listed entry, and one per bias, reads the logit and the
 //     slot, works out the new value in fp32 and writes it over the copy, unless
-//     the mask forbids the id.  (In place the logit is still there: step 2
+//     the mask forbids the id.  (In place the logit is still there: step 1
 //     wrote the same bits, or -inf where the mask forbids it.)
 // A slot of 16 bits holds the counts of a history of fewer than 2^15 ids.
 #include "ls_stream.cuh"
@@ -24,7 +24,8 @@ namespace ops {
 
 constexpr int kProcThreads = 256;
 constexpr int kHistoryBatch = 8;  // history ids of a thread in flight
-constexpr int kListed = 2048;     // touched entries listed; past it step 2 walks the touched bits
+constexpr int kSettleBatch = 4;   // touched entries of a thread in flight
+constexpr int kListed = 4096;     // touched entries listed; past it step 3 walks the table
 
 struct ProcessArgs {
   const void* logits;
@@ -42,16 +43,15 @@ struct ProcessArgs {
   int32_t* error_word;
 };
 
-// A table slot in shared memory: an atomic update of 16-bit slots works on the
-// 32-bit word that holds two (no carry crosses: see the widths above).
+// Marks a table slot and returns whether it was empty.  An atomic update of
+// 16-bit slots works on the 32-bit word that holds two (no carry crosses: see
+// the widths above).
 template <typename Slot>
-__device__ __forceinline__ void mark(Slot* table, int e, bool prompt) {
+__device__ __forceinline__ bool mark(Slot* table, int e, bool prompt) {
   uint32_t* word = reinterpret_cast<uint32_t*>(table) + (sizeof(Slot) == 2 ? e >> 1 : e);
   const int shift = sizeof(Slot) == 2 ? (e & 1) * 16 : 0;
-  if (prompt)
-    atomicOr(word, 1u << shift);
-  else
-    atomicAdd(word, 2u << shift);
+  const uint32_t old = prompt ? atomicOr(word, 1u << shift) : atomicAdd(word, 2u << shift);
+  return (Slot)(old >> shift) == 0;
 }
 
 // Bits [j, j + N) of a mask row, 1 outside [0, vocab) (j may lie before the row).
@@ -79,9 +79,8 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   constexpr int kTileUnits = kProcThreads * kUnits, kEntries = kTileUnits * kN;
   extern __shared__ uint4 dyn_smem[];
   Slot* table = reinterpret_cast<Slot*>(dyn_smem);
-  uint32_t* touched = reinterpret_cast<uint32_t*>(table + kEntries);  // a bit per entry
-  uint32_t* biased = touched + kEntries / 32;                         // entries of a bias
-  uint32_t* settled = biased + kEntries / 32;                         // those whose bias is applied
+  uint32_t* biased = reinterpret_cast<uint32_t*>(table + kEntries);  // a bit per entry: those of a bias
+  uint32_t* settled = biased + kEntries / 32;                        // those whose bias is applied
   __shared__ uint16_t list[kListed];
   __shared__ int listed;
   const int tid = threadIdx.x;
@@ -137,41 +136,27 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   }
   const bool any = L > 0 || b_lo < b_hi;  // the same in every thread
   const uint32_t* mask = mrow >= 0 ? a.mask + mrow * a.mask_stride : nullptr;
+  // the first ids of the history, and a bias, on their way while the units are written
+  int32_t held[kHistoryBatch];
+  auto fetch = [&](int32_t at) {
+#pragma unroll
+    for (int q = 0; q < kHistoryBatch; ++q) {
+      const int32_t t = at + q * kProcThreads;
+      held[q] = t < L ? history[t] : -1;
+    }
+  };
+  auto place = [&](int32_t id) { return id >= 0 && id < run.V ? run.place(id) : -1; };
+  int bias_e = -1;
+  float bias_v = 0.f;
   if (any) {
-    constexpr int kWords = (kEntries * (int)sizeof(Slot) + 3 * (kEntries / 8)) / 16;  // table and bits
+    fetch(tid);
+    if (b_lo + tid < b_hi) {
+      bias_e = place(a.p.bias_ids[b_lo + tid]);
+      bias_v = a.p.bias_values[b_lo + tid];
+    }
+    constexpr int kWords = (kEntries * (int)sizeof(Slot) + 2 * (kEntries / 8)) / 16;  // table and bits
     for (int q = tid; q < kWords; q += kProcThreads) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) listed = 0;
-    int32_t held[kHistoryBatch];
-    auto fetch = [&](int32_t at) {
-#pragma unroll
-      for (int q = 0; q < kHistoryBatch; ++q) {
-        const int32_t t = at + q * kProcThreads;
-        held[q] = t < L ? history[t] : -1;
-      }
-    };
-    fetch(tid);
-    __syncthreads();
-    for (int32_t at = tid; at - tid < L; at += kHistoryBatch * kProcThreads) {
-      if (at != tid) fetch(at);
-#pragma unroll
-      for (int q = 0; q < kHistoryBatch; ++q) {
-        const int e = held[q] >= 0 && held[q] < run.V ? run.place(held[q]) : -1;
-        if (e >= 0) {
-          mark(table, e, at + q * kProcThreads < prompt);
-          const uint32_t bit = 1u << (e & 31);
-          if (!(atomicOr(&touched[e >> 5], bit) & bit)) {
-            const int n = atomicAdd(&listed, 1);
-            if (n < kListed) list[n] = (uint16_t)e;
-          }
-        }
-      }
-    }
-    for (int32_t q = b_lo + tid; q < b_hi; q += kProcThreads) {
-      const int32_t id = a.p.bias_ids[q];
-      const int e = id >= 0 && id < run.V ? run.place(id) : -1;
-      if (e >= 0) atomicOr(&biased[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
   }
 #pragma unroll
   for (int q = 0; q < kUnits; ++q) {
@@ -184,38 +169,72 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
     }
     run.store(out, same, u, v[q]);
   }
-  if (any) {
-    __syncthreads();  // the unit's copies are written before their touched entries are
-    // the new value of entry e (called by one thread per entry)
-    auto settle = [&](int e, float b, bool has_bias) {
-      const int64_t j = run.j0 + e;
-      if (mask && !(__ldg(mask + (j >> 5)) >> (j & 31) & 1u)) return;
-      const uint32_t m = table[e];
-      const float x = E::get(run.row[j]);
-      const float n = (float)(m >> 1);
-      float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
-      y = __fsub_rn(y, __fmul_rn(freq, n));
-      if (n > 0.f) y -= pres;
-      if (has_bias) y += b;
-      out[j] = E::put(guard(y));
-    };
-    const int n_listed = listed;
-    if (n_listed <= kListed) {
-      for (int q = tid; q < n_listed; q += kProcThreads) {
-        const int e = list[q];
-        if (!(biased[e >> 5] >> (e & 31) & 1u)) settle(e, 0.f, false);
+  if (!any) return;
+  __syncthreads();
+  for (int32_t at = tid; at - tid < L; at += kHistoryBatch * kProcThreads) {
+    if (at != tid) fetch(at);
+#pragma unroll
+    for (int q = 0; q < kHistoryBatch; ++q) {
+      const int e = place(held[q]);
+      const bool first = e >= 0 && mark(table, e, at + q * kProcThreads < prompt);
+      const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
+      if (firsts == 0u) continue;
+      int n = 0;
+      if ((tid & 31) == 0) n = atomicAdd(&listed, __popc(firsts));
+      n = __shfl_sync(0xFFFFFFFFu, n, 0) + __popc(firsts & ((1u << (tid & 31)) - 1u));
+      if (first && n < kListed) list[n] = (uint16_t)e;
+    }
+  }
+  if (bias_e >= 0) atomicOr(&biased[bias_e >> 5], 1u << (bias_e & 31));
+  for (int32_t q = b_lo + tid + kProcThreads; q < b_hi; q += kProcThreads) {
+    const int e = place(a.p.bias_ids[q]);
+    if (e >= 0) atomicOr(&biased[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();  // also: the copies are written before their touched entries are
+  auto allowed = [&](int e) {
+    const int64_t j = run.j0 + e;
+    return !mask || (__ldg(mask + (j >> 5)) >> (j & 31) & 1u) != 0u;
+  };
+  // the new value of entry e from its logit (called by one thread per entry)
+  auto settle = [&](int e, float x, float b, bool has_bias) {
+    const uint32_t m = table[e];
+    const float n = (float)(m >> 1);
+    float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
+    y = __fsub_rn(y, __fmul_rn(freq, n));
+    if (n > 0.f) y -= pres;
+    if (has_bias) y += b;
+    out[run.j0 + e] = E::put(guard(y));
+  };
+  auto logit = [&](int e) { return E::get(run.row[run.j0 + e]); };
+  auto settle_bias = [&](int e, float b) {
+    const uint32_t bit = 1u << (e & 31);
+    if (!(atomicOr(&settled[e >> 5], bit) & bit) && allowed(e)) settle(e, logit(e), b, true);
+  };
+  if (bias_e >= 0) settle_bias(bias_e, bias_v);
+  for (int32_t q = b_lo + tid + kProcThreads; q < b_hi; q += kProcThreads) {
+    const int e = place(a.p.bias_ids[q]);
+    if (e >= 0) settle_bias(e, a.p.bias_values[q]);
+  }
+  const int n_listed = listed;
+  if (n_listed <= kListed) {
+    for (int q = tid; q < n_listed; q += kSettleBatch * kProcThreads) {
+      int e[kSettleBatch];
+      float x[kSettleBatch];
+#pragma unroll
+      for (int k = 0; k < kSettleBatch; ++k) {
+        e[k] = -1;
+        if (q + k * kProcThreads < n_listed) e[k] = list[q + k * kProcThreads];
+        if (e[k] >= 0 && (biased[e[k] >> 5] >> (e[k] & 31) & 1u)) e[k] = -1;
+        if (e[k] >= 0) x[k] = logit(e[k]);
+        if (e[k] >= 0 && !allowed(e[k])) e[k] = -1;
       }
-    } else {
-      for (int q = tid; q < kEntries / 32; q += kProcThreads)
-        for (uint32_t w = touched[q] & ~biased[q]; w; w &= w - 1) settle(q * 32 + __ffs((int)w) - 1, 0.f, false);
+#pragma unroll
+      for (int k = 0; k < kSettleBatch; ++k)
+        if (e[k] >= 0) settle(e[k], x[k], 0.f, false);
     }
-    for (int32_t q = b_lo + tid; q < b_hi; q += kProcThreads) {
-      const int32_t id = a.p.bias_ids[q];
-      const int e = id >= 0 && id < run.V ? run.place(id) : -1;
-      if (e < 0) continue;
-      const uint32_t bit = 1u << (e & 31);
-      if (!(atomicOr(&settled[e >> 5], bit) & bit)) settle(e, a.p.bias_values[q], true);
-    }
+  } else {
+    for (int e = tid; e < kEntries; e += kProcThreads)
+      if (table[e] != 0 && !(biased[e >> 5] >> (e & 31) & 1u) && allowed(e)) settle(e, logit(e), 0.f, false);
   }
 }
 
@@ -226,7 +245,7 @@ static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStr
   const int64_t tiles = (row_units(a.vocab, dtype) + kTileUnits - 1) / kTileUnits;
   if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   const bool side = a.has_params && (a.p.tokens || a.p.bias_offsets);
-  const size_t smem = side ? (size_t)kEntries * sizeof(Slot) + 3 * (kEntries / 8) : 0;
+  const size_t smem = side ? (size_t)kEntries * sizeof(Slot) + 2 * (kEntries / 8) : 0;
   if (!open_limits(process_kernel<TIn, Slot, kUnits>, done)) return LS_ERR_CUDA;
   process_kernel<TIn, Slot, kUnits><<<dim3((unsigned)(tiles * n)), dim3(kProcThreads), smem, st>>>(a, (int)tiles);
   return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;

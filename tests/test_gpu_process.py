@@ -284,6 +284,29 @@ def test_one_id_repeated_through_a_long_history(cap):
     _compare(out.cpu().numpy(), x, [_ref(c, 0, 0, cap)], "f32")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cap", [3000, 9000, 30000, 33000])
+def test_many_distinct_ids(dtype, cap):
+    """Histories of mostly distinct ids in a batch large enough that a CTA takes a long run of the row."""
+    import logits_sampling_gb300 as ls
+    rng = np.random.default_rng(cap)
+    n, V = 640, 33000
+    x = R.to_dtype(rng.standard_normal((1, V)), dtype)
+    tokens = np.stack([rng.permutation(V)[:cap] for _ in range(2)]).astype(np.int32)
+    bias = {int(j): float(np.float32(v)) for j, v in zip(rng.permutation(V)[:300], rng.standard_normal(300))}
+    c = {"x": x, "tokens": tokens, "seq": np.array([cap, cap // 2]), "prompt": np.array([100, cap]), "rho": [1.5, 1.25],
+         "pres": [0.1, 0.2], "freq": [0.01, 0.3], "biases": [bias, {}]}
+    t2r = np.arange(n) % 2
+    allowed = rng.random((1, V)) < 0.8
+    out = ls.process_logits(R.device_matrix(x, dtype), n, _params(c), gather_indices=_i32(np.zeros(n)),
+                            token_to_request_index=_i32(t2r), allowed_mask=_i32(R.pack_mask(allowed)),
+                            mask_index=_i32(np.where(np.arange(n) < 4, 0, -1)))
+    got = out[[0, 1, n - 2, n - 1]].float().cpu().numpy()
+    refs = [_ref(c, 0, r, c["seq"][r], m) for m in (allowed[0], None) for r in (0, 1)]
+    _compare(got, np.repeat(x, 4, 0), refs, dtype)
+    assert bool((out[4:] == out[4:6].repeat(n // 2 - 2, 1)).all())
+
+
 def test_offsets_past_32_bits():
     """A logits matrix of more than 2^32 entries: its last rows, gathered."""
     import torch
