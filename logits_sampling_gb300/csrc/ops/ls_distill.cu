@@ -3,8 +3,9 @@
 // ls_distill_loss_grad).
 //
 // Loss, and loss with gradient (distill_kernel): a row over the CTAs of a
-// cluster (ls_stream.cuh).  A bitmap in shared memory marks the teacher's ids;
-// the running maximum and sum skip them, so that the mass outside them (q_r) is
+// cluster (ls_stream.cuh).  A bit per unit in shared memory marks those that hold
+// one of the teacher's ids, and a small hash table says which of their entries
+// do; the running maximum and sum skip them, so that the mass outside them (q_r) is
 // a sum of its own rather than a difference of two.  With the entries outside
 // of maximum M_r and e_j = exp((x_j - M_r) / T), the gradient outside the ids
 // is one multiple of e_j:
@@ -24,7 +25,6 @@ namespace ops {
 struct alignas(16) RowStats {
   float M, alpha, Mr, kappa, scale, pad[3];
 };
-static_assert(kStreamThreads >= LS_MAX_TOP, "a thread per teacher entry");
 static_assert(sizeof(RowStats) == sizeof(float) * LS_DISTILL_STATS, "the header's size of a row's stats");
 
 struct DistillArgs {
@@ -51,47 +51,95 @@ constexpr float kLeastMass = 7.8886e-31f;  // 2^-100
 template <typename TIn>
 __device__ __forceinline__ void unit_grad(uint32_t (&w)[8], const ExpAgainst& x, float coef) {
   constexpr int kN = Unit<TIn>::kN;
-  Unit<TIn>::clean(w);
+  const f32x2 c2 = pack2(coef, coef);
   uint32_t o[8];
+  if (x.fast) {
 #pragma unroll
-  for (int q = 0; q < kN / 2; ++q) {
-    float a, b;
-    unpack2(mul2(x.fast ? x.pair_fast(Unit<TIn>::pair(w, q)) : x.pair_slow(Unit<TIn>::pair(w, q)), pack2(coef, coef)), a,
-            b);
-    Unit<TIn>::set_pair(o, q, a, b);
+    for (int q = 0; q < kN / 2; ++q) {
+      float a, b;
+      unpack2(mul2(x.pair_fast(Unit<TIn>::pair(w, q)), c2), a, b);
+      Unit<TIn>::set_pair(o, q, a, b);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kN / 2; ++q) {
+      float a, b;
+      unpack2(mul2(x.pair_slow(Unit<TIn>::pair(w, q)), c2), a, b);
+      Unit<TIn>::set_pair(o, q, a, b);
+    }
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) w[q] = o[q];
 }
 
+constexpr int kHeld = 2 * LS_MAX_TOP;               // slots of the table of units that hold one
+static_assert((kHeld & (kHeld - 1)) == 0, "a power of two");
+
 struct DistillShared {
   float2 ms[kMaxCluster];  // each CTA's maximum and sum over the entries outside the ids
-  float2 red[kStreamWarps];
+  float2 red[8];
   float x[LS_MAX_TOP];     // the student's logits at the ids (-inf where there is none)
   float p[LS_MAX_TOP];
   float lp[LS_MAX_TOP];
+  int unit[kHeld];         // a unit of the run, -1: free
+  uint32_t entries[kHeld]; // a bit for each of its entries that is one of the ids
   RowStats st;
 };
 
-template <typename TIn, bool kGrad>
-__global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const DistillArgs a, int upc) {
+__device__ __forceinline__ int held_home(int u) { return (int)(((uint32_t)u * 0x9E3779B1u) >> 16) & (kHeld - 1); }
+// Notes that entry e of unit u is one of the ids (never more than half full).
+__device__ __forceinline__ void hold(DistillShared& sh, int u, int e) {
+  int at = held_home(u);
+  for (int t = 0; t < kHeld; ++t) {
+    const int was = atomicCAS(&sh.unit[at], -1, u);
+    if (was == -1 || was == u) {
+      atomicOr(&sh.entries[at], 1u << e);
+      return;
+    }
+    at = (at + 1) & (kHeld - 1);
+  }
+}
+__device__ __forceinline__ uint32_t held_entries(const DistillShared& sh, int u) {
+  int at = held_home(u);
+  for (int t = 0; t < kHeld; ++t) {
+    const int has = sh.unit[at];
+    if (has == u) return sh.entries[at];
+    if (has == -1) return 0u;
+    at = (at + 1) & (kHeld - 1);
+  }
+  return 0u;
+}
+
+template <typename TIn, bool kGrad, int T>
+__global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs a, int upc) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
   constexpr int kN = Unit<TIn>::kN;
+  constexpr int kOwn = LS_MAX_TOP / T;  // teacher entries per thread
+  static_assert(kOwn * T == LS_MAX_TOP, "");
   extern __shared__ uint4 dyn_smem[];
   __shared__ DistillShared sh;
   const int tid = threadIdx.x, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t i = blockIdx.x / (unsigned)C;
-  Run<TIn> run;
+  Run<TIn, T> run;
   run.init(a.logits, i, a.row_stride, a.vocab, upc, rank);
   Raw* grad = kGrad ? static_cast<Raw*>(a.out_grad) + i * a.grad_stride : nullptr;
+  // the teacher's entries of this thread, beside the weight that decides whether they matter
   const float w = a.weights ? a.weights[i] : 1.f;
+  int id[kOwn];
+  float t[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int k = tid + q * T;
+    id[q] = k < a.t.k ? a.t.ids[i * a.t.stride + k] : -1;
+    t[q] = k < a.t.k ? a.t.log_probs[i * a.t.stride + k] : kNegInf;
+  }
   if (w == 0.f) {  // every CTA of the row leaves here, before any cluster barrier
     if (kGrad) {
       const bool same = run.aligned_with(grad);
       uint32_t z[8] = {};
-      for (int u = tid; u < run.n; u += kStreamThreads) run.store(grad, same, u, z);
+      for (int u = tid; u < run.n; u += T) run.store(grad, same, u, z);
     }
     if (tid == 0 && rank == 0) {
       a.out_loss[i] = 0.f;
@@ -99,62 +147,78 @@ __global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const Distil
     }
     return;
   }
-  typename Run<TIn>::Stage first;
+  typename Run<TIn, T>::Stage first;
   run.template prefetch<kGrad>(tid, first);
   if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
-  // one bit per place of the run
+  // a bit per unit of the run
   uint32_t* bits = reinterpret_cast<uint32_t*>(dyn_smem);
-  for (int q = tid; q < (run.n * kN + 127) / 128; q += kStreamThreads) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
-  // the teacher's entry of this thread
-  int id = -1;
-  float x = kNegInf, p = 0.f;
-  if (tid < LS_MAX_TOP) {
-    float t = kNegInf;
-    if (tid < a.t.k) {
-      id = a.t.ids[i * a.t.stride + tid];
-      t = a.t.log_probs[i * a.t.stride + tid];
-      if (id < 0 || (int64_t)id >= a.vocab || !(t > kNegInf)) id = -1;
-      if (id >= 0) {
-        p = expf(t);
-        x = guard(E::get(run.row[id]));
-      }
-    }
-    sh.lp[tid] = t;
-    sh.p[tid] = p;
-    sh.x[tid] = x;
+  for (int q = tid; q < (run.n + 127) / 128; q += T) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int q = 0; q < kHeld / T; ++q) {
+    sh.unit[tid + q * T] = -1;
+    sh.entries[tid + q * T] = 0u;
   }
   __syncthreads();
-  const int mine = id >= 0 ? run.place(id) : -1;
-  if (mine >= 0) atomicOr(&bits[mine >> 5], 1u << (mine & 31));
+  // the student's logits at the ids, on their way while the run streams
+  typename E::Raw x[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    if (id[q] < 0 || (int64_t)id[q] >= a.vocab || !(t[q] > kNegInf)) id[q] = -1;
+    x[q] = id[q] >= 0 ? run.row[id[q]] : E::neg_inf();
+    const int place = id[q] >= 0 ? run.place(id[q]) : -1;
+    if (place >= 0) {
+      atomicOr(&bits[place / kN >> 5], 1u << (place / kN & 31));
+      hold(sh, place / kN, place % kN);
+    }
+  }
   __syncthreads();
   const float c = kLog2e / a.temperature;
   OnlineSum acc;
-  acc.init(c);
-  run.template stream<kGrad>(first, [&](int u, typename Run<TIn>::Stage& v) {
-    float um = kNegInf;
+  // NaN logits: the first pass takes them as they come, and a run whose sum is
+  // NaN is taken again with each of them read as -inf.
+  auto sum_run = [&](bool dirty) {
+    acc.init(c);
+    run.template stream<kGrad>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
+      float um = kNegInf;
 #pragma unroll
-    for (int k = 0; k < kStage; ++k) {
-      const int uk = min(u + k * kStreamThreads, run.n - 1);
-      const uint32_t listed = kN == 16 ? reinterpret_cast<const uint16_t*>(bits)[uk] : reinterpret_cast<const uint8_t*>(bits)[uk];
-      if (listed) Unit<TIn>::drop(v[k], listed);
-      Unit<TIn>::clean(v[k]);
-      um = fmaxf(um, Unit<TIn>::max(v[k]));
-    }
-    acc.raise(um);
+      for (int k = 0; k < kStage; ++k) {
+        const int uk = u + k * T;
+        const uint32_t word = uk - lane < run.n ? bits[uk >> 5] : 0u;  // the warp's 32 units
+        if (word >> lane & 1u) Unit<TIn>::drop(v[k], held_entries(sh, uk));
+        if (dirty) Unit<TIn>::clean(v[k]);
+        um = fmaxf(um, Unit<TIn>::max(v[k]));
+      }
+      acc.raise(um);
 #pragma unroll
-    for (int k = 0; k < kStage; ++k) acc.template add<TIn>(v[k]);
-  });
-  const float2 mine_ms = block_lse(acc.x.m, acc.sum(), c, sh.red);
+      for (int k = 0; k < kStage; ++k) acc.template add<TIn>(v[k]);
+    });
+    return block_lse<T / 32>(acc.x.m, acc.sum(), c, sh.red);
+  };
+  float2 mine_ms = sum_run(false);
+  const bool dirty = !(mine_ms.y == mine_ms.y);  // the same in every thread of the CTA
+  if (dirty) {
+    run.template prefetch<kGrad>(tid, first);
+    __syncthreads();  // sh.red is read
+    mine_ms = sum_run(true);
+  }
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int k = tid + q * T;
+    sh.lp[k] = t[q];
+    sh.p[k] = id[q] >= 0 ? expf(t[q]) : 0.f;
+    sh.x[k] = guard(E::get(x[q]));
+    if (id[q] >= 0 && run.place(id[q]) < 0) id[q] = -1;  // from here on: those of this run
+  }
   if (C > 1) {
-    cluster_wait();
+    cluster_wait();  // every CTA of the cluster runs
     if (tid < C) peer_store2(peer_addr(smem_addr(&sh.ms[rank]), tid), mine_ms.x, mine_ms.y);
     cluster_arrive();
     cluster_wait();
-  } else if (tid == 0) {
-    sh.ms[0] = mine_ms;
+  } else {
+    if (tid == 0) sh.ms[0] = mine_ms;
+    __syncthreads();
   }
   if (tid < 32) {  // the row's scalars, in each CTA from the same numbers
-    __syncwarp();
     constexpr int kPer = LS_MAX_TOP / 32;
     const float2 ms = lane < C ? sh.ms[lane] : make_float2(kNegInf, 0.f);
     const float Mr = warp_max(ms.x);
@@ -168,14 +232,14 @@ __global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const Distil
     }
     const float M = fmaxf(Mr, warp_max(mt));
     P = warp_reduce(P, OpAddF());
-    float S = 0.f;
+    float total = 0.f;
     if (M > kNegInf) {
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) S += xk[q] > kNegInf ? rel_exp(xk[q], M, c) : 0.f;
+      for (int q = 0; q < kPer; ++q) total += xk[q] > kNegInf ? rel_exp(xk[q], M, c) : 0.f;
     }
-    S = warp_reduce(S, OpAddF());
+    total = warp_reduce(total, OpAddF());
     const float rest = Mr > kNegInf ? rel_exp(Mr, M, c) : 0.f;
-    S += Sr * rest;
+    total += Sr * rest;
     float A = P, scale = 1.f, pr = 0.f;
     if (a.tail == LS_TAIL_RENORM) {
       const bool some = P >= kLeastMass;
@@ -185,12 +249,12 @@ __global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const Distil
       pr = fmaxf(1.f - P, 0.f);
       A = P + pr;
     }
-    RowStats st = {M, A / S, Mr, 0.f, scale, {}};
+    RowStats st = {M, A / total, Mr, 0.f, scale, {}};
     if (Mr > kNegInf) st.kappa = st.alpha * rest - (pr > 0.f ? pr / Sr : 0.f);
     if (M == kNegInf) st.alpha = st.kappa = quiet_nan();
     if (lane == 0) sh.st = st;
     if (rank == 0) {
-      const float lnS = logf(S), lnP = a.tail == LS_TAIL_RENORM ? logf(P) : 0.f;
+      const float lnS = logf(total), lnP = a.tail == LS_TAIL_RENORM ? logf(P) : 0.f;
       float kl = 0.f;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
@@ -198,7 +262,7 @@ __global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const Distil
         if (pk > 0.f)
           kl += pk * ((sh.lp[lane + 32 * q] - lnP) - ((xk[q] == M ? 0.f : (xk[q] - M) / a.temperature) - lnS));
       }
-      if (lane == 0 && pr > 0.f) kl += pr * (logf(pr) - ((Mr == M ? 0.f : (Mr - M) / a.temperature) + logf(Sr / S)));
+      if (lane == 0 && pr > 0.f) kl += pr * (logf(pr) - ((Mr == M ? 0.f : (Mr - M) / a.temperature) + logf(Sr / total)));
       kl = warp_reduce(kl, OpAddF());
       if (lane == 0) {
         a.out_loss[i] = M == kNegInf ? quiet_nan() : w * kl;
@@ -208,7 +272,8 @@ __global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const Distil
     }
   }
   if (kGrad) {
-    run.template prefetch<true>(tid, first);
+    // From the run's end: what was read last is the likeliest to be in L2.
+    if (run.n > 0) run.template prefetch<true>(run.last_stage(), first);
     __syncthreads();
     const RowStats st = sh.st;
     const float g = w / a.temperature;
@@ -216,18 +281,27 @@ __global__ void __launch_bounds__(kStreamThreads, 4) distill_kernel(const Distil
     against.init(st.Mr, c);
     const float coef = g * st.kappa * against.scale;
     const bool same = run.aligned_with(grad);
-    run.template stream<true>(first, [&](int u, typename Run<TIn>::Stage& v) {
+    if (run.n > 0)
+      run.template stream_back<true>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
+        const bool whole = run.whole(u) && same;
 #pragma unroll
-      for (int k = 0; k < kStage; ++k) {
-        const int uk = u + k * kStreamThreads;
-        if (uk < run.n) {
+        for (int k = 0; k < kStage; ++k) {
+          const int uk = u + k * T;
+          if (dirty) Unit<TIn>::clean(v[k]);
           unit_grad<TIn>(v[k], against, coef);
-          run.store(grad, same, uk, v[k]);
+          if (whole)
+            store32(grad + run.index(uk), v[k]);
+          else if (uk < run.n)
+            run.store(grad, same, uk, v[k]);
         }
-      }
-    });
+      });
     __syncthreads();
-    if (mine >= 0) grad[id] = E::put(g * (st.alpha * rel_exp(x, st.M, c) - p * st.scale));
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q)
+      if (id[q] >= 0) {
+        const int k = tid + q * T;
+        grad[id[q]] = E::put(g * (st.alpha * rel_exp(sh.x[k], st.M, c) - sh.p[k] * st.scale));
+      }
   }
 }
 
@@ -242,7 +316,7 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   using Raw = typename E::Raw;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)tiles;
-  Run<TIn> run;
+  Run<TIn, kBackThreads> run;
   run.init(a.logits, i, a.row_stride, a.vocab, kBackThreads * kBackUnits, (int)(blockIdx.x % (unsigned)tiles));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
   const float g = (a.weights ? a.weights[i] : 1.f) * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
@@ -277,6 +351,7 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
 #pragma unroll
   for (int k = 0; k < kBackUnits; ++k)
     if (tid + k * kBackThreads < run.n) {
+      Unit<TIn>::clean(v[k]);
       unit_grad<TIn>(v[k], against, coef);
       run.store(grad, same, tid + k * kBackThreads, v[k]);
     }
@@ -284,18 +359,22 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   if (id >= 0) grad[id] = E::put(top);
 }
 
-// Bytes of a CTA's run in the call that reads it twice: two CTAs on each of 152
-// SMs then have at most 38 MB of logits in flight, and as much of gradient, in
-// a 129 MB L2.
-constexpr int64_t kRunTwice = 128 * 1024;
-constexpr int64_t kRunOnce = 1024 * 1024;
+// Bytes of a CTA's run at most.  In the call that reads it twice the runs in
+// flight share L2 with the gradients being written: 1024 x 262144 fp32 takes
+// 394 us with runs of 128 KB (a cluster of 8), 433 with 256 KB.
+constexpr int64_t kRunTwice = 256 * 1024;
+constexpr int64_t kRunOnce = 640 * 1024;
+
+// CTAs of 256 threads, four to an SM (128 threads, eight to an SM: 42 us against
+// 34 on 672 x 151936 bf16, whose rows then leave an SM 18 warps).
+constexpr int kDistillThreads = 256;
 
 template <typename TIn, bool kGrad>
 static ls_status launch(const DistillArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
   const StreamPlan plan = plan_stream(n, a.vocab, dtype, kGrad ? kRunTwice : kRunOnce);
-  const size_t smem = ((size_t)plan.upc * Unit<TIn>::kN + 127) / 128 * 16;
-  return launch_rows(distill_kernel<TIn, kGrad>, a, plan, smem, n, st, done);
+  const size_t smem = ((size_t)plan.upc + 127) / 128 * 16;  // a bit per unit
+  return launch_rows(distill_kernel<TIn, kGrad, kDistillThreads>, a, plan, kDistillThreads, smem, n, st, done);
 }
 
 template <bool kGrad>

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   if (src < 0 || src >= a.logits_rows) bad |= LS_ROW_ERR_BAD_GATHER;
   if (a.has_params && (r < 0 || r >= a.p.num_requests)) bad |= LS_ROW_ERR_BAD_REQUEST;
   if (mrow < -1 || mrow >= a.mask_rows) bad |= a.mask ? LS_ROW_ERR_BAD_MASK : 0;
-  Run<TIn> run;
+  Run<TIn, kProcThreads> run;
   run.init(a.logits, bad & LS_ROW_ERR_BAD_GATHER ? 0 : src, a.row_stride, a.vocab, kTileUnits, tile);
   const bool same = run.aligned_with(out);
   uint32_t v[kUnits][8];

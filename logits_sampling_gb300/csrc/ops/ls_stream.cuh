@@ -3,7 +3,7 @@
 //
 // The row is seen as 32-byte units aligned in global memory (16 bf16 or 8 fp32
 // entries).  CTA q of C owns a contiguous run of units; its threads take them
-// in turn, kStage at a time, with the next stage's loads in flight while one
+// in turn, a few (a stage) at a time, with the next stage's loads in flight while one
 // is computed.  The units that lie wholly in the row are one 256-bit load, the
 // row's first and last partial unit are read entry by entry, with -inf in the
 // places outside the row.
@@ -14,8 +14,6 @@
 namespace lsg {
 namespace ops {
 
-constexpr int kStreamThreads = 256;
-constexpr int kStreamWarps = kStreamThreads / 32;
 constexpr int kStage = 2;  // units of a thread per stage
 constexpr int kMaxCluster = 8;
 
@@ -58,10 +56,17 @@ __device__ __forceinline__ uint32_t peer_add(uint32_t a, uint32_t v) {
 // ---------------------------------------------------------------------------
 // 32-byte units by type
 // ---------------------------------------------------------------------------
+// A streamed line leaves L2 first: what every CTA reuses (the kernel's code among
+// it) stays.
+__device__ __forceinline__ uint64_t stream_policy() {
+  uint64_t pol;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
 __device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
+               : "l"(p), "l"(stream_policy()));
 }
 // The same as an ordinary load, for memory that the kernel itself writes later
 // (a gradient over its logits).
@@ -83,12 +88,12 @@ struct Unit;
 template <>
 struct Unit<bf16_tag> {
   static constexpr int kN = 16;
-  // The unit with its NaNs read as -inf (max with -inf drops a NaN).
+  // NaNs become -inf (max with -inf drops a NaN).
   __device__ __forceinline__ static void clean(uint32_t (&w)[8]) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) w[q] = bmax2(w[q], 0xFF80FF80u);
   }
-  // Maximum of a clean unit.
+  // Maximum of a unit, NaNs ignored (NaN where there is nothing else).
   __device__ __forceinline__ static float max(const uint32_t (&w)[8]) {
     const uint32_t m = bmax2(bmax2(bmax2(w[0], w[1]), bmax2(w[2], w[3])), bmax2(bmax2(w[4], w[5]), bmax2(w[6], w[7])));
     return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
@@ -179,7 +184,7 @@ struct OnlineSum {
   }
   // Before units of maximum um in this lane are added (all lanes call).
   __device__ __forceinline__ void raise(float um) {
-    um = warp_max(um);
+    um = warp_max(um);  // NaN compares false below
     if (um > x.m) {
       const float f = x.m > kNegInf ? x.scale * rel_exp(x.m, um, x.c) : 0.f;
       x.init(um, x.c);
@@ -199,6 +204,11 @@ struct OnlineSum {
     } else if (x.m > kNegInf) {
 #pragma unroll
       for (int q = 0; q < Unit<TIn>::kN / 2; ++q) s0 = add2(s0, x.pair_slow(Unit<TIn>::pair(w, q)));
+    } else {  // nothing yet but -inf and NaN: the sum shall show a NaN
+      uint32_t other = 0u;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) other |= w[q] ^ (Unit<TIn>::kN == 16 ? 0xFF80FF80u : 0xFF800000u);
+      if (other) s0 = pack2(quiet_nan(), quiet_nan());
     }
   }
   __device__ __forceinline__ float sum() const {
@@ -211,7 +221,18 @@ struct OnlineSum {
 // ---------------------------------------------------------------------------
 // One CTA's run of a row's units
 // ---------------------------------------------------------------------------
+// A unit that is not wholly in the row, whose entry 0 has index j: once or twice
+// per row, so out of the loops' code.
 template <typename TIn>
+__device__ __noinline__ void load_edge(const typename Elem<TIn>::Raw* row, int64_t j, int64_t V, uint32_t* w) {
+  constexpr int kN = Unit<TIn>::kN;
+  typename Elem<TIn>::Raw* e = reinterpret_cast<typename Elem<TIn>::Raw*>(w);
+#pragma unroll 1
+  for (int q = 0; q < kN; ++q) e[q] = j + q >= 0 && j + q < V ? row[j + q] : Elem<TIn>::neg_inf();
+}
+
+// T: threads of the CTA.
+template <typename TIn, int T>
 struct Run {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
@@ -250,11 +271,10 @@ struct Run {
       else
         load32(base + (int64_t)u * 32, w);
     } else {
-      Raw e[kN];
-      const int64_t j = index(u);
+      uint32_t edge[8];
+      load_edge<TIn>(row, index(u), V, edge);
 #pragma unroll
-      for (int q = 0; q < kN; ++q) e[q] = j + q >= 0 && j + q < V ? row[j + q] : E::neg_inf();
-      memcpy(w, e, 32);
+      for (int q = 0; q < 8; ++q) w[q] = edge[q];
     }
   }
   // Writes unit u of an output row with this row's indices (`same`: and its alignment).
@@ -274,14 +294,31 @@ struct Run {
     return ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 31u) == 0;
   }
   // Visits this thread's units in order, kStage at a time: visit(u, w) with the
-  // words of units u and u + kStreamThreads (units past n as -inf).  `first`
-  // has been loaded by prefetch().
+  // words of units u and u + T (units past n as -inf).  `first`
+  // has been loaded by prefetch().  A stage whose units all lie wholly in the row
+  // and the run (for the whole CTA: one branch) is loaded without further checks.
   typedef uint32_t Stage[kStage][8];
+  static constexpr int kStep = kStage * T;
+  __device__ __forceinline__ bool whole(int u) const {
+    const int first = u - (int)threadIdx.x;
+    return first >= f && first + kStep <= l;
+  }
   template <bool kPlain = false>
   __device__ __forceinline__ void prefetch(int u, Stage& w) const {
+    if (whole(u)) {
+      const char* p = base + (int64_t)u * 32;
+#pragma unroll
+      for (int k = 0; k < kStage; ++k) {
+        if (kPlain)
+          load32_plain(p + k * T * 32, w[k]);
+        else
+          load32(p + k * T * 32, w[k]);
+      }
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < kStage; ++k) {
-      const int uk = u + k * kStreamThreads;
+      const int uk = u + k * T;
       if (uk < n) {
         load<kPlain>(uk, w[k]);
       } else {
@@ -295,29 +332,42 @@ struct Run {
   template <bool kPlain = false, typename F>
   __device__ __forceinline__ void stream(Stage& first, F visit) const {
     const int lane = threadIdx.x & 31;
-    for (int u = threadIdx.x; u - lane < n; u += 2 * kStage * kStreamThreads) {
+    for (int u = threadIdx.x; u - lane < n; u += 2 * kStep) {
       Stage next;
-      const int u1 = u + kStage * kStreamThreads;
-      prefetch<kPlain>(u1, next);
+      prefetch<kPlain>(u + kStep, next);
       visit(u, first);
-      if (u1 - lane >= n) break;
-      prefetch<kPlain>(u1 + kStage * kStreamThreads, first);
-      visit(u1, next);
+      if (u + kStep - lane >= n) break;
+      prefetch<kPlain>(u + 2 * kStep, first);
+      visit(u + kStep, next);
+    }
+  }
+  // The same from the run's last stage to its first.
+  __device__ __forceinline__ int last_stage() const { return (n - 1) / kStep * kStep + (int)threadIdx.x; }
+  template <bool kPlain = false, typename F>
+  __device__ __forceinline__ void stream_back(Stage& last, F visit) const {
+    for (int u = last_stage(); u >= 0; u -= 2 * kStep) {
+      Stage next;
+      if (u >= kStep) prefetch<kPlain>(u - kStep, next);
+      visit(u, last);
+      if (u < kStep) break;
+      if (u >= 2 * kStep) prefetch<kPlain>(u - 2 * kStep, last);
+      visit(u - kStep, next);
     }
   }
 };
 
 // (maximum, sum) of the block from each warp's maximum and thread's sum, in
-// every thread; the sum's order is fixed.  `red` holds kStreamWarps pairs.
+// every thread; the sum's order is fixed.  `red` holds a pair per warp.
+template <int kWarps>
 __device__ __forceinline__ float2 block_lse(float wm, float s, float c, float2* red) {
   const float ws = warp_reduce(s, OpAddF());
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(wm, ws);
   __syncthreads();
-  const float2 r = red[threadIdx.x & (kStreamWarps - 1)];
+  const float2 r = red[threadIdx.x & (kWarps - 1)];
   const float bm = warp_max(r.x);
-  float bs = r.x > kNegInf ? r.y * rel_exp(r.x, bm, c) : 0.f;
+  float bs = r.y * (r.x > kNegInf ? rel_exp(r.x, bm, c) : 0.f);  // a NaN stays one
 #pragma unroll
-  for (int o = kStreamWarps / 2; o > 0; o >>= 1) bs += __shfl_xor_sync(0xFFFFFFFFu, bs, o);
+  for (int o = kWarps / 2; o > 0; o >>= 1) bs += __shfl_xor_sync(0xFFFFFFFFu, bs, o);
   return make_float2(bm, bs);
 }
 
@@ -364,13 +414,13 @@ static bool open_limits(Kernel kernel, std::atomic<int>* done) {
 
 // Launches one cluster of p.ctas CTAs per row.
 template <typename Kernel, typename Args>
-static ls_status launch_rows(Kernel kernel, const Args& a, const StreamPlan& p, size_t smem, int32_t n,
-                               cudaStream_t stream, std::atomic<int>* done) {
+static ls_status launch_rows(Kernel kernel, const Args& a, const StreamPlan& p, int threads, size_t smem, int32_t n,
+                             cudaStream_t stream, std::atomic<int>* done) {
   if ((int64_t)n * p.ctas > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   if (!open_limits(kernel, done)) return LS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)n * p.ctas));
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

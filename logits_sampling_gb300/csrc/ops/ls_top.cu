@@ -3,7 +3,10 @@
 //
 // A row over the CTAs of a cluster (ls_stream.cuh).  Per row:
 //  1. One pass: each thread's running maximum and sum of exponentials, and in
-//     shared memory the maximum of each stage (kStage units of a thread).
+//     shared memory the maximum of each stage (a few units of a thread), as the
+//     upper 16 bits of its order-preserving key: exact for bf16, rounded down
+//     in key order for fp32, so that a maximum at or above v keeps a key at or
+//     above that of v.
 //  2. A lower bound of the k-th largest entry.  In each of the w warps that hold
 //     units, the ceil(k / w)-th largest lane maximum: at least k entries of the
 //     run are at or above the least of these.  For large k that is far below
@@ -24,7 +27,8 @@ namespace lsg {
 namespace ops {
 
 constexpr int kLocal = 512;      // keys that a CTA sends at most
-constexpr int kTakeMost = 8;      // lane maxima of a warp taken away one by one
+constexpr int kCandidates = 512;  // stages listed for the second read
+constexpr int kTakeMost = 16;     // lane maxima of a warp taken away one by one
 constexpr int kRankMost = 384;   // keys placed by counting; more are sorted
 static_assert(kLocal >= LS_MAX_TOP, "a run's own k best must fit");
 
@@ -40,12 +44,16 @@ struct TopArgs {
   int32_t* error_word;
 };
 
+constexpr int kMostWarps = 8;
+
 struct TopShared {
   float2 ms[kMaxCluster];
-  float2 red[kStreamWarps];
+  float2 red[kMostWarps];
   float bound[kMaxCluster];
-  float redf[kStreamWarps];
-  int warp_n[kStreamWarps];
+  float redf[kMostWarps];
+  int warp_n[kMostWarps];
+  int candidates;               // stages that reach the bound
+  uint32_t stage[kCandidates];  // the first of them
   unsigned int total;  // keys sent to this CTA
   int count;           // keys of this CTA
   int base;            // their place among those sent
@@ -53,33 +61,64 @@ struct TopShared {
 };
 
 // Block-wide sum of small counts.
+template <int kWarps>
 __device__ __forceinline__ int block_count(int v, int* red) {
   v = __reduce_add_sync(0xFFFFFFFFu, v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  return __reduce_add_sync(0xFFFFFFFFu, (threadIdx.x & 31) < kStreamWarps ? red[threadIdx.x & 31] : 0);
+  return __reduce_add_sync(0xFFFFFFFFu, (threadIdx.x & 31) < kWarps ? red[threadIdx.x & 31] : 0);
 }
 
-// Visits the run's entries whose stage maximum is at least `least`: f(value, place in the run).
-template <typename TIn, typename F>
-__device__ __forceinline__ void visit_stages(const Run<TIn>& run, const float* stage_max, float least, F f) {
+__device__ __forceinline__ uint16_t stage_key(float v) { return (uint16_t)(f32_key(v) >> 16); }
+
+// Entry e of a unit for an index that is not known beforehand (local memory).
+template <typename TIn>
+__device__ __forceinline__ float entry_at(const uint32_t (&w)[8], int e) {
+  if (Unit<TIn>::kN == 8) return __uint_as_float(w[e]);
+  const uint32_t word = w[e >> 1];
+  return __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
+}
+
+// Reads the stage that begins with unit u again: f(value, place in the run) for
+// each entry at or above `least`.  Few are: their bits are gathered first and
+// then walked, in little code (code that runs once per row is paid for in
+// instruction fetches).
+template <typename TIn, int T, typename F>
+__device__ __forceinline__ void visit_stage(const Run<TIn, T>& run, int u, float least, F f) {
   constexpr int kN = Unit<TIn>::kN;
-  for (int b = threadIdx.x, u = threadIdx.x; u < run.n; b += kStreamThreads, u += kStage * kStreamThreads) {
-    if (!(stage_max[b] >= least)) continue;
-    typename Run<TIn>::Stage w;
-    run.prefetch(u, w);
+  typename Run<TIn, T>::Stage w;
+  uint32_t hits[kStage];
 #pragma unroll
-    for (int k = 0; k < kStage; ++k) {
+  for (int k = 0; k < kStage; ++k) {
+    hits[k] = 0u;
+    if (u + k * T < run.n) run.load(u + k * T, w[k]);
+  }
 #pragma unroll
-      for (int q = 0; q < kN / 2; ++q) {
-        float x, y;
-        unpack2(Unit<TIn>::pair(w[k], q), x, y);
-        f(x, (u + k * kStreamThreads) * kN + 2 * q);
-        f(y, (u + k * kStreamThreads) * kN + 2 * q + 1);
-      }
+  for (int k = 0; k < kStage; ++k) {
+    if (u + k * T >= run.n) break;
+#pragma unroll
+    for (int q = 0; q < kN / 2; ++q) {
+      float x, y;
+      unpack2(Unit<TIn>::pair(w[k], q), x, y);
+      hits[k] |= (x >= least ? 1u : 0u) << (2 * q) | (y >= least ? 2u : 0u) << (2 * q);
     }
   }
+#pragma unroll 1
+  for (int k = 0; k < kStage; ++k)
+#pragma unroll 1
+    for (uint32_t h = hits[k]; h; h &= h - 1) {
+      const int e = __ffs((int)h) - 1;
+      f(entry_at<TIn>(w[k], e), (u + k * T) * kN + e);
+    }
+}
+
+// Visits the run's entries whose stage maximum is at least `least`.
+template <typename TIn, int T, typename F>
+__device__ __forceinline__ void visit_stages(const Run<TIn, T>& run, const uint16_t* stages, float least, F f) {
+  const uint16_t least_key = stage_key(least);
+  for (int b = threadIdx.x, u = threadIdx.x; u < run.n; b += T, u += kStage * T)
+    if (stages[b] >= least_key) visit_stage<TIn, T>(run, u, least, f);
 }
 
 // The run's k best exactly, for any number of ties: `bound` has at least k
@@ -87,14 +126,14 @@ __device__ __forceinline__ void visit_stages(const Run<TIn>& run, const float* s
 // value; else that is found by bisection of the keys above it.  Entries above
 // the cut all belong to the answer, and of those equal to it the lowest
 // indices, taken in order of the run.
-template <typename TIn>
-__device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage_max, int k, float bound, TopShared& sh) {
+template <typename TIn, int T>
+__device__ __noinline__ void select_ties(const Run<TIn, T>& run, const uint16_t* stages, int k, float bound, TopShared& sh) {
   constexpr int kN = Unit<TIn>::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto above = [&](uint32_t key) {  // entries whose key is above `key`
     int n = 0;
-    visit_stages<TIn>(run, stage_max, f32_from_key(key), [&](float v, int) { n += guard(v) == v && f32_key(v) > key; });
-    return block_count(n, sh.warp_n);
+    visit_stages<TIn, T>(run, stages, f32_from_key(key), [&](float v, int) { n += guard(v) == v && f32_key(v) > key; });
+    return block_count<T / 32>(n, sh.warp_n);
   };
   uint32_t cut = max(f32_key(bound), f32_key(kNegInf) + 1u);  // -inf is never listed
   if (above(cut) >= k) {
@@ -112,7 +151,7 @@ __device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage
   __syncthreads();
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  visit_stages<TIn>(run, stage_max, cut_value, [&](float v, int place) {
+  visit_stages<TIn, T>(run, stages, cut_value, [&](float v, int place) {
     if (v > cut_value) {
       const int at = atomicAdd(&sh.count, 1);
       if (at < kLocal) sh.keys[at] = argmax_key(v, run.j0 + place);
@@ -120,7 +159,7 @@ __device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage
   });
   __syncthreads();
   int have = sh.count;  // fewer than k
-  for (int u0 = 0; u0 < run.n && have < k; u0 += kStreamThreads) {
+  for (int u0 = 0; u0 < run.n && have < k; u0 += T) {
     const int u = u0 + tid;
     float v[kN];
     int n = 0;
@@ -143,7 +182,7 @@ __device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage
     __syncthreads();
     int at = have + before - n, all = 0;
 #pragma unroll
-    for (int q = 0; q < kStreamWarps; ++q) {
+    for (int q = 0; q < (T / 32); ++q) {
       if (q < warp) at += sh.warp_n[q];
       all += sh.warp_n[q];
     }
@@ -164,16 +203,16 @@ __device__ __noinline__ void select_ties(const Run<TIn>& run, const float* stage
 
 // A value with at least k stage maxima at or above it and, where values allow,
 // at most k / 8 more (-inf where there are fewer than k): bisection of the
-// keys up to the run's maximum.
-__device__ __noinline__ float tighten(int units, const float* stage_max, int k, float most, TopShared& sh) {
-  uint32_t lo = f32_key(kNegInf), hi = f32_key(most) + 1u;
+// 16-bit keys up to the run's maximum.
+template <int T>
+__device__ __noinline__ float tighten(int units, const uint16_t* stages, int k, float most, TopShared& sh) {
+  uint32_t lo = stage_key(kNegInf), hi = stage_key(most) + 1u;
   while (hi - lo > 1u) {
     const uint32_t mid = lo + (hi - lo) / 2u;
-    const float t = f32_from_key(mid);
     int n = 0;
-    for (int b = threadIdx.x, u = threadIdx.x; u < units; b += kStreamThreads, u += kStage * kStreamThreads)
-      n += stage_max[b] >= t;
-    n = block_count(n, sh.warp_n);
+    for (int b = threadIdx.x, u = threadIdx.x; u < units; b += T, u += kStage * T)
+      n += stages[b] >= mid;
+    n = block_count<T / 32>(n, sh.warp_n);
     if (n >= k) {
       lo = mid;
       if (n <= k + k / 8) break;
@@ -181,15 +220,16 @@ __device__ __noinline__ float tighten(int units, const float* stage_max, int k, 
       hi = mid;
     }
   }
-  return f32_from_key(lo);
+  return lo == stage_key(kNegInf) ? kNegInf : f32_from_key(lo << 16);
 }
 
 // Descending sort of n keys in shared memory (n a power of two).
+template <int T>
 __device__ __noinline__ void sort_keys(unsigned long long* keys, int n) {
   for (int size = 2; size <= n; size <<= 1)
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
       __syncthreads();
-      for (int t = threadIdx.x; t < n / 2; t += kStreamThreads) {
+      for (int t = threadIdx.x; t < n / 2; t += T) {
         const int a = 2 * t - (t & (stride - 1)), b = a + stride;
         const unsigned long long x = keys[a], y = keys[b];
         if ((x < y) == ((a & size) == 0)) {
@@ -201,11 +241,11 @@ __device__ __noinline__ void sort_keys(unsigned long long* keys, int n) {
   __syncthreads();
 }
 
-template <typename TIn>
-__global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a, int upc) {
-  extern __shared__ uint4 dyn_smem[];  // stage maxima, then the keys sent to the first CTA
+template <typename TIn, int T>
+__global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int upc) {
+  extern __shared__ uint4 dyn_smem[];  // keys of the stage maxima, then the entries sent to the first CTA
   __shared__ TopShared sh;
-  float* stage_max = reinterpret_cast<float*>(dyn_smem);
+  uint16_t* stages = reinterpret_cast<uint16_t*>(dyn_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t i = blockIdx.x / (unsigned)C;
@@ -214,7 +254,7 @@ __global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a,
   int32_t* ids = a.out_ids + i * k;
   float* lp = a.out_lp + i * k;
   auto fail = [&](int32_t bit) {
-    for (int q = tid; q < k; q += kStreamThreads) {
+    for (int q = tid; q < k; q += T) {
       ids[q] = -1;
       lp[q] = quiet_nan();
     }
@@ -227,35 +267,47 @@ __global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a,
     if (rank == 0) fail(LS_ROW_ERR_BAD_GATHER);
     return;
   }
-  Run<TIn> run;
+  Run<TIn, T> run;
   run.init(a.logits, src, a.row_stride, a.vocab, upc, rank);
-  typename Run<TIn>::Stage first;
+  typename Run<TIn, T>::Stage first;
   run.prefetch(tid, first);
   if (C > 1) cluster_arrive();
   if (tid == 0) {
-    sh.count = 0;
+    sh.count = sh.candidates = 0;
     sh.total = 0u;
   }
+  if (run.n > 0) stages[(run.n - 1) / (kStage * T) * T + tid] = 0;  // the last stage need not have units of every warp
   const float c = kLog2e / a.temperature;
-  OnlineSum acc;
-  acc.init(c);
-  float mine = kNegInf;  // this thread's maximum
-  run.stream(first, [&](int u, typename Run<TIn>::Stage& v) {
-    float um = kNegInf;
+  float mine;  // this thread's maximum
+  // NaN logits: the first pass takes them as they come, and a run whose sum is
+  // NaN is taken again with each of them read as -inf.
+  auto sum_run = [&](bool dirty) {
+    OnlineSum acc;
+    acc.init(c);
+    mine = kNegInf;
+    run.stream(first, [&](int u, typename Run<TIn, T>::Stage& v) {
+      float um = kNegInf;
 #pragma unroll
-    for (int q = 0; q < kStage; ++q) {
-      Unit<TIn>::clean(v[q]);
-      um = fmaxf(um, Unit<TIn>::max(v[q]));
-    }
-    // u = tid + stage * kStage * kStreamThreads
-    stage_max[(u - tid) / kStage + tid] = um;
-    mine = fmaxf(mine, um);
-    acc.raise(um);
+      for (int q = 0; q < kStage; ++q) {
+        if (dirty) Unit<TIn>::clean(v[q]);
+        um = fmaxf(um, Unit<TIn>::max(v[q]));
+      }
+      // u = tid + stage * kStage * T
+      stages[(u - tid) / kStage + tid] = stage_key(um);
+      mine = fmaxf(mine, um);
+      acc.raise(um);
 #pragma unroll
-    for (int q = 0; q < kStage; ++q) acc.template add<TIn>(v[q]);
-  });
-  // the j-th largest lane maximum of each warp that holds units (ties ranked by lane)
-  const int warps = min(kStreamWarps, (run.n + 31) / 32);
+      for (int q = 0; q < kStage; ++q) acc.template add<TIn>(v[q]);
+    });
+    return block_lse<T / 32>(acc.x.m, acc.sum(), c, sh.red);
+  };
+  float2 mine_ms = sum_run(false);
+  if (!(mine_ms.y == mine_ms.y)) {  // the same in every thread of the CTA
+    run.prefetch(tid, first);
+    __syncthreads();  // sh.red is read
+    mine_ms = sum_run(true);
+  }
+  const int warps = min((T / 32), (run.n + 31) / 32);
   float bound = kPosInf;
   if (warp < warps) {
     const int j = (k + warps - 1) / warps;
@@ -271,9 +323,9 @@ __global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a,
     }
   }
   if (lane == 0) sh.redf[warp] = bound;
-  const float2 mine_ms = block_lse(acc.x.m, acc.sum(), c, sh.red);  // its barriers order redf too
-  bound = run.n > 0 ? warp_min(sh.redf[tid & (kStreamWarps - 1)]) : kNegInf;
-  if (run.n > 0 && (k + warps - 1) / warps > kTakeMost) bound = tighten(run.n, stage_max, k, mine_ms.x, sh);
+  __syncthreads();
+  bound = run.n > 0 ? warp_min(sh.redf[tid & ((T / 32) - 1)]) : kNegInf;
+  if (run.n > 0 && (k + warps - 1) / warps > kTakeMost) bound = tighten<T>(run.n, stages, k, mine_ms.x, sh);
   if (C > 1) {
     cluster_wait();  // every CTA of the cluster runs
     if (tid < C) {
@@ -296,14 +348,43 @@ __global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a,
     return;
   }
   bound = warp_max(lane < C ? sh.bound[lane] : kNegInf);
-  visit_stages<TIn>(run, stage_max, bound, [&](float v, int place) {
-    if (v >= bound && v > kNegInf) {
+  auto take = [&](float v, int place) {
+    if (v > kNegInf) {
       const int at = atomicAdd(&sh.count, 1);
       if (at < kLocal) sh.keys[at] = argmax_key(v, run.j0 + place);
     }
-  });
+  };
+  // List the stages first (eight keys of any thread's at a time), then read them
+  // again, one per thread: a thread reading its own as it met them would wait
+  // for memory once per stage.
+  const uint16_t bound_key = stage_key(bound);
+  const int slots = (run.n + kStage * T - 1) / (kStage * T) * T;
+  for (int q = tid * 8; q < slots; q += T * 8) {
+    const uint4 eight = *reinterpret_cast<const uint4*>(&stages[q]);
+    const uint32_t words[4] = {eight.x, eight.y, eight.z, eight.w};
+    uint32_t hits = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hits |= ((words[k] & 0xFFFFu) >= bound_key ? 1u : 0u) << (2 * k);
+      hits |= ((words[k] >> 16) >= bound_key ? 1u : 0u) << (2 * k + 1);
+    }
+    for (; hits; hits &= hits - 1) {
+      const int at = atomicAdd(&sh.candidates, 1);
+      if (at < kCandidates) sh.stage[at] = (uint32_t)(q + __ffs((int)hits) - 1);
+    }
+  }
   __syncthreads();
-  if (sh.count > kLocal) select_ties<TIn>(run, stage_max, k, bound, sh);
+  const int listed = sh.candidates;
+  if (listed <= kCandidates) {
+    for (int q = tid; q < listed; q += T) {
+      const int b = (int)sh.stage[q], who = b % T;
+      visit_stage<TIn, T>(run, (b - who) * kStage + who, bound, take);
+    }
+  } else {
+    visit_stages<TIn, T>(run, stages, bound, take);
+  }
+  __syncthreads();
+  if (sh.count > kLocal) select_ties<TIn, T>(run, stages, k, bound, sh);
   const int n_local = sh.count;
   // to the first CTA, over its stage maxima
   unsigned long long* all = reinterpret_cast<unsigned long long*>(dyn_smem);
@@ -313,54 +394,60 @@ __global__ void __launch_bounds__(kStreamThreads, 4) top_kernel(const TopArgs a,
     cluster_arrive();
     cluster_wait();  // every CTA is done with its stage maxima
     const int base = sh.base;
-    for (int q = tid; q < n_local; q += kStreamThreads) peer_store(peer_addr(smem_addr(&all[base + q]), 0), sh.keys[q]);
+    for (int q = tid; q < n_local; q += T) peer_store(peer_addr(smem_addr(&all[base + q]), 0), sh.keys[q]);
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;
     n = (int)sh.total;
+  } else if (n <= kRankMost) {
+    all = sh.keys;
   } else {
-    for (int q = tid; q < n; q += kStreamThreads) all[q] = sh.keys[q];
+    for (int q = tid; q < n; q += T) all[q] = sh.keys[q];
     __syncthreads();
   }
-  const float S = warp_reduce(ms.x > kNegInf ? ms.y * rel_exp(ms.x, M, c) : 0.f, OpAddF());
-  const float lnS = logf(S);
+  const float total = warp_reduce(ms.x > kNegInf ? ms.y * rel_exp(ms.x, M, c) : 0.f, OpAddF());
+  const float lnS = logf(total);
   auto put = [&](int at, unsigned long long key) {
     const float v = f32_from_key((uint32_t)(key >> 32));
     ids[at] = argmax_index(key);
     lp[at] = (v == M ? 0.f : (v - M) / a.temperature) - lnS;
   };
   if (n <= kRankMost) {
-    for (int q = tid; q < n; q += kStreamThreads) {
+    for (int q = tid; q < n; q += T) {
       const unsigned long long key = all[q];
       int at = 0;
+#pragma unroll 8
       for (int o = 0; o < n; ++o) at += all[o] > key;
       if (at < k) put(at, key);
     }
   } else {
     int size = 1;
     while (size < n) size <<= 1;
-    for (int q = n + tid; q < size; q += kStreamThreads) all[q] = 0ull;  // below every key
-    sort_keys(all, size);
-    for (int q = tid; q < min(n, k); q += kStreamThreads) put(q, all[q]);
+    for (int q = n + tid; q < size; q += T) all[q] = 0ull;  // below every key
+    sort_keys<T>(all, size);
+    for (int q = tid; q < min(n, k); q += T) put(q, all[q]);
   }
-  for (int q = n + tid; q < k; q += kStreamThreads) {
+  for (int q = n + tid; q < k; q += T) {
     ids[q] = -1;
     lp[q] = kNegInf;
   }
   if (tid == 0 && a.out_lse) a.out_lse[i] = M / a.temperature + lnS;
 }
 
-constexpr int64_t kRunTop = 1024 * 1024;  // bytes of a CTA's run at most
+// CTAs of 128 threads, eight to an SM: with 256 threads a row's steps after the
+// stream ran beside fewer others (top 20 of 672 x 151936 bf16 50 us against 41).
+constexpr int kTopThreads = 128;
+constexpr int64_t kRunTop = 640 * 1024;  // bytes of a CTA's run at most
 
 template <typename TIn>
 static ls_status launch_top(const TopArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
   const StreamPlan plan = plan_stream(n, a.vocab, dtype, kRunTop);
-  // stage maxima of every thread; the keys of every CTA, padded to a power of two
-  const size_t stages = ((size_t)plan.upc + kStage * kStreamThreads - 1) / (kStage * kStreamThreads);
-  const size_t maxima = stages * kStreamThreads * sizeof(float);
+  // a key per stage of every thread; the entries of every CTA, padded to a power of two
+  const size_t stages = ((size_t)plan.upc + kStage * kTopThreads - 1) / (kStage * kTopThreads);
+  const size_t maxima = stages * kTopThreads * sizeof(uint16_t);
   const size_t keys = (size_t)plan.ctas * kLocal * sizeof(unsigned long long);
-  return launch_rows(top_kernel<TIn>, a, plan, maxima > keys ? maxima : keys, n, st, done);
+  return launch_rows(top_kernel<TIn, kTopThreads>, a, plan, kTopThreads, maxima > keys ? maxima : keys, n, st, done);
 }
 
 }  // namespace ops

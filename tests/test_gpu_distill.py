@@ -176,6 +176,29 @@ def test_special_values(tail, dtype):
     assert got[4] == ls.LS_ROW_ERR_NO_FINITE
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [3001, 120001])
+def test_stretches_of_nan(dtype, V):
+    """NaN logits are -inf wherever they lie: alone, in whole stretches, beside
+    -inf, at the targets, up to a row of nothing else."""
+    rng = np.random.default_rng(V)
+    x = (rng.standard_normal((7, V)) * 2).astype(np.float32)
+    x = R.to_dtype(x, dtype)
+    ids, lp = _targets(rng, x, 9, 1.0)
+    x[0, : V // 2] = np.nan
+    x[1, V // 3:] = np.nan
+    x[2, :] = np.nan
+    x[2, V - 5] = 1.0
+    x[3, : V // 2] = -np.inf
+    x[3, : V // 2: 3] = np.nan
+    x[4, ids[4]] = np.nan
+    x[5, :] = np.nan
+    x[6, 7] = np.nan
+    for tail in TAILS:
+        got = _calls(x, R.device_matrix(x, dtype, 1, 2), ids, lp, 1.0, tail, None, None)
+        _check(x, ids, lp, 1.0, tail, None, None, got, dtype)
+
+
 def test_weight_zero_is_not_read():
     import torch
     import logits_sampling_gb300 as ls

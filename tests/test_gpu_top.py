@@ -107,6 +107,7 @@ def test_special_values(dtype, V):
     x[6, ::2] = -np.inf
     x[7, :] = np.inf
     x[8, :700] = np.nan
+    x[8, 700:720] = -np.inf
     x = R.to_dtype(x, dtype)
     got = _run(R.device_matrix(x, dtype), 30)
     _check(got, x, 30, 1.0)
