@@ -42,10 +42,15 @@ from ._row_ops import (  # noqa: F401
     MAX_TOP,
     LogitsParams,
     distill,
-    distill_loss,
-    distill_loss_backward,
-    distill_loss_grad,
-    process_logits,
     row_ops_max_vocab,
-    top_log_probs,
 )
+
+
+def __getattr__(name):
+    """The calls of include/ls_row_ops.h, loaded (with torch) when first used."""
+    from . import _row_ops
+    if name in _row_ops.CALLS:
+        for call in _row_ops.CALLS:
+            globals()[call] = getattr(_row_ops.calls(), call)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -6,6 +6,10 @@ Compiles logits_sampling_gb300/csrc/*.cu and csrc/ops/*.cu into logits_sampling_
 (-gencode arch=compute_103a,code=sm_103a, -O3, -lineinfo, no fast-math).  The
 build is skipped when the library is newer than every source and header.
 
+The Python calls of include/ls_row_ops.h (csrc/py/row_ops_py.cpp) are a small
+extension module over torch's C++ tensors, _row_ops_c.so, compiled beside it
+with g++ against the installed torch's headers.
+
 VARIANTS holds test-only builds of the same sources with other compile-time
 constants (never loaded by the package itself): ``reselect`` puts the top-p
 candidate bound above every cut, so every top-p row takes the re-select over
@@ -13,16 +17,20 @@ all of its entries -- the path that otherwise runs only when rounding beats
 the bound's slack.
 """
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libls_sampler.so")
+BINDING = os.path.join(PKG, "_row_ops_c.so")
+BINDING_SOURCE = os.path.join(CSRC, "py", "row_ops_py.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {"reselect": ["-DLS_TOPP_SLACK=-64.0f"]}
 
@@ -36,6 +44,23 @@ def _nvcc():
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libls_sampler.so")
+
+
+def _binding_command(out):
+    """The compiler's command line for the extension module."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)  # no import: only its headers are needed
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda,
+               sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *[a for i in include for a in ("-isystem", i)], "-I",
+            INCLUDE, BINDING_SOURCE, "-o", out, "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
+
+
+def _binding_up_to_date():
+    t = os.path.getmtime(BINDING) if os.path.exists(BINDING) else 0
+    return all(os.path.getmtime(p) <= t for p in (BINDING_SOURCE, os.path.join(INCLUDE, "ls_row_ops.h"),
+                                                  os.path.join(INCLUDE, "ls_sampler.h"), os.path.abspath(__file__)))
 
 
 def sources():
@@ -61,8 +86,25 @@ def build(force=False, verbose=False, variant=None):
     objects are then linked."""
     lib = LIB if variant is None else variant_path(variant)
     extra = [] if variant is None else VARIANTS[variant]
+    if variant is None and (force or not _binding_up_to_date()):
+        tmp = f"{BINDING}.tmp{os.getpid()}"
+        binding = subprocess.Popen(_binding_command(tmp))
+    else:
+        binding = None
+    try:
+        _build_library(lib, extra, force, verbose, variant)
+    finally:
+        failed = binding is not None and binding.wait() != 0
+    if failed:
+        raise subprocess.CalledProcessError(1, "g++", f"compiling {BINDING_SOURCE} failed")
+    if binding is not None:
+        os.replace(tmp, BINDING)
+    return lib
+
+
+def _build_library(lib, extra, force, verbose, variant):
     if not force and up_to_date(lib):
-        return lib
+        return
     tag = f".{variant or 'main'}.tmp{os.getpid()}"
     objs, procs = [], []
     for src in sources():
@@ -85,8 +127,6 @@ def build(force=False, verbose=False, variant=None):
         for o in objs:
             if os.path.exists(o):
                 os.remove(o)
-    return lib
-
 
 
 if __name__ == "__main__":

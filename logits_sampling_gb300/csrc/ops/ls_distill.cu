@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
   constexpr int kN = Unit<TIn>::kN;
+  constexpr int kFirst = kGrad ? LOAD_KEEP : LOAD_ONCE;
   constexpr int kOwn = LS_MAX_TOP / T;  // teacher entries per thread
   static_assert(kOwn * T == LS_MAX_TOP, "");
   extern __shared__ uint4 dyn_smem[];
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
     return;
   }
   typename Run<TIn, T>::Stage first;
-  run.template prefetch<kGrad>(tid, first);
+  run.template prefetch<kFirst>(tid, first);
   if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
   // a bit per unit of the run
   uint32_t* bits = reinterpret_cast<uint32_t*>(dyn_smem);
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   // NaN is taken again with each of them read as -inf.
   auto sum_run = [&](bool dirty) {
     acc.init(c);
-    run.template stream<kGrad>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
+    run.template stream<kFirst>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
       float um = kNegInf;
 #pragma unroll
       for (int k = 0; k < kStage; ++k) {
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   float2 mine_ms = sum_run(false);
   const bool dirty = !(mine_ms.y == mine_ms.y);  // the same in every thread of the CTA
   if (dirty) {
-    run.template prefetch<kGrad>(tid, first);
+    run.template prefetch<kFirst>(tid, first);
     __syncthreads();  // sh.red is read
     mine_ms = sum_run(true);
   }
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   }
   if (kGrad) {
     // From the run's end: what was read last is the likeliest to be in L2.
-    if (run.n > 0) run.template prefetch<true>(run.last_stage(), first);
+    if (run.n > 0) run.template prefetch<LOAD_PLAIN>(run.last_stage(), first);
     __syncthreads();
     const RowStats st = sh.st;
     const float g = w / a.temperature;
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
     const float coef = g * st.kappa * against.scale;
     const bool same = run.aligned_with(grad);
     if (run.n > 0)
-      run.template stream_back<true>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
+      run.template stream_back<LOAD_PLAIN>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
         const bool whole = run.whole(u) && same;
 #pragma unroll
         for (int k = 0; k < kStage; ++k) {
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   uint32_t v[kBackUnits][8];
 #pragma unroll
   for (int k = 0; k < kBackUnits; ++k)
-    if (tid + k * kBackThreads < run.n) run.template load<true>(tid + k * kBackThreads, v[k]);
+    if (tid + k * kBackThreads < run.n) run.template load<LOAD_PLAIN>(tid + k * kBackThreads, v[k]);
   const RowStats st = a.stats_in[i];
   const float c = kLog2e / a.temperature;
   int id = -1;

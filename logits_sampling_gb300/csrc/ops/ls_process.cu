@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   }
 #pragma unroll
   for (int q = 0; q < kUnits; ++q)
-    if (tid + q * kProcThreads < run.n) run.template load<true>(tid + q * kProcThreads, v[q]);
+    if (tid + q * kProcThreads < run.n) run.template load<LOAD_PLAIN>(tid + q * kProcThreads, v[q]);
 
   // The request's penalties; neutral ones leave the history unread.
   float rho = 1.f, pres = 0.f, freq = 0.f;

@@ -68,13 +68,32 @@ __device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p), "l"(stream_policy()));
 }
-// The same as an ordinary load, for memory that the kernel itself writes later
-// (a gradient over its logits).
+// The same as an ordinary load, for memory that the kernel itself may write
+// later (an output over its input).
 __device__ __forceinline__ void load32_plain(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
+               : "l"(p), "l"(stream_policy())
                : "memory");
+}
+// And where the line is read again soon: it leaves L2 last.
+__device__ __forceinline__ void load32_keep(const void* p, uint32_t (&w)[8]) {
+  uint64_t pol;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p), "l"(pol)
+               : "memory");
+}
+enum { LOAD_ONCE, LOAD_PLAIN, LOAD_KEEP };
+template <int kHow>
+__device__ __forceinline__ void load_as(const void* p, uint32_t (&w)[8]) {
+  if (kHow == LOAD_ONCE)
+    load32(p, w);
+  else if (kHow == LOAD_PLAIN)
+    load32_plain(p, w);
+  else
+    load32_keep(p, w);
 }
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -262,14 +281,11 @@ struct Run {
     const int64_t e = j - j0;
     return e >= 0 && e < (int64_t)n * kN ? (int)e : -1;
   }
-  // A unit's words (u < n); kPlain: see load32_plain.
-  template <bool kPlain = false>
+  // A unit's words (u < n); kHow: LOAD_*.
+  template <int kHow = LOAD_ONCE>
   __device__ __forceinline__ void load(int u, uint32_t (&w)[8]) const {
     if (full(u)) {
-      if (kPlain)
-        load32_plain(base + (int64_t)u * 32, w);
-      else
-        load32(base + (int64_t)u * 32, w);
+      load_as<kHow>(base + (int64_t)u * 32, w);
     } else {
       uint32_t edge[8];
       load_edge<TIn>(row, index(u), V, edge);
@@ -303,16 +319,13 @@ struct Run {
     const int first = u - (int)threadIdx.x;
     return first >= f && first + kStep <= l;
   }
-  template <bool kPlain = false>
+  template <int kHow = LOAD_ONCE>
   __device__ __forceinline__ void prefetch(int u, Stage& w) const {
     if (whole(u)) {
       const char* p = base + (int64_t)u * 32;
 #pragma unroll
       for (int k = 0; k < kStage; ++k) {
-        if (kPlain)
-          load32_plain(p + k * T * 32, w[k]);
-        else
-          load32(p + k * T * 32, w[k]);
+        load_as<kHow>(p + k * T * 32, w[k]);
       }
       return;
     }
@@ -320,7 +333,7 @@ struct Run {
     for (int k = 0; k < kStage; ++k) {
       const int uk = u + k * T;
       if (uk < n) {
-        load<kPlain>(uk, w[k]);
+        load<kHow>(uk, w[k]);
       } else {
         const uint32_t none = E::kBytes == 2 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
@@ -329,28 +342,28 @@ struct Run {
     }
   }
   // The trip count is the warp's: every lane of a warp visits the same stages.
-  template <bool kPlain = false, typename F>
+  template <int kHow = LOAD_ONCE, typename F>
   __device__ __forceinline__ void stream(Stage& first, F visit) const {
     const int lane = threadIdx.x & 31;
     for (int u = threadIdx.x; u - lane < n; u += 2 * kStep) {
       Stage next;
-      prefetch<kPlain>(u + kStep, next);
+      prefetch<kHow>(u + kStep, next);
       visit(u, first);
       if (u + kStep - lane >= n) break;
-      prefetch<kPlain>(u + 2 * kStep, first);
+      prefetch<kHow>(u + 2 * kStep, first);
       visit(u + kStep, next);
     }
   }
   // The same from the run's last stage to its first.
   __device__ __forceinline__ int last_stage() const { return (n - 1) / kStep * kStep + (int)threadIdx.x; }
-  template <bool kPlain = false, typename F>
+  template <int kHow = LOAD_ONCE, typename F>
   __device__ __forceinline__ void stream_back(Stage& last, F visit) const {
     for (int u = last_stage(); u >= 0; u -= 2 * kStep) {
       Stage next;
-      if (u >= kStep) prefetch<kPlain>(u - kStep, next);
+      if (u >= kStep) prefetch<kHow>(u - kStep, next);
       visit(u, last);
       if (u < kStep) break;
-      if (u >= 2 * kStep) prefetch<kPlain>(u - 2 * kStep, last);
+      if (u >= 2 * kStep) prefetch<kHow>(u - 2 * kStep, last);
       visit(u - kStep, next);
     }
   }
