@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   const int tid = threadIdx.x, lane = tid & 31;
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t i = blockIdx.x / (unsigned)C;
+  wait_for_previous();
   Run<TIn, T> run;
   run.init(a.logits, i, a.row_stride, a.vocab, upc, rank);
   Raw* grad = kGrad ? static_cast<Raw*>(a.out_grad) + i * a.grad_stride : nullptr;
@@ -177,7 +178,10 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   OnlineSum acc;
   // NaN logits: the first pass takes them as they come, and a run whose sum is
   // NaN is taken again with each of them read as -inf.
-  auto sum_run = [&](bool dirty) {
+  bool dirty = false;
+  float2 mine_ms;
+#pragma unroll 1
+  for (;;) {
     acc.init(c);
     run.template stream<kFirst>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
       float um = kNegInf;
@@ -193,15 +197,13 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
 #pragma unroll
       for (int k = 0; k < kStage; ++k) acc.template add<TIn>(v[k]);
     });
-    return block_lse<T / 32>(acc.x.m, acc.sum(), c, sh.red);
-  };
-  float2 mine_ms = sum_run(false);
-  const bool dirty = !(mine_ms.y == mine_ms.y);  // the same in every thread of the CTA
-  if (dirty) {
+    mine_ms = block_lse<T / 32>(acc.x.m, acc.sum(), c, sh.red);
+    if (dirty || mine_ms.y == mine_ms.y) break;  // the same in every thread of the CTA
+    dirty = true;
     run.template prefetch<kFirst>(tid, first);
     __syncthreads();  // sh.red is read
-    mine_ms = sum_run(true);
   }
+  let_next_start();
 #pragma unroll
   for (int q = 0; q < kOwn; ++q) {
     const int k = tid + q * T;
@@ -317,6 +319,8 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   using Raw = typename E::Raw;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)tiles;
+  wait_for_previous();
+  let_next_start();
   Run<TIn, kBackThreads> run;
   run.init(a.logits, i, a.row_stride, a.vocab, kBackThreads * kBackUnits, (int)(blockIdx.x % (unsigned)tiles));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
@@ -388,12 +392,10 @@ static ls_status dispatch_backward(const DistillArgs& a, ls_dtype dtype, int32_t
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t tiles = (row_units(a.vocab, dtype) + kBackThreads * kBackUnits - 1) / (kBackThreads * kBackUnits);
   if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(tiles * n)), block(kBackThreads);
-  if (dtype == LS_DTYPE_BF16)
-    distill_backward_kernel<bf16_tag><<<grid, block, 0, st>>>(a, (int)tiles);
-  else
-    distill_backward_kernel<float><<<grid, block, 0, st>>>(a, (int)tiles);
-  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+  const dim3 grid((unsigned)(tiles * n));
+  return dtype == LS_DTYPE_BF16
+             ? launch_kernel(distill_backward_kernel<bf16_tag>, grid, kBackThreads, 1, 0, st, a, (int)tiles)
+             : launch_kernel(distill_backward_kernel<float>, grid, kBackThreads, 1, 0, st, a, (int)tiles);
 }
 
 // The checks that the three calls share.

@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   const int tile = (int)(blockIdx.x % (unsigned)tiles);
   Raw* out = static_cast<Raw*>(a.out) + i * a.out_stride;
 
+  wait_for_previous();
+  let_next_start();
   int32_t bad = 0;
   const int64_t src = a.gather ? a.gather[i] : i;
   const int64_t r = a.has_params ? (a.t2r ? a.t2r[i] : i) : 0;
@@ -247,8 +249,8 @@ static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStr
   const bool side = a.has_params && (a.p.tokens || a.p.bias_offsets);
   const size_t smem = side ? (size_t)kEntries * sizeof(Slot) + 2 * (kEntries / 8) : 0;
   if (!open_limits(process_kernel<TIn, Slot, kUnits>, done)) return LS_ERR_CUDA;
-  process_kernel<TIn, Slot, kUnits><<<dim3((unsigned)(tiles * n)), dim3(kProcThreads), smem, st>>>(a, (int)tiles);
-  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+  return launch_kernel(process_kernel<TIn, Slot, kUnits>, dim3((unsigned)(tiles * n)), kProcThreads, 1, smem, st, a,
+                       (int)tiles);
 }
 
 template <typename TIn, typename Slot>

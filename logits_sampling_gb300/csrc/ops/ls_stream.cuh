@@ -53,6 +53,13 @@ __device__ __forceinline__ uint32_t peer_add(uint32_t a, uint32_t v) {
   return o;
 }
 
+// Programmatic dependent launch, as the sampling kernels do it: a kernel may be
+// scheduled while the one before it on the stream drains; every CTA waits for
+// that one's completion before it touches memory, and lets the next kernel be
+// scheduled once its own stream is done.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // 32-byte units by type
 // ---------------------------------------------------------------------------
@@ -343,28 +350,32 @@ struct Run {
   }
   // The trip count is the warp's: every lane of a warp visits the same stages.
   template <int kHow = LOAD_ONCE, typename F>
-  __device__ __forceinline__ void stream(Stage& first, F visit) const {
+  __device__ __forceinline__ void stream(Stage& cur, F visit) const {
     const int lane = threadIdx.x & 31;
-    for (int u = threadIdx.x; u - lane < n; u += 2 * kStep) {
+#pragma unroll 1
+    for (int u = threadIdx.x; u - lane < n; u += kStep) {
       Stage next;
       prefetch<kHow>(u + kStep, next);
-      visit(u, first);
-      if (u + kStep - lane >= n) break;
-      prefetch<kHow>(u + 2 * kStep, first);
-      visit(u + kStep, next);
+      visit(u, cur);
+      move(next, cur);
     }
+  }
+  __device__ __forceinline__ static void move(const Stage& from, Stage& to) {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) to[k][q] = from[k][q];
   }
   // The same from the run's last stage to its first.
   __device__ __forceinline__ int last_stage() const { return (n - 1) / kStep * kStep + (int)threadIdx.x; }
   template <int kHow = LOAD_ONCE, typename F>
-  __device__ __forceinline__ void stream_back(Stage& last, F visit) const {
-    for (int u = last_stage(); u >= 0; u -= 2 * kStep) {
+  __device__ __forceinline__ void stream_back(Stage& cur, F visit) const {
+#pragma unroll 1
+    for (int u = last_stage(); u >= 0; u -= kStep) {
       Stage next;
       if (u >= kStep) prefetch<kHow>(u - kStep, next);
-      visit(u, last);
-      if (u < kStep) break;
-      if (u >= 2 * kStep) prefetch<kHow>(u - 2 * kStep, last);
-      visit(u - kStep, next);
+      visit(u, cur);
+      move(next, cur);
     }
   }
 };
@@ -425,26 +436,35 @@ static bool open_limits(Kernel kernel, std::atomic<int>* done) {
   return true;
 }
 
+// Launches a kernel in clusters of `cluster` CTAs, dependent on its predecessor.
+template <typename... Params, typename... Args>
+static ls_status launch_kernel(void (*kernel)(Params...), dim3 grid, int threads, int cluster, size_t smem,
+                               cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return LS_ERR_CUDA;
+  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+}
+
 // Launches one cluster of p.ctas CTAs per row.
 template <typename Kernel, typename Args>
 static ls_status launch_rows(Kernel kernel, const Args& a, const StreamPlan& p, int threads, size_t smem, int32_t n,
                              cudaStream_t stream, std::atomic<int>* done) {
   if ((int64_t)n * p.ctas > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   if (!open_limits(kernel, done)) return LS_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)n * p.ctas));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, a, p.upc) != cudaSuccess) return LS_ERR_CUDA;
-  return cudaPeekAtLastError() == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+  return launch_kernel(kernel, dim3((unsigned)((int64_t)n * p.ctas)), threads, p.ctas, smem, stream, a, p.upc);
 }
 
 }  // namespace ops

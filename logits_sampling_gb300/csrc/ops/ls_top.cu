@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t i = blockIdx.x / (unsigned)C;
   const int k = a.k;
+  wait_for_previous();
   const int64_t src = a.gather ? a.gather[i] : i;
   int32_t* ids = a.out_ids + i * k;
   float* lp = a.out_lp + i * k;
@@ -279,9 +280,11 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
   if (run.n > 0) stages[(run.n - 1) / (kStage * T) * T + tid] = 0;  // the last stage need not have units of every warp
   const float c = kLog2e / a.temperature;
   float mine;  // this thread's maximum
+  float2 mine_ms;
   // NaN logits: the first pass takes them as they come, and a run whose sum is
   // NaN is taken again with each of them read as -inf.
-  auto sum_run = [&](bool dirty) {
+#pragma unroll 1
+  for (bool dirty = false;; dirty = true) {
     OnlineSum acc;
     acc.init(c);
     mine = kNegInf;
@@ -299,14 +302,12 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
 #pragma unroll
       for (int q = 0; q < kStage; ++q) acc.template add<TIn>(v[q]);
     });
-    return block_lse<T / 32>(acc.x.m, acc.sum(), c, sh.red);
-  };
-  float2 mine_ms = sum_run(false);
-  if (!(mine_ms.y == mine_ms.y)) {  // the same in every thread of the CTA
+    mine_ms = block_lse<T / 32>(acc.x.m, acc.sum(), c, sh.red);
+    if (dirty || mine_ms.y == mine_ms.y) break;  // the same in every thread of the CTA
     run.prefetch(tid, first);
     __syncthreads();  // sh.red is read
-    mine_ms = sum_run(true);
   }
+  let_next_start();
   const int warps = min((T / 32), (run.n + 31) / 32);
   float bound = kPosInf;
   if (warp < warps) {
