@@ -15,7 +15,8 @@
  *                             the loss, its gradient, or both in one call
  *
  * Every call is asynchronous on the caller's stream, allocates nothing, never
- * synchronises with the host and launches one kernel.  Buffers are device
+ * synchronises with the host and launches one kernel (ls_process_logits on large
+ * batches: two).  Buffers are device
  * memory owned by the caller; parameter structs are small host structs of
  * device pointers.  Results do not depend on the order in which CTAs run: the
  * same inputs give the same bits.
@@ -87,6 +88,17 @@ ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64_t logits_r
                             const int32_t* row_lens, const int32_t* allowed_mask, int64_t mask_rows,
                             int64_t mask_stride, const int32_t* mask_index, void* out, int64_t out_stride,
                             int32_t* error_word, void* stream);
+
+/*
+ * ls_set_process_policy -- which kernels ls_process_logits launches, for every
+ * later call in the process (tests and tuning; all write the same values):
+ *   0   chosen from the batch (default)
+ *   1   one kernel, which settles each tile's touched entries itself
+ *   2   a copying kernel and, with params, a second one that settles each row's
+ *       touched entries and overlaps the first
+ * Returns LS_OK, or LS_ERR_INVALID_ARG for any other value (unchanged).
+ */
+int ls_set_process_policy(int policy);
 
 /* Largest k of ls_top_log_probs and of the distillation calls. */
 #define LS_MAX_TOP 256

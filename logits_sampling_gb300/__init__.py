@@ -43,6 +43,7 @@ from ._row_ops import (  # noqa: F401
     LogitsParams,
     distill,
     row_ops_max_vocab,
+    set_process_policy,
 )
 
 

@@ -44,6 +44,8 @@ def configure(lib):
     for name in ("ls_process_logits", "ls_top_log_probs", "ls_distill_loss", "ls_distill_loss_backward",
                  "ls_distill_loss_grad"):
         getattr(lib, name).restype = ci
+    lib.ls_set_process_policy.argtypes = [ci]
+    lib.ls_set_process_policy.restype = ci
     lib.ls_row_ops_max_vocab.argtypes = [ci]
     lib.ls_row_ops_max_vocab.restype = i64
     return lib
@@ -58,6 +60,14 @@ def _lib():
     if _ready is not lib:
         _ready = configure(lib)
     return lib
+
+
+def set_process_policy(policy):
+    """ls_set_process_policy: 0 chosen from the batch, 1 one kernel, 2 a copying
+    and a settling kernel (process_logits; every later call of the process)."""
+    st = _lib().ls_set_process_policy(int(policy))
+    if st != _binding.LS_OK:
+        raise LSError(st, f"ls_set_process_policy({policy})")
 
 
 _calls = None

@@ -41,6 +41,7 @@ struct ProcessArgs {
   void* out;
   int64_t out_stride;
   int32_t* error_word;
+  bool keep;  // the output fits in L2 until its touched entries are settled
 };
 
 // Marks a table slot and returns whether it was empty.  An atomic update of
@@ -71,6 +72,67 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int64_t j, i
   return __funnelshift_r(lo, hi, shift) & ((1u << N) - 1u);
 }
 
+// The row that an output row reads, its request and its mask row.
+struct RowSource {
+  int64_t src, request, mask_row;
+  int32_t bad;  // LS_ROW_ERR_* bits
+  __device__ __forceinline__ RowSource(const ProcessArgs& a, int64_t i) {
+    src = a.gather ? a.gather[i] : i;
+    request = a.has_params ? (a.t2r ? a.t2r[i] : i) : 0;
+    mask_row = a.mask ? (a.mask_index ? a.mask_index[i] : i) : -1;
+    bad = 0;
+    if (src < 0 || src >= a.logits_rows) bad |= LS_ROW_ERR_BAD_GATHER;
+    if (a.has_params && (request < 0 || request >= a.p.num_requests)) bad |= LS_ROW_ERR_BAD_REQUEST;
+    if (a.mask && (mask_row < -1 || mask_row >= a.mask_rows)) bad |= LS_ROW_ERR_BAD_MASK;
+  }
+};
+
+// A request's penalties and biases for a row.  Neutral penalties leave the
+// history unread (L = 0).
+struct RowPenalties {
+  float rho = 1.f, pres = 0.f, freq = 0.f;
+  int32_t L = 0, prompt = 0;
+  const int32_t* history = nullptr;
+  int32_t b_lo = 0, b_hi = 0;
+  __device__ __forceinline__ RowPenalties(const ProcessArgs& a, int64_t i, int64_t r) {
+    if (!a.has_params) return;
+    if (a.p.tokens) {
+      if (a.p.repetition) rho = a.p.repetition[r];
+      if (a.p.presence) pres = a.p.presence[r];
+      if (a.p.frequency) freq = a.p.frequency[r];
+      L = a.row_lens ? a.row_lens[i] : a.p.seq_lens[r];
+      prompt = a.p.prompt_lens ? a.p.prompt_lens[r] : 0;
+      L = min(max(L, 0), a.p.token_capacity);
+      if (rho == 1.f && pres == 0.f && freq == 0.f) L = 0;
+      history = a.p.tokens + r * a.p.token_stride;
+    }
+    if (a.p.bias_offsets) {
+      b_lo = max(a.p.bias_offsets[r], 0);
+      b_hi = min(a.p.bias_offsets[r + 1], a.p.bias_count);
+    }
+  }
+  __device__ __forceinline__ bool any() const { return L > 0 || b_lo < b_hi; }
+  // The new value of a logit: `marks` bit 0: the id occurs; above: occurrences past the prompt.
+  __device__ __forceinline__ float value(float x, uint32_t marks, float b, bool has_bias) const {
+    const float n = (float)(marks >> 1);
+    float y = marks != 0u ? (x > 0.f ? x / rho : x * rho) : x;
+    y = __fsub_rn(y, __fmul_rn(freq, n));
+    if (n > 0.f) y -= pres;
+    if (has_bias) y += b;
+    return guard(y);
+  }
+};
+
+// Fills this CTA's run of a bad output row with NaN and notes its error.
+template <typename TIn, int T>
+__device__ __forceinline__ void fail_run(const ProcessArgs& a, const Run<TIn, T>& run, typename Elem<TIn>::Raw* out,
+                                         bool same, bool first, int32_t bad) {
+  const uint32_t nan = Elem<TIn>::kBytes == 2 ? 0x7FC07FC0u : 0x7FC00000u;
+  const uint32_t v[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+  for (int u = threadIdx.x; u < run.n; u += T) run.store(out, same, u, v);
+  if (threadIdx.x == 0 && first && a.error_word) atomicOr(a.error_word, bad);
+}
+
 template <typename TIn, typename Slot, int kUnits>
 __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessArgs a, int tiles) {
   using E = Elem<TIn>;
@@ -90,54 +152,24 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
 
   wait_for_previous();
   let_next_start();
-  int32_t bad = 0;
-  const int64_t src = a.gather ? a.gather[i] : i;
-  const int64_t r = a.has_params ? (a.t2r ? a.t2r[i] : i) : 0;
-  const int64_t mrow = a.mask ? (a.mask_index ? a.mask_index[i] : i) : -1;
-  if (src < 0 || src >= a.logits_rows) bad |= LS_ROW_ERR_BAD_GATHER;
-  if (a.has_params && (r < 0 || r >= a.p.num_requests)) bad |= LS_ROW_ERR_BAD_REQUEST;
-  if (mrow < -1 || mrow >= a.mask_rows) bad |= a.mask ? LS_ROW_ERR_BAD_MASK : 0;
+  const RowSource from(a, i);
   Run<TIn, kProcThreads> run;
-  run.init(a.logits, bad & LS_ROW_ERR_BAD_GATHER ? 0 : src, a.row_stride, a.vocab, kTileUnits, tile);
+  run.init(a.logits, from.bad & LS_ROW_ERR_BAD_GATHER ? 0 : from.src, a.row_stride, a.vocab, kTileUnits, tile);
   const bool same = run.aligned_with(out);
-  uint32_t v[kUnits][8];
-  if (bad) {
-    const Raw nan = E::put(quiet_nan());
-    Raw e[kN];
-#pragma unroll
-    for (int q = 0; q < kN; ++q) e[q] = nan;
-    memcpy(v[0], e, 32);
-    for (int u = tid; u < run.n; u += kProcThreads) run.store(out, same, u, v[0]);
-    if (tid == 0 && tile == 0 && a.error_word) atomicOr(a.error_word, bad);
+  if (from.bad) {
+    fail_run(a, run, out, same, tile == 0, from.bad);
     return;
   }
+  uint32_t v[kUnits][8];
 #pragma unroll
   for (int q = 0; q < kUnits; ++q)
-    if (tid + q * kProcThreads < run.n) run.template load<LOAD_PLAIN>(tid + q * kProcThreads, v[q]);
+    if (tid + q * kProcThreads < run.n) run.template load<LOAD_NORMAL>(tid + q * kProcThreads, v[q]);
 
-  // The request's penalties; neutral ones leave the history unread.
-  float rho = 1.f, pres = 0.f, freq = 0.f;
-  int32_t L = 0, prompt = 0;
-  const int32_t* history = nullptr;
-  int32_t b_lo = 0, b_hi = 0;
-  if (a.has_params) {
-    if (a.p.tokens) {
-      if (a.p.repetition) rho = a.p.repetition[r];
-      if (a.p.presence) pres = a.p.presence[r];
-      if (a.p.frequency) freq = a.p.frequency[r];
-      L = a.row_lens ? a.row_lens[i] : a.p.seq_lens[r];
-      prompt = a.p.prompt_lens ? a.p.prompt_lens[r] : 0;
-      L = min(max(L, 0), a.p.token_capacity);
-      if (rho == 1.f && pres == 0.f && freq == 0.f) L = 0;
-      history = a.p.tokens + r * a.p.token_stride;
-    }
-    if (a.p.bias_offsets) {
-      b_lo = max(a.p.bias_offsets[r], 0);
-      b_hi = min(a.p.bias_offsets[r + 1], a.p.bias_count);
-    }
-  }
-  const bool any = L > 0 || b_lo < b_hi;  // the same in every thread
-  const uint32_t* mask = mrow >= 0 ? a.mask + mrow * a.mask_stride : nullptr;
+  const RowPenalties pen(a, i, from.request);
+  const int32_t L = pen.L, prompt = pen.prompt, b_lo = pen.b_lo, b_hi = pen.b_hi;
+  const int32_t* history = pen.history;
+  const bool any = pen.any();  // the same in every thread
+  const uint32_t* mask = from.mask_row >= 0 ? a.mask + from.mask_row * a.mask_stride : nullptr;
   // the first ids of the history, and a bias, on their way while the units are written
   int32_t held[kHistoryBatch];
   auto fetch = [&](int32_t at) {
@@ -199,13 +231,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   };
   // the new value of entry e from its logit (called by one thread per entry)
   auto settle = [&](int e, float x, float b, bool has_bias) {
-    const uint32_t m = table[e];
-    const float n = (float)(m >> 1);
-    float y = m != 0u ? (x > 0.f ? x / rho : x * rho) : x;
-    y = __fsub_rn(y, __fmul_rn(freq, n));
-    if (n > 0.f) y -= pres;
-    if (has_bias) y += b;
-    out[run.j0 + e] = E::put(guard(y));
+    out[run.j0 + e] = E::put(pen.value(x, table[e], b, has_bias));
   };
   auto logit = [&](int e) { return E::get(run.row[run.j0 + e]); };
   auto settle_bias = [&](int e, float b) {
@@ -253,11 +279,329 @@ static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStr
                        (int)tiles);
 }
 
+// ---------------------------------------------------------------------------
+// The pair of kernels for batches that fill the GPU
+// ---------------------------------------------------------------------------
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnits = 2048;  // units of a CTA's run
+
+// Step 1 alone: the masked copy.  The run's lines that the mask leaves something
+// of are called into L2 first, one per thread: they keep DRAM busy without
+// registers to hold them, and a unit that the mask forbids entirely is not read.
+template <typename TIn>
+__global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const ProcessArgs a, int runs, int upc) {
+  using Raw = typename Elem<TIn>::Raw;
+  using R = Run<TIn, kCopyThreads>;
+  constexpr int kN = Unit<TIn>::kN;
+  constexpr uint32_t kAll = (1u << kN) - 1u;
+  const int tid = threadIdx.x;
+  const int64_t i = blockIdx.x / (unsigned)runs;
+  const int rank = (int)(blockIdx.x % (unsigned)runs);
+  Raw* out = static_cast<Raw*>(a.out) + i * a.out_stride;
+  wait_for_previous();
+  let_next_start();
+  const RowSource from(a, i);
+  R run;
+  run.init(a.logits, from.bad & LS_ROW_ERR_BAD_GATHER ? 0 : from.src, a.row_stride, a.vocab, upc, rank);
+  const bool same = run.aligned_with(out);
+  if (from.bad) {
+    fail_run(a, run, out, same, rank == 0, from.bad);
+    return;
+  }
+  const uint32_t* mask = from.mask_row >= 0 ? a.mask + from.mask_row * a.mask_stride : nullptr;
+  for (int u = tid * 4; u < run.n; u += 4 * kCopyThreads) {  // four units: a line
+    uint32_t kept = 1u;
+    if (mask) {
+      kept = 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (u + k < run.n) kept |= mask_bits<kN>(mask, run.index(u + k), run.V, run.full(u + k));
+    }
+    if (kept && run.full(u)) asm volatile("prefetch.global.L2 [%0];" ::"l"(run.base + (int64_t)u * 32));
+  }
+  // Bits of the entries that a unit may keep, a stage ahead of its logits.
+  typedef uint32_t Bits[kStage];
+  auto keep_bits = [&](int u, Bits& b) {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      const int uk = u + k * kCopyThreads;
+      b[k] = mask && uk < run.n ? mask_bits<kN>(mask, run.index(uk), run.V, run.full(uk)) : kAll;
+    }
+  };
+  auto load = [&](int u, const Bits& b, typename R::Stage& v) {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k)
+      if (u + k * kCopyThreads < run.n && b[k] != 0u) run.template load<LOAD_PLAIN>(u + k * kCopyThreads, v[k]);
+  };
+  typename R::Stage cur = {}, next = {};
+  Bits b0, b1, b2;
+  keep_bits(tid, b0);
+  keep_bits(tid + R::kStep, b1);
+  load(tid, b0, cur);
+#pragma unroll 1
+  for (int u = tid; u < run.n; u += R::kStep) {
+    keep_bits(u + 2 * R::kStep, b2);
+    load(u + R::kStep, b1, next);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      if (u + k * kCopyThreads >= run.n) break;
+      if (b0[k] != kAll) Unit<TIn>::drop(cur[k], ~b0[k] & kAll);
+      run.store(out, same, u + k * kCopyThreads, cur[k], a.keep);
+    }
+    R::move(next, cur);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      b0[k] = b1[k];
+      b1[k] = b2[k];
+    }
+  }
+}
+
+// The touched entries of a row, one CTA per row.  While the copies are being
+// written it builds a hash table of the history's ids and the biases' in shared
+// memory; then it reads the copies of those that the mask allows, which are the
+// logits themselves, and writes the new values over them.
+constexpr int kSettleThreads = 512;
+constexpr int kSettleSlots = 11776;               // two CTAs to an SM
+constexpr int kSettleIds = kSettleSlots / 4 * 3;  // ids that it takes, repeated ones and biases counted
+constexpr int kSettleHistory = 8;                 // history ids of a thread in flight
+
+struct SettleShared {
+  uint32_t id[kSettleSlots];     // id + 1, 0: free
+  uint32_t marks[kSettleSlots];  // as RowPenalties::value; bit 31: a bias settles it
+  uint16_t list[kSettleIds];     // the slots in use
+  int listed;
+};
+
+__device__ __forceinline__ int home_of(uint32_t id) { return (int)__umulhi(id * 0x9E3779B1u, (uint32_t)kSettleSlots); }
+__device__ __forceinline__ int slot_after(int at) { return at + 1 == kSettleSlots ? 0 : at + 1; }
+
+// The slot of an id, taken if it has none, from slot `at` on.
+__device__ __forceinline__ int slot_of(SettleShared& sh, uint32_t id, int at) {
+  for (int t = 0; t < kSettleSlots; ++t) {
+    const uint32_t met = atomicCAS(&sh.id[at], 0u, id + 1u);
+    if (met == 0u || met == id + 1u) break;
+    at = slot_after(at);
+  }
+  return at;
+}
+
+template <typename TIn>
+__global__ void __launch_bounds__(kSettleThreads, 2) settle_kernel(const ProcessArgs a) {
+  using E = Elem<TIn>;
+  using Raw = typename E::Raw;
+  extern __shared__ uint4 dyn_smem[];
+  SettleShared& sh = *reinterpret_cast<SettleShared*>(dyn_smem);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t i = blockIdx.x;
+  // Inputs may be read before the copies are complete: the copying kernel has
+  // itself waited for everything before it.  Every CTA waits for the copies
+  // before it exits, so whoever waits for this kernel waits for them too.
+  const RowSource from(a, i);
+  if (from.bad) {
+    wait_for_previous();
+    return;
+  }
+  const RowPenalties pen(a, i, from.request);
+  if (!pen.any()) {
+    wait_for_previous();
+    return;
+  }
+  const uint32_t V = (uint32_t)a.vocab;
+  Raw* out = static_cast<Raw*>(a.out) + i * a.out_stride;
+  const uint32_t* mask = from.mask_row >= 0 ? a.mask + from.mask_row * a.mask_stride : nullptr;
+  auto allowed = [&](uint32_t j) { return !mask || (__ldg(mask + (j >> 5)) >> (j & 31) & 1u) != 0u; };
+  const int32_t L = pen.L, biases = max(pen.b_hi - pen.b_lo, 0);
+  if ((int64_t)L + biases > kSettleIds) {
+    // A longer history: the row in parts of as many entries as fit, a count each.
+    wait_for_previous();
+    uint32_t* count = sh.id;
+    constexpr int kPart = 2 * kSettleSlots;  // over id and marks
+    for (uint32_t part = 0; part < V; part += kPart) {
+      __syncthreads();
+      for (int q = tid; q < kPart; q += kSettleThreads) count[q] = 0u;
+      __syncthreads();
+#pragma unroll 8
+      for (int32_t at = tid; at < L; at += kSettleThreads) {
+        const uint32_t j = (uint32_t)pen.history[at], e = j - part;
+        if (j < V && e < (uint32_t)kPart) {
+          if (at < pen.prompt)
+            atomicOr(&count[e], 1u);
+          else
+            atomicAdd(&count[e], 2u);
+        }
+      }
+      __syncthreads();
+      for (int32_t q = pen.b_lo + tid; q < pen.b_hi; q += kSettleThreads) {
+        const uint32_t j = (uint32_t)a.p.bias_ids[q], e = j - part;
+        if (j >= V || e >= (uint32_t)kPart) continue;
+        const uint32_t marks = atomicOr(&count[e], 0x80000000u);
+        if (!(marks & 0x80000000u) && allowed(j))
+          out[j] = E::put(pen.value(E::get(out[j]), marks, a.p.bias_values[q], true));
+      }
+      __syncthreads();
+      for (uint32_t e = tid; e < (uint32_t)kPart && part + e < V; e += kSettleThreads) {
+        const uint32_t marks = count[e], j = part + e;
+        if (marks != 0u && !(marks & 0x80000000u) && allowed(j))
+          out[j] = E::put(pen.value(E::get(out[j]), marks, 0.f, false));
+      }
+    }
+    return;
+  }
+  // A batch of ids at a time.  Compare-and-swap takes the lanes of a warp one by
+  // one, so most ids are placed without it: each pending one that finds its slot
+  // free writes itself there and sees after a barrier whether it, or an equal
+  // one, is what stayed; else it moves a slot on.  At a load of 60% three
+  // quarters are placed in each of the two rounds; what is left is swapped in
+  // (the table is never full, so that ends).
+  uint32_t id[kSettleHistory];
+  auto insert = [&](uint32_t pending, uint32_t output) {  // bits: ids to insert, occurrences past the prompt
+    int at[kSettleHistory];
+#pragma unroll
+    for (int q = 0; q < kSettleHistory; ++q) at[q] = home_of(id[q]);
+    const uint32_t all = pending;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+#pragma unroll
+      for (int q = 0; q < kSettleHistory; ++q)
+        if ((pending >> q & 1u) && sh.id[at[q]] == 0u) sh.id[at[q]] = id[q] + 1u;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kSettleHistory; ++q)
+        if (pending >> q & 1u) {
+          if (sh.id[at[q]] == id[q] + 1u)
+            pending &= ~(1u << q);
+          else
+            at[q] = slot_after(at[q]);
+        }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < kSettleHistory; ++q)
+      if (pending >> q & 1u) at[q] = slot_of(sh, id[q], at[q]);
+    uint32_t fresh = 0u;
+#pragma unroll
+    for (int q = 0; q < kSettleHistory; ++q)
+      if (all >> q & 1u) {
+        const uint32_t was = output >> q & 1u ? atomicAdd(&sh.marks[at[q]], 2u) : atomicOr(&sh.marks[at[q]], 1u);
+        if (was == 0u) fresh |= 1u << q;
+      }
+    if (!__any_sync(0xFFFFFFFFu, fresh != 0u)) return;
+    const int mine = __popc(fresh);
+    int upto = mine;  // with this lane
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += t;
+    }
+    int n = 0;
+    if (lane == 31) n = atomicAdd(&sh.listed, upto);
+    n = __shfl_sync(0xFFFFFFFFu, n, 31) + upto - mine;
+#pragma unroll
+    for (int q = 0; q < kSettleHistory; ++q)
+      if (fresh >> q & 1u) sh.list[n++] = (uint16_t)at[q];
+  };
+  auto fetch = [&](int32_t at) {
+#pragma unroll
+    for (int q = 0; q < kSettleHistory; ++q)
+      id[q] = at + q * kSettleThreads < L ? (uint32_t)pen.history[at + q * kSettleThreads] : 0xFFFFFFFFu;
+  };
+  fetch(tid);
+  for (int q = tid; q < 2 * kSettleSlots / 4; q += kSettleThreads) dyn_smem[q] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) sh.listed = 0;
+  __syncthreads();
+  for (int32_t at = tid; at - tid < L; at += kSettleHistory * kSettleThreads) {
+    if (at != tid) fetch(at);
+    uint32_t pending = 0u, output = 0u;
+#pragma unroll
+    for (int q = 0; q < kSettleHistory; ++q) {
+      if (id[q] < V) pending |= 1u << q;
+      if (at + q * kSettleThreads >= pen.prompt) output |= 1u << q;
+    }
+    insert(pending, output);
+  }
+  __syncthreads();
+  // biased entries belong to the thread of their bias
+  auto claim = [&](uint32_t j, uint32_t* marks) {  // whether this bias is its id's first; *marks as before
+    const int at = slot_of(sh, j, home_of(j));
+    const uint32_t was = atomicOr(&sh.marks[at], 0x80000000u);
+    *marks = was;
+    return !(was & 0x80000000u);
+  };
+  uint32_t bias_j = V, bias_marks = 0u;
+  float bias_v = 0.f;
+  if (tid < biases) {
+    const uint32_t j = (uint32_t)a.p.bias_ids[pen.b_lo + tid];
+    bias_v = a.p.bias_values[pen.b_lo + tid];
+    if (j < V && claim(j, &bias_marks) && allowed(j)) bias_j = j;
+  }
+  const int listed = sh.listed;
+  if (biases > kSettleThreads) {  // the remaining biases, one after another
+    wait_for_previous();
+    for (int32_t q = pen.b_lo + tid + kSettleThreads; q < pen.b_hi; q += kSettleThreads) {
+      const uint32_t j = (uint32_t)a.p.bias_ids[q];
+      uint32_t marks;
+      if (j < V && claim(j, &marks) && allowed(j))
+        out[j] = E::put(pen.value(E::get(out[j]), marks, a.p.bias_values[q], true));
+    }
+  }
+  if (biases > 0) __syncthreads();
+  wait_for_previous();
+  Raw bias_x = bias_j < V ? out[bias_j] : E::neg_inf();
+  for (int q = tid; q < listed; q += kSettleBatch * kSettleThreads) {
+    uint32_t j[kSettleBatch], marks[kSettleBatch];
+    float x[kSettleBatch];
+#pragma unroll
+    for (int k = 0; k < kSettleBatch; ++k) {
+      j[k] = V;
+      if (q + k * kSettleThreads < listed) {
+        const int slot = sh.list[q + k * kSettleThreads];
+        marks[k] = sh.marks[slot];
+        if (!(marks[k] & 0x80000000u)) {
+          j[k] = sh.id[slot] - 1u;
+          x[k] = E::get(out[j[k]]);
+          if (!allowed(j[k])) j[k] = V;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kSettleBatch; ++k)
+      if (j[k] < V) out[j[k]] = E::put(pen.value(x[k], marks[k], 0.f, false));
+  }
+  if (bias_j < V) out[bias_j] = E::put(pen.value(E::get(bias_x), bias_marks, bias_v, true));
+}
+
+constexpr int64_t kPairBytesPerId = 64 * 1024;  // of logits per id that a history may hold
+
+// ls_set_process_policy: 0 = chosen from the batch; 1 = one kernel; 2 = the pair.
+static std::atomic<int> g_policy{0};
+
+template <typename TIn>
+static ls_status launch_pair(ProcessArgs a, ls_dtype dtype, int32_t n, cudaStream_t st) {
+  static std::atomic<int> done[kMaxDevices];
+  const int64_t units = row_units(a.vocab, dtype), runs = (units + kCopyUnits - 1) / kCopyUnits;
+  if (runs * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  a.keep = (int64_t)n * a.vocab * Elem<TIn>::kBytes * 5 <= (int64_t)device_attr<cudaDevAttrL2CacheSize>() * 3;
+  const ls_status rc = launch_kernel(copy_kernel<TIn>, dim3((unsigned)(runs * n)), kCopyThreads, 1, 0, st, a, (int)runs, kCopyUnits);
+  if (rc != LS_OK || !(a.has_params && (a.p.tokens || a.p.bias_offsets))) return rc;
+  if (!open_limits(settle_kernel<TIn>, done)) return LS_ERR_CUDA;
+  return launch_kernel(settle_kernel<TIn>, dim3((unsigned)n), kSettleThreads, 1, sizeof(SettleShared), st, a);
+}
+
 template <typename TIn, typename Slot>
 static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   const int64_t wide = (row_units(a.vocab, dtype) + 4 * kProcThreads - 1) / (4 * kProcThreads) * n;
-  return wide < 2 * device_attr<cudaDevAttrMultiProcessorCount>() ? launch<TIn, Slot, 1>(a, dtype, n, st)
-                                                                  : launch<TIn, Slot, 4>(a, dtype, n, st);
+  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
+  // The pair copies at the speed of memory (1024 x 262144 fp32 with histories up
+  // to 2048: 301 us against 375), but settles a row on one SM, whose scattered
+  // accesses take some microseconds per thousand ids; the one kernel spreads a
+  // row's over its tiles (256 x 128256 bf16: histories up to 2048 34 us either
+  // way, up to 8192 46 us against 75).
+  const bool light = !a.has_params || !a.p.tokens ||
+                     (int64_t)n * a.vocab * Elem<TIn>::kBytes >= (int64_t)a.p.token_capacity * kPairBytesPerId;
+  const int policy = g_policy.load(std::memory_order_relaxed);
+  if (policy == 2 || (policy == 0 && wide >= 8 * sms && light)) return launch_pair<TIn>(a, dtype, n, st);
+  return wide < 2 * sms ? launch<TIn, Slot, 1>(a, dtype, n, st) : launch<TIn, Slot, 4>(a, dtype, n, st);
 }
 
 }  // namespace ops
@@ -311,4 +655,10 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
   const bool narrow = !a.has_params || !a.p.tokens || a.p.token_capacity < (1 << 15);
   if (dtype == LS_DTYPE_F32) return narrow ? launch<float, uint16_t>(a, dtype, n, st) : launch<float, uint32_t>(a, dtype, n, st);
   return narrow ? launch<bf16_tag, uint16_t>(a, dtype, n, st) : launch<bf16_tag, uint32_t>(a, dtype, n, st);
+}
+
+extern "C" int ls_set_process_policy(int policy) {
+  if (policy < 0 || policy > 2) return (int)LS_ERR_INVALID_ARG;
+  g_policy.store(policy, std::memory_order_relaxed);
+  return (int)LS_OK;
 }

@@ -83,6 +83,13 @@ __device__ __forceinline__ void load32_plain(const void* p, uint32_t (&w)[8]) {
                : "l"(p), "l"(stream_policy())
                : "memory");
 }
+// And with no wish about L2.
+__device__ __forceinline__ void load32_normal(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
 // And where the line is read again soon: it leaves L2 last.
 __device__ __forceinline__ void load32_keep(const void* p, uint32_t (&w)[8]) {
   uint64_t pol;
@@ -92,16 +99,24 @@ __device__ __forceinline__ void load32_keep(const void* p, uint32_t (&w)[8]) {
                : "l"(p), "l"(pol)
                : "memory");
 }
-enum { LOAD_ONCE, LOAD_PLAIN, LOAD_KEEP };
+__device__ __forceinline__ void store32_normal(void* p, const uint32_t (&w)[8]) {  // may be read again from L2
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+enum { LOAD_ONCE, LOAD_PLAIN, LOAD_KEEP, LOAD_NORMAL };
 template <int kHow>
 __device__ __forceinline__ void load_as(const void* p, uint32_t (&w)[8]) {
   if (kHow == LOAD_ONCE)
     load32(p, w);
   else if (kHow == LOAD_PLAIN)
     load32_plain(p, w);
-  else
+  else if (kHow == LOAD_KEEP)
     load32_keep(p, w);
+  else
+    load32_normal(p, w);
 }
+// A store whose line leaves L2 first.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -301,10 +316,13 @@ struct Run {
     }
   }
   // Writes unit u of an output row with this row's indices (`same`: and its alignment).
-  __device__ __forceinline__ void store(Raw* out, bool same, int u, const uint32_t (&w)[8]) const {
+  __device__ __forceinline__ void store(Raw* out, bool same, int u, const uint32_t (&w)[8], bool keep = false) const {
     const int64_t j = index(u);
     if (same && full(u)) {
-      store32(out + j, w);
+      if (keep)
+        store32_normal(out + j, w);
+      else
+        store32(out + j, w);
     } else {
       Raw e[kN];
       memcpy(e, w, 32);

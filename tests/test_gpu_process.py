@@ -20,6 +20,15 @@ def _lib():
     ls.load_library()
 
 
+@pytest.fixture(autouse=True, params=[1, 2], ids=["one-kernel", "pair"])
+def policy(request):
+    """Every test runs with either choice of kernels forced."""
+    import logits_sampling_gb300 as ls
+    ls.set_process_policy(request.param)
+    yield
+    ls.set_process_policy(0)
+
+
 def _i32(v):
     import torch
     return None if v is None else torch.from_numpy(np.ascontiguousarray(v, np.int32)).cuda()
@@ -326,6 +335,21 @@ def test_offsets_past_32_bits():
     ls.process_logits(x, rows, p, token_to_request_index=t2r, out=x)
     got = x[-3:].float().cpu().numpy()
     _compare(got, host, [R.process_row(h, bias={V - 1: 1.5}) for h in host], "bf16")
+
+
+def test_the_choice_by_batch_size_changes_nothing():
+    import torch
+    import logits_sampling_gb300 as ls
+    x = (torch.randn(400, 128256, device="cuda") * 3).to(torch.bfloat16)
+    hist = torch.randint(0, 128256, (400, 50), dtype=torch.int32, device="cuda")
+    ones = torch.ones(400, device="cuda")
+    p = ls.LogitsParams(tokens=hist, seq_lens=(ones * 50).int(), repetition_penalty=ones * 1.25, frequency_penalty=ones)
+    forced = ls.process_logits(x, 400, p)
+    ls.set_process_policy(0)
+    assert torch.equal(ls.process_logits(x, 400, p), forced)
+    assert torch.equal(ls.process_logits(x[:3], 3, ls.LogitsParams(
+        tokens=hist[:3], seq_lens=(ones[:3] * 50).int(), repetition_penalty=ones[:3] * 1.25,
+        frequency_penalty=ones[:3])), forced[:3])
 
 
 def test_on_another_stream_and_in_a_graph():

@@ -52,6 +52,13 @@ def test_process_refusals(lib):
         assert call(**kw) == 1, kw
 
 
+def test_process_policy_values(lib):
+    for bad in (-1, 3, 8):
+        assert lib.ls_set_process_policy(bad) == 1, bad
+    for good in (1, 2, 0):
+        assert lib.ls_set_process_policy(good) == 0, good
+
+
 def test_top_refusals(lib):
     def call(logits=FAKE, dt=1, rows=4, V=400, stride=400, n=4, gather=None, k=4, T=1.0, ids=FAR, lp=FAR):
         return lib.ls_top_log_probs(logits, dt, rows, V, stride, n, gather, k, T, ids, lp, None, None, None)
