@@ -377,7 +377,7 @@ constexpr int kDistillThreads = 256;
 template <typename TIn, bool kGrad>
 static ls_status launch(const DistillArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
-  const StreamPlan plan = plan_stream(n, a.vocab, dtype, kGrad ? kRunTwice : kRunOnce);
+  const StreamPlan plan = plan_stream(n, a.vocab, dtype, kGrad ? kRunTwice : kRunOnce, 512 / kDistillThreads);
   const size_t smem = ((size_t)plan.upc + 127) / 128 * 16;  // a bit per unit
   return launch_rows(distill_kernel<TIn, kGrad, kDistillThreads>, a, plan, kDistillThreads, smem, n, st, done);
 }

@@ -427,15 +427,19 @@ static inline int64_t row_units(int64_t vocab, ls_dtype dtype) {  // at the wors
 }
 
 // The fewest CTAs per row that keep a CTA's run within `most` bytes and, while
-// runs stay above kRunLeast bytes, give each SM kRowsPerSm CTAs' worth of work.
+// runs stay above kRunLeast bytes, give each SM `per_sm` CTAs (half of what it
+// holds).  Measured on 128256 bf16 entries a row, us with 1 / 2 / 4 / 8 CTAs per
+// row: the 20 best of 8 rows 16.1 / 12.7 / 9.7 / 8.4, of 150 26.3 / 18.2 / 16.4 /
+// 20.7, of 400 30.9 / 28.2 / 32.7 / 49.3; the distillation loss of 8 rows 12.8 /
+// 9.4 / 7.2 / 5.9, of 150 16.3 / 13.1 / 11.5 / 15.0, of 400 21.4 / 25.1 / 25.7 /
+// 33.5.
 constexpr int64_t kRunLeast = 16 * 1024;
-constexpr int kCtasPerSm = 4;
 
-static inline StreamPlan plan_stream(int32_t n, int64_t vocab, ls_dtype dtype, int64_t most) {
+static inline StreamPlan plan_stream(int32_t n, int64_t vocab, ls_dtype dtype, int64_t most, int per_sm) {
   const int64_t units = row_units(vocab, dtype), sms = device_attr<cudaDevAttrMultiProcessorCount>();
   int c = 1;
   while (c < kMaxCluster && (units + c - 1) / c * 32 > most) c *= 2;
-  while (c < kMaxCluster && (int64_t)n * c < kCtasPerSm * sms && units * 32 / (2 * c) >= kRunLeast) c *= 2;
+  while (c < kMaxCluster && (int64_t)n * c < per_sm * sms && units * 32 / (2 * c) >= kRunLeast) c *= 2;
   return StreamPlan{c, (int)((units + c - 1) / c)};
 }
 

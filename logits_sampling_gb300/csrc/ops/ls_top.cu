@@ -443,7 +443,7 @@ constexpr int64_t kRunTop = 640 * 1024;  // bytes of a CTA's run at most
 template <typename TIn>
 static ls_status launch_top(const TopArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   static std::atomic<int> done[kMaxDevices];
-  const StreamPlan plan = plan_stream(n, a.vocab, dtype, kRunTop);
+  const StreamPlan plan = plan_stream(n, a.vocab, dtype, kRunTop, 512 / kTopThreads);
   // a key per stage of every thread; the entries of every CTA, padded to a power of two
   const size_t stages = ((size_t)plan.upc + kStage * kTopThreads - 1) / (kStage * kTopThreads);
   const size_t maxima = stages * kTopThreads * sizeof(uint16_t);
