@@ -57,7 +57,7 @@ struct TopShared {
   unsigned int total;  // keys sent to this CTA
   int count;           // keys of this CTA
   int base;            // their place among those sent
-  unsigned long long keys[kLocal];
+  alignas(16) unsigned long long keys[kLocal];
 };
 
 // Block-wide sum of small counts.
@@ -72,30 +72,29 @@ __device__ __forceinline__ int block_count(int v, int* red) {
 
 __device__ __forceinline__ uint16_t stage_key(float v) { return (uint16_t)(f32_key(v) >> 16); }
 
-// Entry e of a unit for an index that is not known beforehand (local memory).
+// Entry e of a unit for an index that is not known beforehand.
 template <typename TIn>
 __device__ __forceinline__ float entry_at(const uint32_t (&w)[8], int e) {
-  if (Unit<TIn>::kN == 8) return __uint_as_float(w[e]);
-  const uint32_t word = w[e >> 1];
+  const int at = Unit<TIn>::kN == 8 ? e : e >> 1;
+  uint32_t word = w[0];
+#pragma unroll
+  for (int q = 1; q < 8; ++q) word = select_word(word, w[q], at == q);
+  if (Unit<TIn>::kN == 8) return __uint_as_float(word);
   return __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
 }
 
-// Reads the stage that begins with unit u again: f(value, place in the run) for
-// each entry at or above `least`.  Few are: their bits are gathered first and
-// then walked, in little code (code that runs once per row is paid for in
-// instruction fetches).
+// f(value, place in the run) for each entry at or above `least` of the stage that
+// begins with unit u and has the words w.  Few are: their bits are gathered
+// first and then walked, in little code (code that runs once per row is paid for
+// in instruction fetches).
 template <typename TIn, int T, typename F>
-__device__ __forceinline__ void visit_stage(const Run<TIn, T>& run, int u, float least, F f) {
+__device__ __forceinline__ void visit_words(const Run<TIn, T>& run, int u, const typename Run<TIn, T>::Stage& w, float least,
+                                            F f) {
   constexpr int kN = Unit<TIn>::kN;
-  typename Run<TIn, T>::Stage w;
   uint32_t hits[kStage];
 #pragma unroll
   for (int k = 0; k < kStage; ++k) {
     hits[k] = 0u;
-    if (u + k * T < run.n) run.load(u + k * T, w[k]);
-  }
-#pragma unroll
-  for (int k = 0; k < kStage; ++k) {
     if (u + k * T >= run.n) break;
 #pragma unroll
     for (int q = 0; q < kN / 2; ++q) {
@@ -104,10 +103,12 @@ __device__ __forceinline__ void visit_stage(const Run<TIn, T>& run, int u, float
       hits[k] |= (x >= least ? 1u : 0u) << (2 * q) | (y >= least ? 2u : 0u) << (2 * q);
     }
   }
-#pragma unroll 1
+  // Their values by a chain of selects: an index into the words would put them,
+  // and with them the whole stream, into local memory.
+#pragma unroll
   for (int k = 0; k < kStage; ++k)
 #pragma unroll 1
-    for (uint32_t h = hits[k]; h; h &= h - 1) {
+    for (uint32_t h = u + k * T < run.n ? hits[k] : 0u; h; h &= h - 1) {
       const int e = __ffs((int)h) - 1;
       f(entry_at<TIn>(w[k], e), (u + k * T) * kN + e);
     }
@@ -118,7 +119,13 @@ template <typename TIn, int T, typename F>
 __device__ __forceinline__ void visit_stages(const Run<TIn, T>& run, const uint16_t* stages, float least, F f) {
   const uint16_t least_key = stage_key(least);
   for (int b = threadIdx.x, u = threadIdx.x; u < run.n; b += T, u += kStage * T)
-    if (stages[b] >= least_key) visit_stage<TIn, T>(run, u, least, f);
+    if (stages[b] >= least_key) {
+      typename Run<TIn, T>::Stage w;
+#pragma unroll
+      for (int k = 0; k < kStage; ++k)
+        if (u + k * T < run.n) run.load(u + k * T, w[k]);
+      visit_words<TIn, T>(run, u, w, least, f);
+    }
 }
 
 // The run's k best exactly, for any number of ties: `bound` has at least k
@@ -279,7 +286,8 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
   }
   if (run.n > 0) stages[(run.n - 1) / (kStage * T) * T + tid] = 0;  // the last stage need not have units of every warp
   const float c = kLog2e / a.temperature;
-  float mine;  // this thread's maximum
+  float mine;  // this thread's maximum, and the stage that holds it
+  int best;
   float2 mine_ms;
   // NaN logits: the first pass takes them as they come, and a run whose sum is
   // NaN is taken again with each of them read as -inf.
@@ -288,6 +296,7 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
     OnlineSum acc;
     acc.init(c);
     mine = kNegInf;
+    best = -1;
     run.stream(first, [&](int u, typename Run<TIn, T>::Stage& v) {
       float um = kNegInf;
 #pragma unroll
@@ -297,7 +306,10 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
       }
       // u = tid + stage * kStage * T
       stages[(u - tid) / kStage + tid] = stage_key(um);
-      mine = fmaxf(mine, um);
+      if (um > mine) {
+        mine = um;
+        best = u;
+      }
       acc.raise(um);
 #pragma unroll
       for (int q = 0; q < kStage; ++q) acc.template add<TIn>(v[q]);
@@ -308,6 +320,14 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
     __syncthreads();  // sh.red is read
   }
   let_next_start();
+  // Most stages that reach the bound are some thread's best (for k = 64 of 128256
+  // entries 73 of 107, for k = 20 34 of 38): read those again while the bound is
+  // worked out.
+  if (best >= 0) {
+#pragma unroll
+    for (int q = 0; q < kStage; ++q)
+      if (best + q * T < run.n) run.load(best + q * T, first[q]);
+  }
   const int warps = min((T / 32), (run.n + 31) / 32);
   float bound = kPosInf;
   if (warp < warps) {
@@ -355,10 +375,14 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
       if (at < kLocal) sh.keys[at] = argmax_key(v, run.j0 + place);
     }
   };
-  // List the stages first (eight keys of any thread's at a time), then read them
-  // again, one per thread: a thread reading its own as it met them would wait
-  // for memory once per stage.
+  // The other stages are listed first (eight keys of any thread's at a time) and
+  // then read again, one per thread: a thread reading its own as it met them
+  // would wait for memory once per stage.
   const uint16_t bound_key = stage_key(bound);
+  const int own = (best - tid) / kStage + tid;  // the place of this thread's best stage
+  const bool has_own = best >= 0 && stage_key(mine) >= bound_key;
+  if (has_own) stages[own] = 0;
+  __syncthreads();
   const int slots = (run.n + kStage * T - 1) / (kStage * T) * T;
   for (int q = tid * 8; q < slots; q += T * 8) {
     const uint4 eight = *reinterpret_cast<const uint4*>(&stages[q]);
@@ -376,16 +400,24 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
   }
   __syncthreads();
   const int listed = sh.candidates;
-  if (listed <= kCandidates) {
-    for (int q = tid; q < listed; q += T) {
-      const int b = (int)sh.stage[q], who = b % T;
-      visit_stage<TIn, T>(run, (b - who) * kStage + who, bound, take);
-    }
-  } else {
-    visit_stages<TIn, T>(run, stages, bound, take);
+  int u = has_own ? best : -1;
+#pragma unroll 1
+  for (int q = tid;; q += T) {  // its own, then of the list
+    if (u >= 0) visit_words<TIn, T>(run, u, first, bound, take);
+    if (listed > kCandidates || q >= listed) break;
+    const int b = (int)sh.stage[q], who = b % T;
+    u = (b - who) * kStage + who;
+#pragma unroll
+    for (int k = 0; k < kStage; ++k)
+      if (u + k * T < run.n) run.load(u + k * T, first[k]);
   }
+  if (listed > kCandidates) visit_stages<TIn, T>(run, stages, bound, take);
   __syncthreads();
-  if (sh.count > kLocal) select_ties<TIn, T>(run, stages, k, bound, sh);
+  if (sh.count > kLocal) {
+    if (has_own) stages[own] = stage_key(mine);
+    __syncthreads();
+    select_ties<TIn, T>(run, stages, k, bound, sh);
+  }
   const int n_local = sh.count;
   // to the first CTA, over its stage maxima
   unsigned long long* all = reinterpret_cast<unsigned long long*>(dyn_smem);
@@ -414,11 +446,16 @@ __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int u
     lp[at] = (v == M ? 0.f : (v - M) / a.temperature) - lnS;
   };
   if (n <= kRankMost) {
+    if (tid == 0 && (n & 1)) all[n] = 0ull;  // pairs: below every key
+    __syncthreads();
     for (int q = tid; q < n; q += T) {
       const unsigned long long key = all[q];
       int at = 0;
-#pragma unroll 8
-      for (int o = 0; o < n; ++o) at += all[o] > key;
+#pragma unroll 4
+      for (int o = 0; o < n; o += 2) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&all[o]);
+        at += (two.x > key) + (two.y > key);
+      }
       if (at < k) put(at, key);
     }
   } else {
