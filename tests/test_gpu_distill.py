@@ -273,6 +273,19 @@ def test_offsets_past_32_bits():
     _check(host, ids, lp, 1.0, "bucket", None, None, (f(loss), grad, f(loss2), f(grad2), 0), "bf16")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_largest_vocab(dtype):
+    import logits_sampling_gb300 as ls
+    V = ls.row_ops_max_vocab(ls.LS_DTYPE_BF16)
+    rng = np.random.default_rng(0)
+    x = R.to_dtype(rng.standard_normal((1, V)) * 3, dtype)
+    ids, lp = _targets(rng, x, 40, 1.0)
+    got = _calls(x, R.device_matrix(x, dtype, 1, 1), ids, lp, 1.0, "bucket", None, None)
+    _check(x, ids, lp, 1.0, "bucket", None, None, got, dtype)
+    with pytest.raises(ls.LSError):
+        ls.distill_loss(R.device_matrix(np.zeros((1, V + 1)), dtype), _dev(ids, np.int32), _dev(lp, np.float32))
+
+
 def test_same_bits_every_time_on_any_stream():
     import torch
     import logits_sampling_gb300 as ls

@@ -147,6 +147,18 @@ def test_offsets_past_32_bits():
     _check((ids[-2:], lp[-2:], lse[-2:], 0), host, 3, 1.0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_largest_vocab(dtype):
+    import logits_sampling_gb300 as ls
+    V = ls.row_ops_max_vocab(ls.LS_DTYPE_BF16)
+    assert V == ls.row_ops_max_vocab(ls.LS_DTYPE_F32) >= 1 << 22
+    rng = np.random.default_rng(0)
+    x = R.to_dtype(rng.standard_normal((2, V)) * 3, dtype)
+    _check(_run(R.device_matrix(x, dtype, 1, 1), 100), x, 100, 1.0)
+    with pytest.raises(ls.LSError):
+        ls.top_log_probs(R.device_matrix(np.zeros((1, V + 1)), dtype), 3)
+
+
 def test_same_bits_every_time_on_any_stream():
     import torch
     import logits_sampling_gb300 as ls
