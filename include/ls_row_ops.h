@@ -16,9 +16,8 @@
  *
  * Every call is asynchronous on the caller's stream, allocates nothing, never
  * synchronises with the host and launches one kernel (ls_process_logits on large
- * batches: two).  Buffers are device
- * memory owned by the caller; parameter structs are small host structs of
- * device pointers.  Results do not depend on the order in which CTAs run: the
+ * batches: two).  Buffers are device memory owned by the caller; parameter
+ * structs are small host structs of device pointers.  Results do not depend on the order in which CTAs run: the
  * same inputs give the same bits.
  */
 #ifndef LS_ROW_OPS_H
@@ -38,16 +37,17 @@ enum { LS_ROW_ERR_BAD_MASK = 8 };
 typedef struct {
   const int32_t* tokens;       /* [num_requests, token_stride]: each request's ids, prompt first; NULL: no penalties */
   int64_t token_stride;        /* >= token_capacity */
-  int32_t token_capacity;      /* ids that a row of `tokens` may hold; lengths are clamped to it */
+  int32_t token_capacity;      /* ids that a row of `tokens` may hold (< 2^30); lengths are clamped to it */
   const int32_t* prompt_lens;  /* ids of the prompt (NULL: 0) */
   const int32_t* seq_lens;     /* ids in all, prompt included (may be NULL when row_lens is given) */
   const float* repetition;     /* rho > 0; NULL: 1 */
   const float* presence;       /* NULL: 0 */
   const float* frequency;      /* NULL: 0 */
-  const int32_t* bias_offsets; /* [num_requests + 1]: request r owns entries [offsets[r], offsets[r+1]); NULL: none */
+  const int32_t* bias_offsets; /* [num_requests + 1]: request r owns entries [offsets[r], offsets[r+1]), clamped to
+                                  [0, bias_count); NULL: none */
   const int32_t* bias_ids;     /* [bias_count], distinct within a request */
   const float* bias_values;    /* [bias_count] */
-  int32_t bias_count;
+  int32_t bias_count;          /* < 2^30 */
   int32_t num_requests;
 } ls_logits_params;
 

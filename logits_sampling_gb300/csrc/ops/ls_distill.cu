@@ -13,7 +13,7 @@
 // and the at most 256 ids follow one by one: g / T * (alpha exp((x - M) / T) -
 // p), alpha = A / S.  M_r, kappa, M, alpha and the scale of p are the row's
 // `stats`: the backward pass (distill_backward_kernel) reads them and nothing
-// else of the forward pass, and is one sweep over the logits in tiles.  In the
+// else of the forward pass, and is one sweep over the logits.  In the
 // call that gives both, each CTA reads its run a second time for the gradient;
 // runs are short enough that what is in flight stays in L2.
 #include "ls_stream.cuh"
@@ -110,6 +110,13 @@ __device__ __forceinline__ uint32_t held_entries(const DistillShared& sh, int u)
   return 0u;
 }
 
+// Bound by DRAM, and by rows that start and end together: the loss of 2048 x
+// 128256 bf16 takes 87 us (6.0 TB/s, 0.90 of the measured copy rate), of 600 such
+// rows, one wave, 27 us (5.6 TB/s), of 1024 x 262144 fp32 163 us (6.6 TB/s, 0.98).
+// With the gradient the last takes 406 us (5.3 TB/s, 0.79: a quarter of the second
+// read misses L2, and each row waits once for its whole cluster; fewer CTAs per
+// SM, 441 us with three and 549 with two, lose more than they hit), 2048 x 128256
+// bf16 204 us (5.1 TB/s).
 template <typename TIn, bool kGrad, int T>
 __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs a, int upc) {
   using E = Elem<TIn>;
@@ -308,21 +315,27 @@ __global__ void __launch_bounds__(T, 1024 / T) distill_kernel(const DistillArgs 
   }
 }
 
-// The backward pass alone: kBackUnits units per thread, loaded to registers
-// before anything is written (the gradient may replace the logits).
+// The backward pass alone, in runs of a row.  In place (the gradient may replace
+// the logits) each unit is read before the same thread writes it, and the logits
+// at the ids are read before anything is written.  Bound by DRAM: 2048 x 128256
+// bf16 156 us (6.7 TB/s, the measured copy rate), 1024 x 262144 fp32 312 us; 193
+// and 313 in tiles of 512 units held in registers, which pay a tile's start and
+// ids for 16 KB.  Runs of 1024 units 160 and 322 us, of 4096 162 and 315.  Batches
+// that would leave SMs idle have runs of one stage.
 constexpr int kBackThreads = 256;
-constexpr int kBackUnits = 2;
+constexpr int kBackRun = 2048;  // units of a CTA's run
+static_assert(kBackThreads >= LS_MAX_TOP, "a thread per teacher entry");
 
 template <typename TIn>
-__global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const DistillArgs a, int tiles) {
+__global__ void __launch_bounds__(kBackThreads, 4) distill_backward_kernel(const DistillArgs a, int runs, int upc) {
   using E = Elem<TIn>;
   using Raw = typename E::Raw;
   const int tid = threadIdx.x;
-  const int64_t i = blockIdx.x / (unsigned)tiles;
+  const int64_t i = blockIdx.x / (unsigned)runs;
   wait_for_previous();
   let_next_start();
   Run<TIn, kBackThreads> run;
-  run.init(a.logits, i, a.row_stride, a.vocab, kBackThreads * kBackUnits, (int)(blockIdx.x % (unsigned)tiles));
+  run.init(a.logits, i, a.row_stride, a.vocab, upc, (int)(blockIdx.x % (unsigned)runs));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
   const float g = (a.weights ? a.weights[i] : 1.f) * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
   const bool same = run.aligned_with(grad);
@@ -331,10 +344,8 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
     for (int u = tid; u < run.n; u += kBackThreads) run.store(grad, same, u, z);
     return;
   }
-  uint32_t v[kBackUnits][8];
-#pragma unroll
-  for (int k = 0; k < kBackUnits; ++k)
-    if (tid + k * kBackThreads < run.n) run.template load<LOAD_PLAIN>(tid + k * kBackThreads, v[k]);
+  typename Run<TIn, kBackThreads>::Stage first;
+  run.template prefetch<LOAD_PLAIN>(tid, first);
   const RowStats st = a.stats_in[i];
   const float c = kLog2e / a.temperature;
   int id = -1;
@@ -352,22 +363,28 @@ __global__ void __launch_bounds__(kBackThreads) distill_backward_kernel(const Di
   ExpAgainst against;
   against.init(st.Mr, c);
   const float coef = g * st.kappa * against.scale;
-  __syncthreads();  // every load of the tile is done
+  __syncthreads();
+  run.template stream<LOAD_PLAIN>(first, [&](int u, typename Run<TIn, kBackThreads>::Stage& v) {
+    const bool whole = run.whole(u) && same;
 #pragma unroll
-  for (int k = 0; k < kBackUnits; ++k)
-    if (tid + k * kBackThreads < run.n) {
+    for (int k = 0; k < kStage; ++k) {
+      const int uk = u + k * kBackThreads;
       Unit<TIn>::clean(v[k]);
       unit_grad<TIn>(v[k], against, coef);
-      run.store(grad, same, tid + k * kBackThreads, v[k]);
+      if (whole)
+        store32(grad + run.index(uk), v[k]);
+      else if (uk < run.n)
+        run.store(grad, same, uk, v[k]);
     }
+  });
   __syncthreads();
   if (id >= 0) grad[id] = E::put(top);
 }
 
 // Bytes of a CTA's run at most.  In the call that reads it twice the runs in
-// flight share L2 with the gradients being written: 1024 x 262144 fp32 takes
-// 394 us with runs of 128 KB (a cluster of 8), 433 with 256 KB.
-constexpr int64_t kRunTwice = 256 * 1024;
+// flight share L2 with the gradients being written: 2048 x 128256 bf16 takes 204
+// us with runs of up to 128 KB, 227 with 256 KB and 215 with 64 KB.
+constexpr int64_t kRunTwice = 128 * 1024;
 constexpr int64_t kRunOnce = 640 * 1024;
 
 // CTAs of 256 threads, four to an SM (128 threads, eight to an SM: 42 us against
@@ -390,12 +407,15 @@ static ls_status dispatch(const DistillArgs& a, ls_dtype dtype, int32_t n, void*
 
 static ls_status dispatch_backward(const DistillArgs& a, ls_dtype dtype, int32_t n, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t tiles = (row_units(a.vocab, dtype) + kBackThreads * kBackUnits - 1) / (kBackThreads * kBackUnits);
-  if (tiles * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(tiles * n));
+  const int64_t units = row_units(a.vocab, dtype);
+  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
+  const int upc = (units + kBackRun - 1) / kBackRun * n >= 8 * sms ? kBackRun : kBackThreads * kStage;
+  const int64_t runs = (units + upc - 1) / upc;
+  if (runs * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(runs * n));
   return dtype == LS_DTYPE_BF16
-             ? launch_kernel(distill_backward_kernel<bf16_tag>, grid, kBackThreads, 1, 0, st, a, (int)tiles)
-             : launch_kernel(distill_backward_kernel<float>, grid, kBackThreads, 1, 0, st, a, (int)tiles);
+             ? launch_kernel(distill_backward_kernel<bf16_tag>, grid, kBackThreads, 1, 0, st, a, (int)runs, upc)
+             : launch_kernel(distill_backward_kernel<float>, grid, kBackThreads, 1, 0, st, a, (int)runs, upc);
 }
 
 // The checks that the three calls share.

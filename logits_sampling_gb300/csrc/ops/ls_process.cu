@@ -1,22 +1,24 @@
 // ls_process.cu -- penalties, biases and masks of allowed tokens on logits
 // rows (ls_process_logits).
 //
-// A row is cut into tiles, one CTA each: kUnits 32-byte units per thread,
-// loaded to registers at the start and written at the end (four, or one where
-// that leaves SMs without a CTA).  In between, the few
-// entries that the history or a bias touches are worked out on the side:
-//  1. Each unit takes -inf where the mask says so and is written: entries that
-//     nothing touches keep their bits.
-//  2. Meanwhile the request's history arrives (every tile of the row reads all
-//     of it: at the lengths that occur it is small against the row).  The ids of
-//     the CTA's own tile go to a table with one slot per entry: bit 0 says that
-//     the id occurs, the bits above count its occurrences past the prompt.  An
-//     id's first occurrence lists the entry.
-//  3. One thread per listed entry, and one per bias, reads the logit and the
-//     slot, works out the new value in fp32 and writes it over the copy, unless
-//     the mask forbids the id.  (In place the logit is still there: step 1
-//     wrote the same bits, or -inf where the mask forbids it.)
-// A slot of 16 bits holds the counts of a history of fewer than 2^15 ids.
+// Most entries are copied bit for bit, or replaced by -inf where the mask
+// forbids them; the few that the history or a bias touches are worked out on
+// the side, in fp32 with one rounding to the type of the logits:
+//     y = (x > 0 ? x / rho : x rho) - freq n - pres [n > 0] + bias
+// (the quotient for ids that occur at all, n the occurrences past the prompt).
+// Two forms, chosen in launch():
+//
+// One kernel (process_kernel).  A row is cut into tiles, one CTA each: kUnits
+// 32-byte units per thread (four, or one where that leaves SMs without a CTA),
+// loaded to registers, masked and written.  Meanwhile the request's history
+// arrives: every tile of the row reads all of it and marks the ids of its own
+// entries in a table in shared memory.  Then one thread per touched entry, and
+// one per bias, works out the new value and writes it over the copy.
+//
+// A pair for batches that fill the GPU.  copy_kernel does the masked copy at
+// the speed of memory; settle_kernel, one CTA per row, builds a hash table of
+// the row's ids while the copies are still being written, and then writes the
+// touched entries' new values over them.
 #include "ls_stream.cuh"
 
 namespace lsg {
@@ -26,6 +28,8 @@ constexpr int kProcThreads = 256;
 constexpr int kHistoryBatch = 8;  // history ids of a thread in flight
 constexpr int kSettleBatch = 4;   // touched entries of a thread in flight
 constexpr int kListed = 4096;     // touched entries listed; past it step 3 walks the table
+
+constexpr int32_t kMostListed = 1 << 30;  // ids of a history, or biases: counts and strides stay within 32 bits
 
 struct ProcessArgs {
   const void* logits;
@@ -107,7 +111,7 @@ struct RowPenalties {
       history = a.p.tokens + r * a.p.token_stride;
     }
     if (a.p.bias_offsets) {
-      b_lo = max(a.p.bias_offsets[r], 0);
+      b_lo = min(max(a.p.bias_offsets[r], 0), a.p.bias_count);
       b_hi = min(a.p.bias_offsets[r + 1], a.p.bias_count);
     }
   }
@@ -133,6 +137,25 @@ __device__ __forceinline__ void fail_run(const ProcessArgs& a, const Run<TIn, T>
   if (threadIdx.x == 0 && first && a.error_word) atomicOr(a.error_word, bad);
 }
 
+// One tile:
+//  1. Each unit takes -inf where the mask says so and is written: entries that
+//     nothing touches keep their bits.
+//  2. The ids of the CTA's own tile go to a table with one slot per entry: bit 0
+//     says that the id occurs, the bits above count its occurrences past the
+//     prompt (16-bit slots for histories of fewer than 2^15 ids).  An id's first
+//     occurrence lists the entry.
+//  3. One thread per listed entry, and one per bias, reads the logit and the
+//     slot and writes the new value over the copy, unless the mask forbids the
+//     id.  (In place the logit is still there: step 1 wrote the same bits, or -inf
+//     where the mask forbids it.)
+// Bound by latency: a tile's life is a chain of reads (row, request, history,
+// logits again) beside 2 x 32 KB of copying, four tiles to an SM.  1 x 32000 bf16
+// with 256 ids 3.2 us, 63 x 32003 with 2048 ids 7.5 us, 256 x 128256 with 8192
+// ids 45 us (3.0 TB/s; every tile marks its share of 2 M ids; with 512 ids 32 us).
+// Measured against it on the last: tiles of 512 threads 42 us (but 36 against 34
+// with 2048 ids); the tile's logits in shared memory and settled there 49 us
+// (72 KB of it per CTA leaves L1 too small for the loads in flight); a hash table
+// in place of a slot per entry 52 us.
 template <typename TIn, typename Slot, int kUnits>
 __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessArgs a, int tiles) {
   using E = Elem<TIn>;
@@ -179,7 +202,13 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
       held[q] = t < L ? history[t] : -1;
     }
   };
-  auto place = [&](int32_t id) { return id >= 0 && id < run.V ? run.place(id) : -1; };
+  // the tile's entry of an id, -1 for an id of another tile or of none
+  const uint32_t least = (uint32_t)max(run.j0, (int64_t)0);
+  const uint32_t span = run.n > 0 ? (uint32_t)(min(run.index(run.n), run.V) - (int64_t)least) : 0u;
+  auto place = [&](int32_t id) {
+    const uint32_t e = (uint32_t)id - least;
+    return e < span ? (int)e : -1;
+  };
   int bias_e = -1;
   float bias_v = 0.f;
   if (any) {
@@ -226,14 +255,14 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessA
   }
   __syncthreads();  // also: the copies are written before their touched entries are
   auto allowed = [&](int e) {
-    const int64_t j = run.j0 + e;
+    const uint32_t j = least + e;
     return !mask || (__ldg(mask + (j >> 5)) >> (j & 31) & 1u) != 0u;
   };
   // the new value of entry e from its logit (called by one thread per entry)
   auto settle = [&](int e, float x, float b, bool has_bias) {
-    out[run.j0 + e] = E::put(pen.value(x, table[e], b, has_bias));
+    out[least + e] = E::put(pen.value(x, table[e], b, has_bias));
   };
-  auto logit = [&](int e) { return E::get(run.row[run.j0 + e]); };
+  auto logit = [&](int e) { return E::get(run.row[least + e]); };
   auto settle_bias = [&](int e, float b) {
     const uint32_t bit = 1u << (e & 31);
     if (!(atomicOr(&settled[e >> 5], bit) & bit) && allowed(e)) settle(e, logit(e), b, true);
@@ -285,9 +314,11 @@ static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStr
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 2048;  // units of a CTA's run
 
-// Step 1 alone: the masked copy.  The run's lines that the mask leaves something
-// of are called into L2 first, one per thread: they keep DRAM busy without
-// registers to hold them, and a unit that the mask forbids entirely is not read.
+// The masked copy.  The run's lines that the mask leaves something of are called
+// into L2 first, one per thread: they keep DRAM busy without registers to hold
+// them, and a unit that the mask forbids entirely is not read.  Bound by DRAM:
+// with the kernel below 300 us on 1024 x 262144 fp32 (7.2 TB/s of logits, mask
+// and output, some of which the mask spares; 370 us in one kernel).
 template <typename TIn>
 __global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const ProcessArgs a, int runs, int upc) {
   using Raw = typename Elem<TIn>::Raw;
@@ -360,7 +391,9 @@ __global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const ProcessArgs
 // The touched entries of a row, one CTA per row.  While the copies are being
 // written it builds a hash table of the history's ids and the biases' in shared
 // memory; then it reads the copies of those that the mask allows, which are the
-// logits themselves, and writes the new values over them.
+// logits themselves, and writes the new values over them.  Bound by its scattered
+// accesses, about one per clock and SM: 300 rows of 2048 ids 24 us when it runs
+// alone.
 constexpr int kSettleThreads = 512;
 constexpr int kSettleSlots = 11776;               // two CTAs to an SM
 constexpr int kSettleIds = kSettleSlots / 4 * 3;  // ids that it takes, repeated ones and biases counted
@@ -629,6 +662,7 @@ extern "C" ls_status ls_process_logits(const void* logits, ls_dtype dtype, int64
     a.has_params = true;
     if (a.p.num_requests < 1) return LS_ERR_INVALID_ARG;
     if (!token_to_request_index && n > a.p.num_requests) return LS_ERR_INVALID_ARG;
+    if (a.p.token_capacity >= kMostListed || a.p.bias_count >= kMostListed) return LS_ERR_UNSUPPORTED;
     if (a.p.tokens && (a.p.token_capacity < 0 || a.p.token_stride < a.p.token_capacity || !(a.p.seq_lens || row_lens)))
       return LS_ERR_INVALID_ARG;
     if (a.p.bias_offsets && (a.p.bias_count < 0 || (a.p.bias_count > 0 && (!a.p.bias_ids || !a.p.bias_values))))

@@ -2,11 +2,16 @@
 // CTAs of a cluster where one CTA would be too slow or its share too large.
 //
 // The row is seen as 32-byte units aligned in global memory (16 bf16 or 8 fp32
-// entries).  CTA q of C owns a contiguous run of units; its threads take them
-// in turn, a few (a stage) at a time, with the next stage's loads in flight while one
-// is computed.  The units that lie wholly in the row are one 256-bit load, the
-// row's first and last partial unit are read entry by entry, with -inf in the
-// places outside the row.
+// entries).  CTA q of C owns a contiguous run of units; its threads take them in
+// turn, a few (a stage) at a time, with the next stage's loads in flight while
+// one is computed.  The units that lie wholly in the row are one 256-bit load,
+// the row's first and last partial unit are read entry by entry, with -inf in
+// the places outside the row.
+//
+// Registers rather than shared memory hold what is in flight: the same kernels
+// with a row's share copied to the shared memory of a cluster took 173 us
+// against 44 (20 best of 672 x 151936 bf16) and 96 against 32 (the loss there);
+// a stream alone reaches the measured copy rate this way.
 #pragma once
 
 #include "ls_row_ops.cuh"
@@ -181,6 +186,17 @@ struct Unit<float> {
   }
 };
 
+// Entry e of a unit for an index that is not known beforehand.
+template <typename TIn>
+__device__ __forceinline__ float entry_at(const uint32_t (&w)[8], int e) {
+  const int at = Unit<TIn>::kN == 8 ? e : e >> 1;
+  uint32_t word = w[0];
+#pragma unroll
+  for (int q = 1; q < 8; ++q) word = select_word(word, w[q], at == q);
+  if (Unit<TIn>::kN == 8) return __uint_as_float(word);
+  return __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
+}
+
 // exp((v - M) / T), c = log2(e) / T, for v <= M; entries at an infinite
 // maximum share it.
 __device__ __forceinline__ float rel_exp(float v, float M, float c) { return v == M ? 1.f : ex2((v - M) * c); }
@@ -335,9 +351,9 @@ struct Run {
     return ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 31u) == 0;
   }
   // Visits this thread's units in order, kStage at a time: visit(u, w) with the
-  // words of units u and u + T (units past n as -inf).  `first`
-  // has been loaded by prefetch().  A stage whose units all lie wholly in the row
-  // and the run (for the whole CTA: one branch) is loaded without further checks.
+  // words of units u and u + T (units past n as -inf); the first stage has been
+  // loaded by prefetch().  A stage whose units all lie wholly in the row and the
+  // run (for the whole CTA: one branch) is loaded without further checks.
   typedef uint32_t Stage[kStage][8];
   static constexpr int kStep = kStage * T;
   __device__ __forceinline__ bool whole(int u) const {
@@ -430,16 +446,16 @@ static inline int64_t row_units(int64_t vocab, ls_dtype dtype) {  // at the wors
 // runs stay above kRunLeast bytes, give each SM `per_sm` CTAs (half of what it
 // holds).  Measured on 128256 bf16 entries a row, us with 1 / 2 / 4 / 8 CTAs per
 // row: the 20 best of 8 rows 16.1 / 12.7 / 9.7 / 8.4, of 150 26.3 / 18.2 / 16.4 /
-// 20.7, of 400 30.9 / 28.2 / 32.7 / 49.3; the distillation loss of 8 rows 12.8 /
-// 9.4 / 7.2 / 5.9, of 150 16.3 / 13.1 / 11.5 / 15.0, of 400 21.4 / 25.1 / 25.7 /
-// 33.5.
+// 20.7, of 600 36.9 / 34.6 / 48.4, of 672 40.1 / 48.4 / 52.4; the distillation
+// loss of 8 rows 12.8 / 9.4 / 7.2 / 5.9, of 150 16.3 / 13.1 / 11.5 / 15.0, of 304
+// 20.5 / 17.3 / 23.7, of 400 22.0 / 24.9 / 27.8.
 constexpr int64_t kRunLeast = 16 * 1024;
 
 static inline StreamPlan plan_stream(int32_t n, int64_t vocab, ls_dtype dtype, int64_t most, int per_sm) {
   const int64_t units = row_units(vocab, dtype), sms = device_attr<cudaDevAttrMultiProcessorCount>();
   int c = 1;
   while (c < kMaxCluster && (units + c - 1) / c * 32 > most) c *= 2;
-  while (c < kMaxCluster && (int64_t)n * c < per_sm * sms && units * 32 / (2 * c) >= kRunLeast) c *= 2;
+  while (c < kMaxCluster && (int64_t)n * c <= per_sm * sms && units * 32 / (2 * c) >= kRunLeast) c *= 2;
   return StreamPlan{c, (int)((units + c - 1) / c)};
 }
 

@@ -281,6 +281,20 @@ def test_lengths_beyond_the_buffer_are_clamped():
     _compare(out.cpu().numpy(), c["x"], refs, "f32")
 
 
+def test_bias_offsets_outside_the_list_are_clamped():
+    import logits_sampling_gb300 as ls
+    V = 500
+    x = R.to_dtype(np.random.default_rng(3).standard_normal((5, V)), "f32")
+    # row 0 begins past the list, 1 is empty, 2 ends before it begins, 3 is the whole list, 4 is empty
+    off = _i32([0x7FFFFFF0, 3, 3, -5, 1000, 3])
+    ids, val = [7, 499, 250], [1.0, -2.0, 0.5]
+    got = ls.process_logits(R.device_matrix(x, "f32"), 5,
+                            ls.LogitsParams(bias_offsets=off, bias_ids=_i32(ids), bias_values=_f32(val))).cpu().numpy()
+    want = x.copy()
+    want[3, ids] += np.array(val, np.float32)
+    assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("cap", [32000, 70000])
 def test_one_id_repeated_through_a_long_history(cap):
     """Counts past 16 bits."""

@@ -50,6 +50,9 @@ def test_process_refusals(lib):
                {"params": params(bias_offsets=fake, bias_count=-1)},
                {"params": params(bias_offsets=fake, bias_count=3, bias_ids=fake)}):
         assert call(**kw) == 1, kw
+    big = 1 << 30  # lengths whose strides through them would pass 32 bits
+    assert call(params=params(tokens=fake, token_capacity=big, token_stride=big, seq_lens=fake)) == 2
+    assert call(params=params(bias_offsets=fake, bias_count=big, bias_ids=fake, bias_values=fake)) == 2
 
 
 def test_process_policy_values(lib):
