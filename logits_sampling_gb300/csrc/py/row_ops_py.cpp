@@ -9,7 +9,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -163,10 +163,14 @@ struct Output {
     return given;
   }
 };
+// A new tensor on the logits' device, without a turn through the dispatcher.
+at::Tensor fresh(at::IntArrayRef shape, const Matrix& m, at::ScalarType type) {
+  return at::detail::empty_cuda(shape, type, m.t->device(), std::nullopt);
+}
 Output out_matrix(PyObject* o, const Matrix& m, int64_t n, const char* what) {
   Output r;
   if (!o) {
-    r.made = at::empty({n, m.vocab}, at::TensorOptions().dtype(m.t->scalar_type()).device(m.t->device()));
+    r.made = fresh({n, m.vocab}, m, m.t->scalar_type());
     r.p = r.made.data_ptr();
     r.stride = m.vocab;
     return r;
@@ -188,7 +192,7 @@ Output out_vec(PyObject* o, const Matrix& m, at::IntArrayRef shape, at::ScalarTy
     r.p = vec<void>(o, type, what, c10::multiply_integers(shape));
     r.given = o;
   } else {
-    r.made = at::empty(shape, at::TensorOptions().dtype(type).device(m.t->device()));
+    r.made = fresh(shape, m, type);
     r.p = r.made.data_ptr();
   }
   return r;
