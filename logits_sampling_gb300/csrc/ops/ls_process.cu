@@ -25,7 +25,7 @@ namespace lsg {
 namespace ops {
 
 constexpr int kProcThreads = 256;
-constexpr int kHistoryBatch = 8;  // history ids of a thread in flight
+constexpr int kHistoryBatch = 4;  // history ids of a thread in flight (8: 2.9 -> 3.3 us for one row, 358 -> 370 for 1 GB)
 constexpr int kSettleBatch = 4;   // touched entries of a thread in flight
 constexpr int kListed = 4096;     // touched entries listed; past it step 3 walks the table
 
@@ -150,8 +150,8 @@ __device__ __forceinline__ void fail_run(const ProcessArgs& a, const Run<TIn, T>
 //     where the mask forbids it.)
 // Bound by latency: a tile's life is a chain of reads (row, request, history,
 // logits again) beside 2 x 32 KB of copying, four tiles to an SM.  1 x 32000 bf16
-// with 256 ids 3.2 us, 63 x 32003 with 2048 ids 7.5 us, 256 x 128256 with 8192
-// ids 45 us (3.0 TB/s; every tile marks its share of 2 M ids; with 512 ids 32 us).
+// with 256 ids 2.9 us, 63 x 32003 with 2048 ids 7.4 us, 256 x 128256 with 8192
+// ids 44 us (3.0 TB/s; every tile marks its share of 2 M ids; with 512 ids 31 us).
 // Measured against it on the last: tiles of 512 threads 42 us (but 36 against 34
 // with 2048 ids); the tile's logits in shared memory and settled there 49 us
 // (72 KB of it per CTA leaves L1 too small for the loads in flight); a hash table
@@ -318,7 +318,7 @@ constexpr int kCopyUnits = 2048;  // units of a CTA's run
 // into L2 first, one per thread: they keep DRAM busy without registers to hold
 // them, and a unit that the mask forbids entirely is not read.  Bound by DRAM:
 // with the kernel below 300 us on 1024 x 262144 fp32 (7.2 TB/s of logits, mask
-// and output, some of which the mask spares; 370 us in one kernel).
+// and output, some of which the mask spares; 358 us in one kernel).
 template <typename TIn>
 __global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const ProcessArgs a, int runs, int upc) {
   using Raw = typename Elem<TIn>::Raw;
@@ -626,10 +626,10 @@ static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStr
   const int64_t wide = (row_units(a.vocab, dtype) + 4 * kProcThreads - 1) / (4 * kProcThreads) * n;
   const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
   // The pair copies at the speed of memory (1024 x 262144 fp32 with histories up
-  // to 2048: 301 us against 375), but settles a row on one SM, whose scattered
+  // to 2048: 302 us against 358), but settles a row on one SM, whose scattered
   // accesses take some microseconds per thousand ids; the one kernel spreads a
-  // row's over its tiles (256 x 128256 bf16: histories up to 2048 34 us either
-  // way, up to 8192 46 us against 75).
+  // row's over its tiles (256 x 128256 bf16: histories up to 2048 33 us
+  // in one kernel and 35 in the pair, up to 512 31 and 28, up to 8192 44 and 61).
   const bool light = !a.has_params || !a.p.tokens ||
                      (int64_t)n * a.vocab * Elem<TIn>::kBytes >= (int64_t)a.p.token_capacity * kPairBytesPerId;
   const int policy = g_policy.load(std::memory_order_relaxed);
