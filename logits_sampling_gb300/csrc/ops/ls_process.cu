@@ -486,7 +486,9 @@ __global__ void __launch_bounds__(kSettleThreads, 2) settle_kernel(const Process
   // free writes itself there and sees after a barrier whether it, or an equal
   // one, is what stayed; else it moves a slot on.  At a load of 60% three
   // quarters are placed in each of the two rounds; what is left is swapped in
-  // (the table is never full, so that ends).
+  // (the table is never full, so that ends).  A batch begins when every warp has
+  // swapped in what it had left of the one before: the rounds' test and store
+  // are two accesses, and a swap between them would be overwritten.
   uint32_t id[kSettleHistory];
   auto insert = [&](uint32_t pending, uint32_t output) {  // bits: ids to insert, occurrences past the prompt
     int at[kSettleHistory];
@@ -544,7 +546,10 @@ __global__ void __launch_bounds__(kSettleThreads, 2) settle_kernel(const Process
   if (tid == 0) sh.listed = 0;
   __syncthreads();
   for (int32_t at = tid; at - tid < L; at += kSettleHistory * kSettleThreads) {
-    if (at != tid) fetch(at);
+    if (at != tid) {
+      fetch(at);
+      __syncthreads();
+    }
     uint32_t pending = 0u, output = 0u;
 #pragma unroll
     for (int q = 0; q < kSettleHistory; ++q) {
