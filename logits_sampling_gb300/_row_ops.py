@@ -132,6 +132,10 @@ class LogitsParams:
 
     def __post_init__(self):
         struct = self._marshal()  # its pointers stay valid with the tensors that the fields hold
+        devices = {t.device for t in vars(self).values() if t is not None}
+        if len(devices) > 1:
+            raise ValueError(f"fields lie on different devices: {sorted(map(str, devices))}")
+        object.__setattr__(self, "_device", devices.pop().index)
         object.__setattr__(self, "_struct", struct)
         object.__setattr__(self, "_addr", ctypes.addressof(struct))
 

@@ -27,6 +27,7 @@ decltype(&ls_distill_loss_backward) f_backward;
 decltype(&ls_distill_loss_grad) f_grad;
 PyObject* ls_error;  // the package's LSError(status, what)
 PyObject* s_addr;    // "_addr": a LogitsParams' struct
+PyObject* s_device;  // "_device": the index of the device its tensors lie on
 
 // An error on its way to Python.
 struct Fail {
@@ -134,44 +135,60 @@ Matrix matrix(PyObject* o) {
   return m;
 }
 
+// Every tensor of a call lies on the logits' device, on which its kernels run.
+void on_device(int64_t device, const Matrix& m, const char* what) {
+  if (device != m.t->get_device())
+    throw Fail{PyExc_ValueError, std::string(what) + " is on cuda:" + std::to_string(device) + ", the logits are on cuda:" +
+                                     std::to_string(m.t->get_device())};
+}
+void on_device(const at::Tensor& t, const Matrix& m, const char* what) {
+  if (!t.is_cuda()) throw Fail{PyExc_ValueError, std::string(what) + ": expected a CUDA tensor"};
+  on_device(t.get_device(), m, what);
+}
+
 // The pointer of an optional contiguous device tensor of at least n entries.
 template <typename T>
-T* vec(PyObject* o, at::ScalarType type, const char* what, int64_t n) {
+T* vec(PyObject* o, at::ScalarType type, const char* what, int64_t n, const Matrix& m) {
   if (!o) return nullptr;
   const at::Tensor& t = tensor(o, what);
   if (t.scalar_type() != type)
     throw Fail{PyExc_TypeError, std::string(what) + " must be " + (type == at::kInt ? "int32" : "float32")};
-  if (!t.is_cuda()) throw Fail{PyExc_ValueError, std::string(what) + ": expected a CUDA tensor"};
+  on_device(t, m, what);
   if (!t.is_contiguous()) throw Fail{PyExc_ValueError, std::string(what) + ": expected a contiguous tensor"};
   if (t.numel() < n)
     throw Fail{PyExc_ValueError,
                std::string(what) + " has " + std::to_string(t.numel()) + " entries, " + std::to_string(n) + " are needed"};
   return static_cast<T*>(t.data_ptr());
 }
-int32_t* i32(PyObject* o, const char* what, int64_t n) { return vec<int32_t>(o, at::kInt, what, n); }
-float* f32(PyObject* o, const char* what, int64_t n) { return vec<float>(o, at::kFloat, what, n); }
+int32_t* i32(PyObject* o, const char* what, int64_t n, const Matrix& m) { return vec<int32_t>(o, at::kInt, what, n, m); }
+float* f32(PyObject* o, const char* what, int64_t n, const Matrix& m) { return vec<float>(o, at::kFloat, what, n, m); }
 
-// An output: the caller's tensor (checked), or a new one.
+// An output: the caller's tensor (checked), or a new one, made once the call's
+// device and stream are current.
 struct Output {
   PyObject* given = nullptr;
   at::Tensor made;
   void* p = nullptr;
   int64_t stride = 0;
+  c10::SmallVector<int64_t, 2> shape;  // of a new one
+  at::ScalarType type = at::kFloat;
+  void make(const Matrix& m) {
+    if (given) return;
+    // without a turn through the dispatcher
+    made = at::detail::empty_cuda(shape, type, m.t->device(), std::nullopt);
+    p = made.data_ptr();
+  }
   PyObject* take() {  // a new reference
     if (!given) return THPVariable_Wrap(std::move(made));
     Py_INCREF(given);
     return given;
   }
 };
-// A new tensor on the logits' device, without a turn through the dispatcher.
-at::Tensor fresh(at::IntArrayRef shape, const Matrix& m, at::ScalarType type) {
-  return at::detail::empty_cuda(shape, type, m.t->device(), std::nullopt);
-}
 Output out_matrix(PyObject* o, const Matrix& m, int64_t n, const char* what) {
   Output r;
   if (!o) {
-    r.made = fresh({n, m.vocab}, m, m.t->scalar_type());
-    r.p = r.made.data_ptr();
+    r.shape = {n, m.vocab};
+    r.type = m.t->scalar_type();
     r.stride = m.vocab;
     return r;
   }
@@ -180,7 +197,7 @@ Output out_matrix(PyObject* o, const Matrix& m, int64_t n, const char* what) {
     throw Fail{PyExc_ValueError, std::string(what) + " must be [" + std::to_string(n) + ", " + std::to_string(m.vocab) +
                                      "] of the logits' type"};
   if (t.stride(1) != 1) throw Fail{PyExc_ValueError, std::string(what) + "'s rows must be contiguous (stride(1) == 1)"};
-  if (!t.is_cuda()) throw Fail{PyExc_ValueError, std::string(what) + ": expected a CUDA tensor"};
+  on_device(t, m, what);
   r.given = o;
   r.p = t.data_ptr();
   r.stride = t.size(0) <= 1 && t.stride(0) < m.vocab ? m.vocab : t.stride(0);
@@ -189,18 +206,20 @@ Output out_matrix(PyObject* o, const Matrix& m, int64_t n, const char* what) {
 Output out_vec(PyObject* o, const Matrix& m, at::IntArrayRef shape, at::ScalarType type, const char* what) {
   Output r;
   if (o) {
-    r.p = vec<void>(o, type, what, c10::multiply_integers(shape));
+    r.p = vec<void>(o, type, what, c10::multiply_integers(shape), m);
     r.given = o;
   } else {
-    r.made = fresh(shape, m, type);
-    r.p = r.made.data_ptr();
+    r.shape.assign(shape.begin(), shape.end());
+    r.type = type;
   }
   return r;
 }
 
 // The stream a call runs on: the caller's (made current, so that outputs are
-// allocated on it), or the current one.
+// allocated on it), or the current one of the logits' device.  That device is
+// the current one while this lives: launches and device attributes follow it.
 struct OnStream {
+  std::optional<c10::cuda::CUDAGuard> device;
   std::optional<c10::cuda::CUDAStreamGuard> guard;
   void* raw;
   OnStream(PyObject* o, const Matrix& m) {
@@ -215,15 +234,18 @@ struct OnStream {
         Py_DECREF(v);
         return r;
       };
-      guard.emplace(c10::cuda::CUDAStream::unpack3(attr("stream_id"), (c10::DeviceIndex)attr("device_index"),
+      on_device(attr("device_index"), m, "stream");
+      guard.emplace(c10::cuda::CUDAStream::unpack3(attr("stream_id"), m.t->device().index(),
                                                    (c10::DeviceType)attr("device_type")));
+    } else if (c10::cuda::current_device() != m.t->get_device()) {
+      device.emplace(m.t->device());
     }
     raw = (void*)c10::cuda::getCurrentCUDAStream(m.t->get_device()).stream();
   }
 };
 
 struct Teacher : ls_teacher {
-  Teacher(PyObject* ids_, PyObject* log_probs_, int64_t n) {
+  Teacher(PyObject* ids_, PyObject* log_probs_, int64_t n, const Matrix& m) {
     const at::Tensor& i = tensor(ids_, "teacher_ids");
     const at::Tensor& l = tensor(log_probs_, "teacher_log_probs");
     if (i.dim() != 2 || l.dim() != 2 || i.size(0) != n || l.size(0) != n || i.size(1) != l.size(1))
@@ -235,7 +257,8 @@ struct Teacher : ls_teacher {
       throw Fail{PyExc_ValueError, "teacher_ids and teacher_log_probs must have contiguous rows"};
     if (n > 1 && i.stride(0) != l.stride(0))
       throw Fail{PyExc_ValueError, "teacher_ids and teacher_log_probs must have one row stride"};
-    if (!i.is_cuda() || !l.is_cuda()) throw Fail{PyExc_ValueError, "teacher: expected CUDA tensors"};
+    on_device(i, m, "teacher_ids");
+    on_device(l, m, "teacher_log_probs");
     stride = n > 1 ? i.stride(0) : k;
     ids = static_cast<const int32_t*>(i.data_ptr());
     log_probs = static_cast<const float*>(l.data_ptr());
@@ -302,7 +325,6 @@ PyObject* process_logits(PyObject*, PyObject* const* args, Py_ssize_t positional
     PyObject* o[kMostArgs];
     parse(n_process, args, positional, keywords, o);
     const Matrix m = matrix(o[0]);
-    const OnStream on(o[10], m);
     const int32_t n = count32(o[1] ? integer(o[1], "n") : o[3] ? tensor(o[3], "gather_indices").numel() : m.rows, "n");
     const ls_logits_params* params = nullptr;
     PyObject* addr = nullptr;
@@ -314,6 +336,11 @@ PyObject* process_logits(PyObject*, PyObject* const* args, Py_ssize_t positional
       }
       params = static_cast<const ls_logits_params*>(PyLong_AsVoidPtr(addr));
       Py_DECREF(addr);
+      PyObject* device = PyObject_GetAttr(o[2], s_device);
+      const long index = device ? PyLong_AsLong(device) : -1;
+      Py_XDECREF(device);
+      PyErr_Clear();
+      on_device(index, m, "params");
     }
     const int32_t* mask = nullptr;
     int64_t mask_rows = 0, mask_stride = 0;
@@ -321,17 +348,19 @@ PyObject* process_logits(PyObject*, PyObject* const* args, Py_ssize_t positional
       const at::Tensor& t = tensor(o[6], "allowed_mask");
       if (t.dim() != 2 || t.scalar_type() != at::kInt || (t.size(1) > 1 && t.stride(1) != 1))
         throw Fail{PyExc_ValueError, "allowed_mask must be int32 [mask_rows, words] with contiguous rows"};
-      if (!t.is_cuda()) throw Fail{PyExc_ValueError, "allowed_mask: expected a CUDA tensor"};
+      on_device(t, m, "allowed_mask");
       mask = static_cast<const int32_t*>(t.data_ptr());
       mask_rows = t.size(0);
       mask_stride = mask_rows > 1 ? t.stride(0) : t.size(1);
     }
-    const int32_t* gather = i32(o[3], "gather_indices", n);
-    const int32_t* t2r = i32(o[4], "token_to_request_index", n);
-    const int32_t* lens = i32(o[5], "row_lens", n);
-    const int32_t* index = i32(o[7], "mask_index", n);
-    int32_t* error = i32(o[9], "error_word", 1);
+    const int32_t* gather = i32(o[3], "gather_indices", n, m);
+    const int32_t* t2r = i32(o[4], "token_to_request_index", n, m);
+    const int32_t* lens = i32(o[5], "row_lens", n, m);
+    const int32_t* index = i32(o[7], "mask_index", n, m);
+    int32_t* error = i32(o[9], "error_word", 1, m);
     Output out = out_matrix(o[8], m, n < 0 ? 0 : n, "out");
+    const OnStream on(o[10], m);
+    out.make(m);
     call("ls_process_logits", [&] {
       return f_process(m.p, m.dtype, m.rows, m.vocab, m.stride, n, gather, t2r, params, lens, mask, mask_rows,
                        mask_stride, index, out.p, out.stride, error, on.raw);
@@ -348,17 +377,20 @@ PyObject* top_log_probs(PyObject*, PyObject* const* args, Py_ssize_t positional,
     PyObject* o[kMostArgs];
     parse(n_top, args, positional, keywords, o);
     const Matrix m = matrix(o[0]);
-    const OnStream on(o[9], m);
     const int32_t k = count32(integer(o[1], "k"), "k");
     const int32_t n = count32(o[2] ? integer(o[2], "n") : o[4] ? tensor(o[4], "gather_indices").numel() : m.rows, "n");
     if (k < 1 || k > LS_MAX_TOP || n < 0)
       throw Fail{PyExc_ValueError, "k must lie in [1, " + std::to_string(LS_MAX_TOP) + "], n be 0 or more"};
     const float temperature = number(o[3], 1.f, "temperature");
-    const int32_t* gather = i32(o[4], "gather_indices", n);
-    int32_t* error = i32(o[8], "error_word", 1);
+    const int32_t* gather = i32(o[4], "gather_indices", n, m);
+    int32_t* error = i32(o[8], "error_word", 1, m);
     Output ids = out_vec(o[5], m, {n, k}, at::kInt, "out_ids");
     Output lp = out_vec(o[6], m, {n, k}, at::kFloat, "out_log_probs");
     Output lse = out_vec(o[7], m, {n}, at::kFloat, "out_lse");
+    const OnStream on(o[9], m);
+    ids.make(m);
+    lp.make(m);
+    lse.make(m);
     call("ls_top_log_probs", [&] {
       return f_top(m.p, m.dtype, m.rows, m.vocab, m.stride, n, gather, k, temperature, static_cast<int32_t*>(ids.p),
                    static_cast<float*>(lp.p), static_cast<float*>(lse.p), error, on.raw);
@@ -380,15 +412,17 @@ PyObject* distill_loss(PyObject*, PyObject* const* args, Py_ssize_t positional, 
     PyObject* o[kMostArgs];
     parse(n_loss, args, positional, keywords, o);
     const Matrix m = matrix(o[0]);
-    const OnStream on(o[9], m);
     const int32_t n = count32(m.rows, "rows");
-    const Teacher teacher(o[1], o[2], n);
+    const Teacher teacher(o[1], o[2], n, m);
     const float temperature = number(o[3], 1.f, "temperature");
     const ls_tail tail = tail_of(o[4]);
-    const float* weights = f32(o[5], "weights", n);
-    int32_t* error = i32(o[8], "error_word", 1);
+    const float* weights = f32(o[5], "weights", n, m);
+    int32_t* error = i32(o[8], "error_word", 1, m);
     Output loss = out_vec(o[6], m, {n}, at::kFloat, "out");
     Output stats = out_vec(o[7], m, {n, LS_DISTILL_STATS}, at::kFloat, "out_stats");
+    const OnStream on(o[9], m);
+    loss.make(m);
+    stats.make(m);
     call("ls_distill_loss", [&] {
       return f_loss(m.p, m.dtype, m.vocab, m.stride, n, &teacher, temperature, tail, weights,
                     static_cast<float*>(loss.p), static_cast<float*>(stats.p), error, on.raw);
@@ -405,15 +439,16 @@ PyObject* distill_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t pos
     PyObject* o[kMostArgs];
     parse(n_backward, args, positional, keywords, o);
     const Matrix m = matrix(o[0]);
-    const OnStream on(o[9], m);
     const int32_t n = count32(m.rows, "rows");
-    const Teacher teacher(o[1], o[2], n);
-    const float* stats = f32(o[3], "stats", (int64_t)n * LS_DISTILL_STATS);
-    const float* grad_loss = f32(o[4], "grad_loss", n);
+    const Teacher teacher(o[1], o[2], n, m);
+    const float* stats = f32(o[3], "stats", (int64_t)n * LS_DISTILL_STATS, m);
+    const float* grad_loss = f32(o[4], "grad_loss", n, m);
     const float temperature = number(o[5], 1.f, "temperature");
     const ls_tail tail = tail_of(o[6]);
-    const float* weights = f32(o[7], "weights", n);
+    const float* weights = f32(o[7], "weights", n, m);
     Output grad = out_matrix(o[8], m, n, "out");
+    const OnStream on(o[9], m);
+    grad.make(m);
     call("ls_distill_loss_backward", [&] {
       return f_backward(m.p, m.dtype, m.vocab, m.stride, n, &teacher, temperature, tail, weights, stats, grad_loss,
                         grad.p, grad.stride, on.raw);
@@ -430,15 +465,17 @@ PyObject* distill_loss_grad(PyObject*, PyObject* const* args, Py_ssize_t positio
     PyObject* o[kMostArgs];
     parse(n_grad, args, positional, keywords, o);
     const Matrix m = matrix(o[0]);
-    const OnStream on(o[9], m);
     const int32_t n = count32(m.rows, "rows");
-    const Teacher teacher(o[1], o[2], n);
+    const Teacher teacher(o[1], o[2], n, m);
     const float temperature = number(o[3], 1.f, "temperature");
     const ls_tail tail = tail_of(o[4]);
-    const float* weights = f32(o[5], "weights", n);
-    int32_t* error = i32(o[8], "error_word", 1);
+    const float* weights = f32(o[5], "weights", n, m);
+    int32_t* error = i32(o[8], "error_word", 1, m);
     Output loss = out_vec(o[6], m, {n}, at::kFloat, "out_loss");
     Output grad = out_matrix(o[7], m, n, "out_grad");
+    const OnStream on(o[9], m);
+    loss.make(m);
+    grad.make(m);
     call("ls_distill_loss_grad", [&] {
       return f_grad(m.p, m.dtype, m.vocab, m.stride, n, &teacher, temperature, tail, weights,
                     static_cast<float*>(loss.p), grad.p, grad.stride, error, on.raw);
@@ -501,6 +538,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_row_ops_c", "The calls of include
 
 PyMODINIT_FUNC PyInit__row_ops_c() {
   s_addr = PyUnicode_InternFromString("_addr");
+  s_device = PyUnicode_InternFromString("_device");
   for (Names* n : {&n_process, &n_top, &n_loss, &n_backward, &n_grad})
     for (int i = 0; i < n->count; ++i) n->name[i] = PyUnicode_InternFromString(n->text[i]);
   return PyModule_Create(&module);
