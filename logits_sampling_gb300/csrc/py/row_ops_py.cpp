@@ -178,8 +178,13 @@ struct Output {
     made = at::detail::empty_cuda(shape, type, m.t->device(), std::nullopt);
     p = made.data_ptr();
   }
-  PyObject* take() {  // a new reference
+  // A new reference.  To autograd a caller's tensor has been written in place: a
+  // graph that saved it says so in its backward pass.  Inference tensors have no
+  // version, and no graph can have saved one.
+  PyObject* take() {
     if (!given) return THPVariable_Wrap(std::move(made));
+    const at::Tensor& t = THPVariable_Unpack(given);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
     Py_INCREF(given);
     return given;
   }
