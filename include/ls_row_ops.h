@@ -157,8 +157,8 @@ typedef struct {
  *            student's mass outside the k ids (the term is left out where
  *            p_r = 0 or no entry above -inf lies outside them)
  * All in fp32.  NaN logits are read as -inf.  A row of weight 0 is not read:
- * loss 0, gradient 0.  A row without an entry above -inf: loss and gradient
- * NaN, LS_ROW_ERR_NO_FINITE.
+ * loss 0, gradient 0 whatever grad_loss holds.  A row without an entry above
+ * -inf: loss and gradient NaN, LS_ROW_ERR_NO_FINITE.
  *
  *   weights    device float[n] or NULL (1)
  *   out_loss   device float[n]

@@ -337,9 +337,10 @@ __global__ void __launch_bounds__(kBackThreads, 4) distill_backward_kernel(const
   Run<TIn, kBackThreads> run;
   run.init(a.logits, i, a.row_stride, a.vocab, upc, (int)(blockIdx.x % (unsigned)runs));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
-  const float g = (a.weights ? a.weights[i] : 1.f) * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
+  const float w = a.weights ? a.weights[i] : 1.f;
+  const float g = w * (a.grad_loss ? a.grad_loss[i] : 1.f) / a.temperature;
   const bool same = run.aligned_with(grad);
-  if (g == 0.f) {
+  if (w == 0.f || g == 0.f) {  // a row of weight 0 counts nothing, whatever the gradient of its loss
     uint32_t z[8] = {};
     for (int u = tid; u < run.n; u += kBackThreads) run.store(grad, same, u, z);
     return;
