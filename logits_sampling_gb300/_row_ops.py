@@ -83,6 +83,10 @@ def calls():
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with `python -m logits_sampling_gb300.build` "
                                "(there is no CPU fallback)")
+        from . import build
+        if build.binding_built_for() != build.binding_target():
+            raise RuntimeError(f"{path} was built for {build.binding_built_for() or 'an unknown torch'}, this is "
+                               f"{build.binding_target()}: run `python -m logits_sampling_gb300.build`")
         import torch  # noqa: F401  (its libraries first: the module links against them)
         spec = importlib.util.spec_from_file_location("logits_sampling_gb300._row_ops_c", path)
         module = importlib.util.module_from_spec(spec)

@@ -8,7 +8,8 @@ build is skipped when the library is newer than every source and header.
 
 The Python calls of include/ls_row_ops.h (csrc/py/row_ops_py.cpp) are a small
 extension module over torch's C++ tensors, _row_ops_c.so, compiled beside it
-with g++ against the installed torch's headers.
+with g++ against the installed torch's headers.  _row_ops_c.for says which torch
+and Python that was: with others it is compiled again, and not loaded.
 
 VARIANTS holds test-only builds of the same sources with other compile-time
 constants (never loaded by the package itself): ``reselect`` puts the top-p
@@ -17,6 +18,7 @@ all of its entries -- the path that otherwise runs only when rounding beats
 the bound's slack.
 """
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -30,6 +32,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libls_sampler.so")
 BINDING = os.path.join(PKG, "_row_ops_c.so")
+BINDING_FOR = os.path.join(PKG, "_row_ops_c.for")
 BINDING_SOURCE = os.path.join(CSRC, "py", "row_ops_py.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {"reselect": ["-DLS_TOPP_SLACK=-64.0f"]}
@@ -57,7 +60,27 @@ def _binding_command(out):
             "-ltorch_python"]
 
 
+def binding_target():
+    """The torch and the Python that an extension module is for: it is linked against their ABIs."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def binding_built_for():
+    """What binding_target() was when the extension module was compiled, "" when unknown."""
+    if not os.path.exists(BINDING_FOR):
+        return ""
+    with open(BINDING_FOR) as f:
+        return f.read().strip()
+
+
 def _binding_up_to_date():
+    if binding_built_for() != binding_target():
+        return False
     t = os.path.getmtime(BINDING) if os.path.exists(BINDING) else 0
     return all(os.path.getmtime(p) <= t for p in (BINDING_SOURCE, os.path.join(INCLUDE, "ls_row_ops.h"),
                                                   os.path.join(INCLUDE, "ls_sampler.h"), os.path.abspath(__file__)))
@@ -99,6 +122,9 @@ def build(force=False, verbose=False, variant=None):
         raise subprocess.CalledProcessError(1, "g++", f"compiling {BINDING_SOURCE} failed")
     if binding is not None:
         os.replace(tmp, BINDING)
+        with open(tmp, "w") as f:
+            f.write(binding_target() + "\n")
+        os.replace(tmp, BINDING_FOR)
     return lib
 
 
