@@ -123,7 +123,9 @@ class LogitsParams:
     many belong to the prompt.  The caller appends to tokens and seq_lens as it
     samples.  Penalties are float32 [R].  Biases are a ragged list: request r
     owns bias_ids/bias_values[bias_offsets[r]:bias_offsets[r + 1]], ids distinct.
-    Fields left None switch their part off."""
+    Fields left None switch their part off.  Values may change in place at any
+    time; a tensor that is resized or given another storage needs a new
+    LogitsParams (the calls refuse the old one)."""
     tokens: object = None
     prompt_lens: object = None
     seq_lens: object = None
@@ -136,12 +138,14 @@ class LogitsParams:
 
     def __post_init__(self):
         struct = self._marshal()  # its pointers stay valid with the tensors that the fields hold
-        devices = {t.device for t in vars(self).values() if t is not None}
+        fields = {name: t for name, t in vars(self).items() if t is not None}
+        devices = {t.device for t in fields.values()}
         if len(devices) > 1:
             raise ValueError(f"fields lie on different devices: {sorted(map(str, devices))}")
-        object.__setattr__(self, "_device", devices.pop().index)
+        # what the calls read; they refuse a tensor that is no longer as it was here
+        seen = (v for name, t in fields.items() for v in (name, t, t.data_ptr(), t.numel()))
         object.__setattr__(self, "_struct", struct)
-        object.__setattr__(self, "_addr", ctypes.addressof(struct))
+        object.__setattr__(self, "_marshalled", (ctypes.addressof(struct), devices.pop().index, *seen))
 
     def _marshal(self):
         import torch

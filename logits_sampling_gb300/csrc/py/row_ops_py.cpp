@@ -8,6 +8,7 @@
 // package has loaded: their addresses are handed over once (bind).
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -25,9 +26,8 @@ decltype(&ls_top_log_probs) f_top;
 decltype(&ls_distill_loss) f_loss;
 decltype(&ls_distill_loss_backward) f_backward;
 decltype(&ls_distill_loss_grad) f_grad;
-PyObject* ls_error;  // the package's LSError(status, what)
-PyObject* s_addr;    // "_addr": a LogitsParams' struct
-PyObject* s_device;  // "_device": the index of the device its tensors lie on
+PyObject* ls_error;      // the package's LSError(status, what)
+PyObject* s_marshalled;  // "_marshalled": what a LogitsParams holds (marshalled)
 
 // An error on its way to Python.
 struct Fail {
@@ -270,6 +270,28 @@ struct Teacher : ls_teacher {
   }
 };
 
+// The struct of a LogitsParams, whose _marshalled is (its address, the index of
+// its tensors' device, and for each tensor its field's name, itself, its address
+// and its number of entries).  The struct holds addresses, so a tensor that has
+// been resized or given another storage since is refused.
+const ls_logits_params* marshalled(PyObject* o, const Matrix& m) {
+  if (!o) return nullptr;
+  THPObjectPtr held(PyObject_GetAttr(o, s_marshalled));
+  PyObject* t = held.get();
+  PyErr_Clear();
+  if (!t || !PyTuple_CheckExact(t) || PyTuple_GET_SIZE(t) < 2)
+    throw Fail{PyExc_TypeError, "params must be a LogitsParams"};
+  on_device(PyLong_AsLong(PyTuple_GET_ITEM(t, 1)), m, "params");
+  for (Py_ssize_t q = 2; q + 3 < PyTuple_GET_SIZE(t); q += 4) {
+    const at::Tensor& field = THPVariable_Unpack(PyTuple_GET_ITEM(t, q + 1));
+    if (field.const_data_ptr() != PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, q + 2)) ||
+        field.numel() != PyLong_AsLongLong(PyTuple_GET_ITEM(t, q + 3)))
+      throw Fail{PyExc_ValueError, std::string("params' ") + PyUnicode_AsUTF8(PyTuple_GET_ITEM(t, q)) +
+                                       " has been resized or given another storage: make a new LogitsParams"};
+  }
+  return static_cast<const ls_logits_params*>(PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, 0)));
+}
+
 ls_tail tail_of(PyObject* o) {
   if (!o) return LS_TAIL_BUCKET;
   if (PyUnicode_Check(o)) {
@@ -331,22 +353,7 @@ PyObject* process_logits(PyObject*, PyObject* const* args, Py_ssize_t positional
     parse(n_process, args, positional, keywords, o);
     const Matrix m = matrix(o[0]);
     const int32_t n = count32(o[1] ? integer(o[1], "n") : o[3] ? tensor(o[3], "gather_indices").numel() : m.rows, "n");
-    const ls_logits_params* params = nullptr;
-    PyObject* addr = nullptr;
-    if (o[2]) {
-      addr = PyObject_GetAttr(o[2], s_addr);
-      if (!addr) {
-        PyErr_Clear();
-        throw Fail{PyExc_TypeError, "params must be a LogitsParams"};
-      }
-      params = static_cast<const ls_logits_params*>(PyLong_AsVoidPtr(addr));
-      Py_DECREF(addr);
-      PyObject* device = PyObject_GetAttr(o[2], s_device);
-      const long index = device ? PyLong_AsLong(device) : -1;
-      Py_XDECREF(device);
-      PyErr_Clear();
-      on_device(index, m, "params");
-    }
+    const ls_logits_params* params = marshalled(o[2], m);
     const int32_t* mask = nullptr;
     int64_t mask_rows = 0, mask_stride = 0;
     if (o[6]) {
@@ -542,8 +549,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_row_ops_c", "The calls of include
 }  // namespace
 
 PyMODINIT_FUNC PyInit__row_ops_c() {
-  s_addr = PyUnicode_InternFromString("_addr");
-  s_device = PyUnicode_InternFromString("_device");
+  s_marshalled = PyUnicode_InternFromString("_marshalled");
   for (Names* n : {&n_process, &n_top, &n_loss, &n_backward, &n_grad})
     for (int i = 0; i < n->count; ++i) n->name[i] = PyUnicode_InternFromString(n->text[i]);
   return PyModule_Create(&module);
