@@ -28,6 +28,15 @@ class _LogitsParams(ctypes.Structure):
                 ("bias_ids", _P), ("bias_values", _P), ("bias_count", _i32t), ("num_requests", _i32t)]
 
 
+class _Field(ctypes.Structure):
+    _fields_ = [("name", ctypes.c_char_p), ("tensor", ctypes.py_object), ("data", _P), ("numel", _i64t)]
+
+
+class _Marshalled(ctypes.Structure):
+    """What process_logits reads of a LogitsParams: the C struct, and the tensors as they were when it was made."""
+    _fields_ = [("params", _LogitsParams), ("device", _i32t), ("count", _i32t), ("fields", _Field * 9)]
+
+
 class _Teacher(ctypes.Structure):
     _fields_ = [("ids", _P), ("log_probs", _P), ("stride", _i64t), ("k", _i32t)]
 
@@ -137,15 +146,17 @@ class LogitsParams:
     bias_values: object = None
 
     def __post_init__(self):
-        struct = self._marshal()  # its pointers stay valid with the tensors that the fields hold
+        kept = _Marshalled(params=self._marshal())
         fields = {name: t for name, t in vars(self).items() if t is not None}
         devices = {t.device for t in fields.values()}
         if len(devices) > 1:
             raise ValueError(f"fields lie on different devices: {sorted(map(str, devices))}")
-        # what the calls read; they refuse a tensor that is no longer as it was here
-        seen = (v for name, t in fields.items() for v in (name, t, t.data_ptr(), t.numel()))
-        object.__setattr__(self, "_struct", struct)
-        object.__setattr__(self, "_marshalled", (ctypes.addressof(struct), devices.pop().index, *seen))
+        # the addresses are valid while the tensors keep their storages: the calls refuse one that does not
+        kept.device, kept.count = devices.pop().index, len(fields)
+        for field, (name, t) in zip(kept.fields, fields.items()):
+            field.name, field.tensor, field.data, field.numel = name.encode(), t, t.data_ptr(), t.numel()
+        object.__setattr__(self, "_kept", kept)
+        object.__setattr__(self, "_marshalled", ctypes.addressof(kept))
 
     def _marshal(self):
         import torch

@@ -8,7 +8,6 @@
 // package has loaded: their addresses are handed over once (bind).
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -27,7 +26,7 @@ decltype(&ls_distill_loss) f_loss;
 decltype(&ls_distill_loss_backward) f_backward;
 decltype(&ls_distill_loss_grad) f_grad;
 PyObject* ls_error;      // the package's LSError(status, what)
-PyObject* s_marshalled;  // "_marshalled": what a LogitsParams holds (marshalled)
+PyObject* s_marshalled;  // "_marshalled": the address of what a LogitsParams keeps
 
 // An error on its way to Python.
 struct Fail {
@@ -270,26 +269,35 @@ struct Teacher : ls_teacher {
   }
 };
 
-// The struct of a LogitsParams, whose _marshalled is (its address, the index of
-// its tensors' device, and for each tensor its field's name, itself, its address
-// and its number of entries).  The struct holds addresses, so a tensor that has
-// been resized or given another storage since is refused.
+// What a LogitsParams keeps at the address _marshalled (_Marshalled in _row_ops.py).
+struct Marshalled {
+  ls_logits_params params;
+  int32_t device, count;  // the tensors' device and their number
+  struct {
+    const char* name;
+    PyObject* tensor;
+    const void* data;
+    int64_t numel;
+  } field[9];
+};
+
+// The struct of a LogitsParams.  It holds addresses, so a tensor that has been
+// resized or given another storage since is refused.
 const ls_logits_params* marshalled(PyObject* o, const Matrix& m) {
   if (!o) return nullptr;
-  THPObjectPtr held(PyObject_GetAttr(o, s_marshalled));
-  PyObject* t = held.get();
+  PyObject* address = PyObject_GetAttr(o, s_marshalled);
+  const auto* p = address ? static_cast<const Marshalled*>(PyLong_AsVoidPtr(address)) : nullptr;
+  Py_XDECREF(address);
   PyErr_Clear();
-  if (!t || !PyTuple_CheckExact(t) || PyTuple_GET_SIZE(t) < 2)
-    throw Fail{PyExc_TypeError, "params must be a LogitsParams"};
-  on_device(PyLong_AsLong(PyTuple_GET_ITEM(t, 1)), m, "params");
-  for (Py_ssize_t q = 2; q + 3 < PyTuple_GET_SIZE(t); q += 4) {
-    const at::Tensor& field = THPVariable_Unpack(PyTuple_GET_ITEM(t, q + 1));
-    if (field.const_data_ptr() != PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, q + 2)) ||
-        field.numel() != PyLong_AsLongLong(PyTuple_GET_ITEM(t, q + 3)))
-      throw Fail{PyExc_ValueError, std::string("params' ") + PyUnicode_AsUTF8(PyTuple_GET_ITEM(t, q)) +
+  if (!p) throw Fail{PyExc_TypeError, "params must be a LogitsParams"};
+  on_device(p->device, m, "params");
+  for (int q = 0; q < p->count; ++q) {
+    const at::Tensor& t = THPVariable_Unpack(p->field[q].tensor);
+    if (t.const_data_ptr() != p->field[q].data || t.numel() != p->field[q].numel)
+      throw Fail{PyExc_ValueError, std::string("params' ") + p->field[q].name +
                                        " has been resized or given another storage: make a new LogitsParams"};
   }
-  return static_cast<const ls_logits_params*>(PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, 0)));
+  return &p->params;
 }
 
 ls_tail tail_of(PyObject* o) {
