@@ -49,8 +49,8 @@ struct ProcessArgs {
 };
 
 // Marks a table slot and returns whether it was empty.  An atomic update of
-// 16-bit slots works on the 32-bit word that holds two (no carry crosses: see
-// the widths above).
+// 16-bit slots works on the 32-bit word that holds two (no carry crosses: they
+// are used where a history has fewer than 2^15 ids, so 2 n + 1 stays below 2^16).
 template <typename Slot>
 __device__ __forceinline__ bool mark(Slot* table, int e, bool prompt) {
   uint32_t* word = reinterpret_cast<uint32_t*>(table) + (sizeof(Slot) == 2 ? e >> 1 : e);
@@ -149,13 +149,17 @@ __device__ __forceinline__ void fail_run(const ProcessArgs& a, const Run<TIn, T>
 //     id.  (In place the logit is still there: step 1 wrote the same bits, or -inf
 //     where the mask forbids it.)
 // Bound by latency: a tile's life is a chain of reads (row, request, history,
-// logits again) beside 2 x 32 KB of copying, four tiles to an SM.  1 x 32000 bf16
-// with 256 ids 2.9 us, 63 x 32003 with 2048 ids 7.4 us, 256 x 128256 with 8192
-// ids 44 us (3.0 TB/s; every tile marks its share of 2 M ids; with 512 ids 31 us).
-// Measured against it on the last: tiles of 512 threads 42 us (but 36 against 34
-// with 2048 ids); the tile's logits in shared memory and settled there 49 us
-// (72 KB of it per CTA leaves L1 too small for the loads in flight); a hash table
-// in place of a slot per entry 52 us.
+// logits again) beside 2 x 32 KB of copying, four tiles to an SM, and every tile
+// reads the row's whole history in batches of 1024 ids, one after another with
+// none in flight between them.  1 x 32000 bf16 2.9 us with 256 ids; with biases
+// and masks 63 x 32003 9.0 us with 2048 ids in every row; 256 x 128256 32 / 40 / 78
+// us with 512 / 2048 / 8192 ids in every row, and 31 / 33 / 44 us (3.1 TB/s) with
+// lengths spread over their logarithm from 16 up to those (130, 366 and 1170 ids a
+// row: the longest rows decide).
+// Measured against it on lengths up to 8192: tiles of 512 threads 42 us (but 36
+// against 34 on lengths up to 2048); the tile's logits in shared memory and settled
+// there 49 us (72 KB of it per CTA leaves L1 too small for the loads in flight); a
+// hash table in place of a slot per entry 52 us.
 template <typename TIn, typename Slot, int kUnits>
 __global__ void __launch_bounds__(kProcThreads, 4) process_kernel(const ProcessArgs a, int tiles) {
   using E = Elem<TIn>;
@@ -317,8 +321,8 @@ constexpr int kCopyUnits = 2048;  // units of a CTA's run
 // The masked copy.  The run's lines that the mask leaves something of are called
 // into L2 first, one per thread: they keep DRAM busy without registers to hold
 // them, and a unit that the mask forbids entirely is not read.  Bound by DRAM:
-// with the kernel below 300 us on 1024 x 262144 fp32 (7.2 TB/s of logits, mask
-// and output, some of which the mask spares; 358 us in one kernel).
+// with the kernel below 302 us on 1024 x 262144 fp32 under masks (7.2 TB/s of
+// logits, mask and output, some of which the mask spares), 346 us without.
 template <typename TIn>
 __global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const ProcessArgs a, int runs, int upc) {
   using Raw = typename Elem<TIn>::Raw;
@@ -391,9 +395,10 @@ __global__ void __launch_bounds__(kCopyThreads, 4) copy_kernel(const ProcessArgs
 // The touched entries of a row, one CTA per row.  While the copies are being
 // written it builds a hash table of the history's ids and the biases' in shared
 // memory; then it reads the copies of those that the mask allows, which are the
-// logits themselves, and writes the new values over them.  Bound by its scattered
-// accesses, about one per clock and SM: 300 rows of 2048 ids 24 us when it runs
-// alone.
+// logits themselves, and writes the new values over them.  Bound by latency, two
+// CTAs to an SM: a chain of dependent reads (row, request, length, ids) and then
+// barriers and scattered accesses to the table and the copies.  Alone it takes 24
+// us on 300 rows of 395 ids on average (16 to 2048) and 34 us with 2048 in each.
 constexpr int kSettleThreads = 512;
 constexpr int kSettleSlots = 11776;               // two CTAs to an SM
 constexpr int kSettleIds = kSettleSlots / 4 * 3;  // ids that it takes, repeated ones and biases counted
@@ -630,11 +635,18 @@ template <typename TIn, typename Slot>
 static ls_status launch(const ProcessArgs& a, ls_dtype dtype, int32_t n, cudaStream_t st) {
   const int64_t wide = (row_units(a.vocab, dtype) + 4 * kProcThreads - 1) / (4 * kProcThreads) * n;
   const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
-  // The pair copies at the speed of memory (1024 x 262144 fp32 with histories up
-  // to 2048: 302 us against 358), but settles a row on one SM, whose scattered
-  // accesses take some microseconds per thousand ids; the one kernel spreads a
-  // row's over its tiles (256 x 128256 bf16: histories up to 2048 33 us
-  // in one kernel and 35 in the pair, up to 512 31 and 28, up to 8192 44 and 61).
+  // The pair copies at the speed of memory and spares what a mask forbids, but
+  // settles a row on one SM; the one kernel spreads a row's touched entries over its
+  // tiles.  Measured in us, one kernel / pair, with lengths spread over their
+  // logarithm up to the buffer's, and with every row that long:
+  //   1024 x 262144 fp32, masks, buffers of 2048    358 / 302   414 / 369
+  //   the same, no masks                            303 / 346   351 / 407
+  //   1024 x 262144 fp32, masks, buffers of 8192    396 / 368   703 / 618
+  //   256 x 128256 bf16, masks, buffers of 512       31 /  29    32 /  30
+  //   the same, buffers of 2048                      33 /  35    40 /  41
+  //   the same, buffers of 8192                      44 /  62    78 /  90
+  // Lengths lie on the device, so the rule goes by the buffer's; it does not look
+  // for a mask, without which the one kernel would be the faster one.
   const bool light = !a.has_params || !a.p.tokens ||
                      (int64_t)n * a.vocab * Elem<TIn>::kBytes >= (int64_t)a.p.token_capacity * kPairBytesPerId;
   const int policy = g_policy.load(std::memory_order_relaxed);

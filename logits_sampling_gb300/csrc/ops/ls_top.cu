@@ -240,8 +240,11 @@ __device__ __noinline__ void sort_keys(unsigned long long* keys, int n) {
 // do not; several rows on an SM cover each other's, but the steps after the last
 // rows' streams run alone.  20 best of 672 x 151936 bf16 take 44 us (4.6 TB/s, 0.69
 // of the measured copy rate), 64 of 2048 x 128256 bf16 100 us (5.3 TB/s, 0.79), 64
-// of 1024 x 262144 fp32 184 us (5.8 TB/s, 0.87), 5 of 4 x 1000 fp32 6.2 us.  A thread's own best stage is read again without being
-// listed first: 44 us against 49 on the first of these.
+// of 1024 x 262144 fp32 184 us (5.8 TB/s, 0.87), 5 of 4 x 1000 fp32 6.2 us a call.
+// On few rows the steps after the stream decide, which grow with k: 1 / 20 / 64 / 128
+// / 256 best of 4 x 262144 bf16 take 9.3 / 12.8 / 24 / 41 / 77 us.  A thread's own
+// best stage is read again without being listed first: 44 us against 49 on the first
+// of these.
 template <typename TIn, int T>
 __global__ void __launch_bounds__(T, 1024 / T) top_kernel(const TopArgs a, int upc) {
   extern __shared__ uint4 dyn_smem[];  // keys of the stage maxima, then the entries sent to the first CTA
