@@ -179,19 +179,20 @@ def _i32(t, what):
 
 
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _on(stream):
-    """The stream a call runs on (the current stream when None) and a context
-    that makes it current: outputs and temporaries are allocated and filled on
-    the stream the kernels use, so an explicit stream never races with the
-    call's own set-up, and the caching allocator reuses their memory only in
+def _on(stream, tensor):
+    """The stream a call runs on (when None the current stream of `tensor`'s
+    device) and a context that makes it and its device current: kernels launch on
+    the device that holds the data, and outputs and temporaries are allocated and
+    filled on the stream the kernels use, so an explicit stream never races with
+    the call's own set-up, and the caching allocator reuses their memory only in
     that stream's order."""
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
+    if stream is not None and stream.device != tensor.device:
+        raise ValueError(f"stream is on {stream.device}, {tensor.device} holds the data")
+    s = torch.cuda.current_stream(tensor.device) if stream is None else stream
     return s, torch.cuda.stream(s)
 
 
@@ -201,7 +202,7 @@ def sample(logits, n, params, step, no_top_k, no_top_p, gather_indices=None, tok
     import torch
     lib = load_library()
     ptr, dt, rows, V, stride = _logits_desc(logits)
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.int32, device=logits.device)
@@ -223,7 +224,7 @@ def sample_speculative(required_logits, num_decode, num_prefill, num_speculative
     lib = load_library()
     ptr, dt, rows, V, stride = _logits_desc(required_logits)
     n = num_decode * (1 + num_speculative_tokens) + num_prefill
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, required_logits)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.int32, device=required_logits.device)
@@ -270,7 +271,7 @@ def log_probs(logits, params, num_rows=None, gather_indices=None, token_to_reque
     ptr, dt, rows, V, stride = _logits_desc(logits)
     if num_rows is None:
         num_rows = len(gather_indices) if gather_indices is not None else rows
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         if out is None:
             out = torch.empty((num_rows, V), dtype=torch.float32, device=logits.device)
@@ -294,7 +295,7 @@ def sample_log_probs(logits, n, params, step, no_top_k, no_top_p, gather_indices
     import torch
     lib = load_library()
     ptr, dt, rows, V, stride = _logits_desc(logits)
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.int32, device=logits.device)
@@ -333,7 +334,7 @@ def sample_log_probs_noalloc(logits, n, params, step, no_top_k, no_top_p, gather
     import torch
     lib = load_library()
     ptr, dt, rows, V, stride = _logits_desc(logits)
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.int32, device=logits.device)
@@ -362,7 +363,7 @@ def sample_device_step(logits, n, params, step, no_top_k, no_top_p, gather_indic
     ptr, dt, rows, V, stride = _logits_desc(logits)
     if step.dtype not in (torch.int64, torch.uint64) or step.numel() != 1:
         raise TypeError("step must be a one-element int64/uint64 device tensor")
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.int32, device=logits.device)
@@ -384,7 +385,7 @@ def argmax(logits, n=None, gather_indices=None, out=None, error_word=None, strea
     ptr, dt, rows, V, stride = _logits_desc(logits)
     if n is None:
         n = len(gather_indices) if gather_indices is not None else rows
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         if out is None:
             out = torch.empty(n, dtype=torch.int32, device=logits.device)
@@ -403,7 +404,7 @@ def verify_chain(candidates, target_sampled, predicts=None, accept_index=None, a
     lib = load_library()
     bs, n = candidates.shape
     dev = candidates.device
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, candidates)
     with ctx:
         if predicts is None:
             predicts = torch.full((bs * n,), -1, dtype=torch.int32, device=dev)
@@ -429,7 +430,7 @@ def sample_verify(logits, candidates, params, step, no_top_k, no_top_p, gather_i
     ptr, dt, rows, V, stride = _logits_desc(logits)
     bs, n = candidates.shape
     dev = logits.device
-    s, ctx = _on(stream)
+    s, ctx = _on(stream, logits)
     with ctx:
         target = torch.empty(bs * n, dtype=torch.int32, device=dev)
         predicts = torch.full((bs * n,), -1, dtype=torch.int32, device=dev)
