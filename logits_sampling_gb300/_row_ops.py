@@ -11,7 +11,7 @@ import importlib.util
 import os
 from dataclasses import dataclass
 
-from . import _binding
+from . import _binding, _token_ops
 from ._binding import LSError, load_library
 
 LS_ROW_ERR_BAD_MASK = 8
@@ -67,7 +67,7 @@ def _lib():
     global _ready
     lib = load_library()
     if _ready is not lib:
-        _ready = configure(lib)
+        _ready = _token_ops.configure(configure(lib))
     return lib
 
 
@@ -100,7 +100,8 @@ def calls():
         spec = importlib.util.spec_from_file_location("logits_sampling_gb300._row_ops_c", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.bind(LSError, *(ctypes.cast(getattr(lib, "ls_" + name), ctypes.c_void_p).value for name in CALLS))
+        module.bind(LSError, *(ctypes.cast(getattr(lib, "ls_" + name), ctypes.c_void_p).value
+                               for name in CALLS + _token_ops.CALLS))
         _calls = module
     return _calls
 

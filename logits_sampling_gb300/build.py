@@ -6,7 +6,7 @@ Compiles logits_sampling_gb300/csrc/*.cu and csrc/ops/*.cu into logits_sampling_
 (-gencode arch=compute_103a,code=sm_103a, -O3, -lineinfo, no fast-math).  The
 build is skipped when the library is newer than every source and header.
 
-The Python calls of include/ls_row_ops.h (csrc/py/row_ops_py.cpp) are a small
+The Python calls of include/ls_row_ops.h and ls_token_ops.h (csrc/py) are a small
 extension module over torch's C++ tensors, _row_ops_c.so, compiled beside it
 with g++ against the installed torch's headers.  _row_ops_c.for says which torch
 and Python that was: with others it is compiled again, and not loaded.
@@ -82,8 +82,8 @@ def _binding_up_to_date():
     if binding_built_for() != binding_target():
         return False
     t = os.path.getmtime(BINDING) if os.path.exists(BINDING) else 0
-    return all(os.path.getmtime(p) <= t for p in (BINDING_SOURCE, os.path.join(INCLUDE, "ls_row_ops.h"),
-                                                  os.path.join(INCLUDE, "ls_sampler.h"), os.path.abspath(__file__)))
+    inputs = glob.glob(os.path.join(CSRC, "py", "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return all(os.path.getmtime(p) <= t for p in inputs + [os.path.abspath(__file__)])
 
 
 def sources():

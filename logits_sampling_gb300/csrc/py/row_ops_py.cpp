@@ -1,22 +1,16 @@
-// row_ops_py.cpp -- the Python calls of include/ls_row_ops.h: argument checks,
-// allocation of outputs, one call of the C ABI.  No arithmetic.
+// row_ops_py.cpp -- the Python calls of include/ls_row_ops.h, and the extension
+// module: argument checks, allocation of outputs, one call of the C ABI.  No
+// arithmetic.
 //
 // A small call's kernels take 3 to 8 us on the device; marshalled in Python
 // the call took 11 to 15 us of host time, most of it checks and tensor
 // properties.  The functions here are plain CPython (vectorcall) functions over
 // torch's C++ tensors.  The C ABI's functions are those of the library that the
-// package has loaded: their addresses are handed over once (bind).
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-
-#include <optional>
-#include <string>
-
+// package has loaded: their addresses are handed over once (bind).  The calls of
+// include/ls_token_ops.h are in token_ops_py.h, what both share in ops_py.h.
 #include "ls_row_ops.h"
+#include "ops_py.h"
+#include "token_ops_py.h"
 
 namespace {
 
@@ -25,228 +19,7 @@ decltype(&ls_top_log_probs) f_top;
 decltype(&ls_distill_loss) f_loss;
 decltype(&ls_distill_loss_backward) f_backward;
 decltype(&ls_distill_loss_grad) f_grad;
-PyObject* ls_error;      // the package's LSError(status, what)
 PyObject* s_marshalled;  // "_marshalled": the address of what a LogitsParams keeps
-
-// An error on its way to Python.
-struct Fail {
-  PyObject* type;
-  std::string what;
-};
-
-// ---------------------------------------------------------------------------
-// Arguments
-// ---------------------------------------------------------------------------
-constexpr int kMostArgs = 16;
-struct Names {
-  const char* function;
-  int count, required;
-  const char* text[kMostArgs];
-  PyObject* name[kMostArgs];  // interned
-};
-
-// Fills out[] (NULL: absent, or None) from a vectorcall's arguments.
-void parse(const Names& n, PyObject* const* args, Py_ssize_t positional, PyObject* keywords, PyObject** out) {
-  if (positional > n.count)
-    throw Fail{PyExc_TypeError, std::string(n.function) + "() takes at most " + std::to_string(n.count) + " arguments"};
-  for (int i = 0; i < n.count; ++i) out[i] = i < positional ? args[i] : nullptr;
-  const Py_ssize_t k = keywords ? PyTuple_GET_SIZE(keywords) : 0;
-  for (Py_ssize_t q = 0; q < k; ++q) {
-    PyObject* key = PyTuple_GET_ITEM(keywords, q);
-    int at = -1;
-    for (int i = 0; i < n.count && at < 0; ++i)
-      if (key == n.name[i]) at = i;
-    for (int i = 0; i < n.count && at < 0; ++i)
-      if (PyUnicode_Compare(key, n.name[i]) == 0) at = i;
-    if (at < 0)
-      throw Fail{PyExc_TypeError, std::string(n.function) + "() got an unexpected keyword argument '" +
-                                      PyUnicode_AsUTF8(key) + "'"};
-    if (out[at])
-      throw Fail{PyExc_TypeError, std::string(n.function) + "() got multiple values for argument '" + n.text[at] + "'"};
-    out[at] = args[positional + q];
-  }
-  for (int i = 0; i < n.count; ++i) {
-    if (out[i] == Py_None) out[i] = nullptr;
-    if (i < n.required && !out[i])
-      throw Fail{PyExc_TypeError, std::string(n.function) + "() misses argument '" + n.text[i] + "'"};
-  }
-}
-
-const at::Tensor& tensor(PyObject* o, const char* what) {
-  if (!THPVariable_Check(o)) throw Fail{PyExc_TypeError, std::string(what) + " must be a tensor"};
-  return THPVariable_Unpack(o);
-}
-
-int64_t integer(PyObject* o, const char* what) {
-  const long long v = PyLong_Check(o) ? PyLong_AsLongLong(o) : [&] {
-    PyObject* i = PyNumber_Index(o);
-    if (!i) return -1ll;
-    const long long r = PyLong_AsLongLong(i);
-    Py_DECREF(i);
-    return r;
-  }();
-  if (v == -1 && PyErr_Occurred()) {
-    PyErr_Clear();
-    throw Fail{PyExc_TypeError, std::string(what) + " must be an integer"};
-  }
-  return v;
-}
-
-int32_t count32(int64_t v, const char* what) {
-  if (v < INT32_MIN || v > INT32_MAX) throw Fail{PyExc_ValueError, std::string(what) + " is out of range"};
-  return (int32_t)v;
-}
-
-float number(PyObject* o, float otherwise, const char* what) {
-  if (!o) return otherwise;
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) {
-    PyErr_Clear();
-    throw Fail{PyExc_TypeError, std::string(what) + " must be a number"};
-  }
-  return (float)v;
-}
-
-// A logits matrix.
-struct Matrix {
-  const at::Tensor* t;
-  void* p;
-  ls_dtype dtype;
-  int64_t rows, vocab, stride;
-};
-Matrix matrix(PyObject* o) {
-  const at::Tensor& t = tensor(o, "logits");
-  Matrix m;
-  m.t = &t;
-  if (t.scalar_type() == at::kFloat)
-    m.dtype = LS_DTYPE_F32;
-  else if (t.scalar_type() == at::kBFloat16)
-    m.dtype = LS_DTYPE_BF16;
-  else
-    throw Fail{PyExc_TypeError, std::string("unsupported logits dtype ") + c10::toString(t.scalar_type())};
-  if (t.dim() != 2) throw Fail{PyExc_ValueError, "logits must be 2-D [rows, vocab]"};
-  if (t.stride(1) != 1) throw Fail{PyExc_ValueError, "logits rows must be contiguous (stride(1) == 1)"};
-  if (!t.is_cuda()) throw Fail{PyExc_ValueError, "logits must be a CUDA tensor"};
-  m.rows = t.size(0);
-  m.vocab = t.size(1);
-  m.stride = m.rows <= 1 && t.stride(0) < m.vocab ? m.vocab : t.stride(0);
-  m.p = t.data_ptr();
-  return m;
-}
-
-// Every tensor of a call lies on the logits' device, on which its kernels run.
-void on_device(int64_t device, const Matrix& m, const char* what) {
-  if (device != m.t->get_device())
-    throw Fail{PyExc_ValueError, std::string(what) + " is on cuda:" + std::to_string(device) + ", the logits are on cuda:" +
-                                     std::to_string(m.t->get_device())};
-}
-void on_device(const at::Tensor& t, const Matrix& m, const char* what) {
-  if (!t.is_cuda()) throw Fail{PyExc_ValueError, std::string(what) + ": expected a CUDA tensor"};
-  on_device(t.get_device(), m, what);
-}
-
-// The pointer of an optional contiguous device tensor of at least n entries.
-template <typename T>
-T* vec(PyObject* o, at::ScalarType type, const char* what, int64_t n, const Matrix& m) {
-  if (!o) return nullptr;
-  const at::Tensor& t = tensor(o, what);
-  if (t.scalar_type() != type)
-    throw Fail{PyExc_TypeError, std::string(what) + " must be " + (type == at::kInt ? "int32" : "float32")};
-  on_device(t, m, what);
-  if (!t.is_contiguous()) throw Fail{PyExc_ValueError, std::string(what) + ": expected a contiguous tensor"};
-  if (t.numel() < n)
-    throw Fail{PyExc_ValueError,
-               std::string(what) + " has " + std::to_string(t.numel()) + " entries, " + std::to_string(n) + " are needed"};
-  return static_cast<T*>(t.data_ptr());
-}
-int32_t* i32(PyObject* o, const char* what, int64_t n, const Matrix& m) { return vec<int32_t>(o, at::kInt, what, n, m); }
-float* f32(PyObject* o, const char* what, int64_t n, const Matrix& m) { return vec<float>(o, at::kFloat, what, n, m); }
-
-// An output: the caller's tensor (checked), or a new one, made once the call's
-// device and stream are current.
-struct Output {
-  PyObject* given = nullptr;
-  at::Tensor made;
-  void* p = nullptr;
-  int64_t stride = 0;
-  c10::SmallVector<int64_t, 2> shape;  // of a new one
-  at::ScalarType type = at::kFloat;
-  void make(const Matrix& m) {
-    if (given) return;
-    // without a turn through the dispatcher
-    made = at::detail::empty_cuda(shape, type, m.t->device(), std::nullopt);
-    p = made.data_ptr();
-  }
-  // A new reference.  To autograd a caller's tensor has been written in place: a
-  // graph that saved it says so in its backward pass.  Inference tensors have no
-  // version, and no graph can have saved one.
-  PyObject* take() {
-    if (!given) return THPVariable_Wrap(std::move(made));
-    const at::Tensor& t = THPVariable_Unpack(given);
-    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-    Py_INCREF(given);
-    return given;
-  }
-};
-Output out_matrix(PyObject* o, const Matrix& m, int64_t n, const char* what) {
-  Output r;
-  if (!o) {
-    r.shape = {n, m.vocab};
-    r.type = m.t->scalar_type();
-    r.stride = m.vocab;
-    return r;
-  }
-  const at::Tensor& t = tensor(o, what);
-  if (t.scalar_type() != m.t->scalar_type() || t.dim() != 2 || t.size(0) < n || t.size(1) != m.vocab)
-    throw Fail{PyExc_ValueError, std::string(what) + " must be [" + std::to_string(n) + ", " + std::to_string(m.vocab) +
-                                     "] of the logits' type"};
-  if (t.stride(1) != 1) throw Fail{PyExc_ValueError, std::string(what) + "'s rows must be contiguous (stride(1) == 1)"};
-  on_device(t, m, what);
-  r.given = o;
-  r.p = t.data_ptr();
-  r.stride = t.size(0) <= 1 && t.stride(0) < m.vocab ? m.vocab : t.stride(0);
-  return r;
-}
-Output out_vec(PyObject* o, const Matrix& m, at::IntArrayRef shape, at::ScalarType type, const char* what) {
-  Output r;
-  if (o) {
-    r.p = vec<void>(o, type, what, c10::multiply_integers(shape), m);
-    r.given = o;
-  } else {
-    r.shape.assign(shape.begin(), shape.end());
-    r.type = type;
-  }
-  return r;
-}
-
-// The stream a call runs on: the caller's (made current, so that outputs are
-// allocated on it), or the current one of the logits' device.  That device is
-// the current one while this lives: launches and device attributes follow it.
-struct OnStream {
-  std::optional<c10::cuda::CUDAGuard> device;
-  std::optional<c10::cuda::CUDAStreamGuard> guard;
-  void* raw;
-  OnStream(PyObject* o, const Matrix& m) {
-    if (o) {
-      auto attr = [&](const char* name) {
-        PyObject* v = PyObject_GetAttrString(o, name);
-        if (!v) {
-          PyErr_Clear();
-          throw Fail{PyExc_TypeError, "stream must be a torch.cuda.Stream"};
-        }
-        const long long r = PyLong_AsLongLong(v);
-        Py_DECREF(v);
-        return r;
-      };
-      on_device(attr("device_index"), m, "stream");
-      guard.emplace(c10::cuda::CUDAStream::unpack3(attr("stream_id"), m.t->device().index(),
-                                                   (c10::DeviceType)attr("device_type")));
-    } else if (c10::cuda::current_device() != m.t->get_device()) {
-      device.emplace(m.t->device());
-    }
-    raw = (void*)c10::cuda::getCurrentCUDAStream(m.t->get_device()).stream();
-  }
-};
 
 struct Teacher : ls_teacher {
   Teacher(PyObject* ids_, PyObject* log_probs_, int64_t n, const Matrix& m) {
@@ -308,45 +81,6 @@ ls_tail tail_of(PyObject* o) {
     if (PyUnicode_CompareWithASCIIString(o, "renorm") == 0) return LS_TAIL_RENORM;
   }
   throw Fail{PyExc_ValueError, "tail must be one of ['bucket', 'drop', 'renorm']"};
-}
-
-// Runs a C call without the GIL; its failure becomes LSError.
-template <typename F>
-void call(const char* what, F f) {
-  ls_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
-  if (st == LS_OK) return;
-  PyObject* args = Py_BuildValue("(is)", (int)st, what);
-  PyObject* e = args ? PyObject_CallObject(ls_error, args) : nullptr;
-  Py_XDECREF(args);
-  if (e) {
-    PyErr_SetObject(ls_error, e);
-    Py_DECREF(e);
-  }
-  throw Fail{nullptr, ""};
-}
-
-template <typename F>
-PyObject* entry(F f) {
-  HANDLE_TH_ERRORS
-  try {
-    if (!f_process) throw Fail{PyExc_RuntimeError, "the library is not bound"};
-    return f();
-  } catch (const Fail& e) {
-    if (e.type) PyErr_SetString(e.type, e.what.c_str());
-    return nullptr;
-  }
-  END_HANDLE_TH_ERRORS
-}
-
-PyObject* pair(Output& a, Output& b) {
-  PyObject* r = PyTuple_New(2);
-  if (!r) return nullptr;
-  PyTuple_SET_ITEM(r, 0, a.take());
-  PyTuple_SET_ITEM(r, 1, b.take());
-  return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -504,22 +238,23 @@ PyObject* distill_loss_grad(PyObject*, PyObject* const* args, Py_ssize_t positio
   });
 }
 
-// bind(LSError, addresses of the five C functions in the order of the header)
+// bind(LSError, addresses of the C functions in the order of the headers)
 PyObject* bind(PyObject*, PyObject* args) {
-  PyObject *err, *a[5];
-  if (!PyArg_ParseTuple(args, "OOOOOO", &err, &a[0], &a[1], &a[2], &a[3], &a[4])) return nullptr;
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
-    p[i] = PyLong_AsVoidPtr(a[i]);
+  void* const to[] = {&f_process, &f_top,    &f_loss,            &f_backward,    &f_grad,       &f_score,
+                      &f_score_backward, &f_policy, &f_policy_backward, &f_policy_grad, &f_preference, &f_preference_backward};
+  constexpr int kCount = sizeof(to) / sizeof(to[0]);
+  if (PyTuple_GET_SIZE(args) != 1 + kCount) {
+    PyErr_SetString(PyExc_TypeError, "bind() takes LSError and the address of each call");
+    return nullptr;
+  }
+  void* p[kCount];
+  for (int i = 0; i < kCount; ++i) {
+    p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(args, 1 + i));
     if (!p[i] && PyErr_Occurred()) return nullptr;
   }
-  Py_INCREF(err);
-  ls_error = err;
-  f_process = reinterpret_cast<decltype(f_process)>(p[0]);
-  f_top = reinterpret_cast<decltype(f_top)>(p[1]);
-  f_loss = reinterpret_cast<decltype(f_loss)>(p[2]);
-  f_backward = reinterpret_cast<decltype(f_backward)>(p[3]);
-  f_grad = reinterpret_cast<decltype(f_grad)>(p[4]);
+  for (int i = 0; i < kCount; ++i) memcpy(to[i], &p[i], sizeof(p[i]));
+  ls_error = PyTuple_GET_ITEM(args, 0);
+  Py_INCREF(ls_error);
   Py_RETURN_NONE;
 }
 
@@ -550,15 +285,24 @@ PyMethodDef methods[] = {
             "                  out_loss=None, out_grad=None, error_word=None, stream=None) -> (loss, grad)\n\n"
             "ls_distill_loss_grad: loss (float32 [n]) and gradient ([n, vocab] of the logits' type) from one call; out_grad\n"
             "may be the logits themselves."),
-    {"bind", bind, METH_VARARGS, "bind(error, process, top, loss, backward, grad): the C functions' addresses"},
+    LS_CALL(token_log_probs, doc_score),
+    LS_CALL(token_log_probs_backward, doc_score_backward),
+    LS_CALL(policy_loss, doc_policy),
+    LS_CALL(policy_loss_backward, doc_policy_backward),
+    LS_CALL(policy_loss_grad, doc_policy_grad),
+    LS_CALL(preference_loss, doc_preference),
+    LS_CALL(preference_loss_backward, doc_preference_backward),
+    {"bind", bind, METH_VARARGS, "bind(error, address of each call): the C functions"},
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_row_ops_c", "The calls of include/ls_row_ops.h on torch tensors.", -1, methods};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_row_ops_c",
+                      "The calls of include/ls_row_ops.h and include/ls_token_ops.h on torch tensors.", -1, methods};
 
 }  // namespace
 
 PyMODINIT_FUNC PyInit__row_ops_c() {
   s_marshalled = PyUnicode_InternFromString("_marshalled");
-  for (Names* n : {&n_process, &n_top, &n_loss, &n_backward, &n_grad})
+  for (Names* n : {&n_process, &n_top, &n_loss, &n_backward, &n_grad, &n_score, &n_score_backward, &n_policy, &n_policy_backward,
+                   &n_policy_grad, &n_preference, &n_preference_backward})
     for (int i = 0; i < n->count; ++i) n->name[i] = PyUnicode_InternFromString(n->text[i]);
   return PyModule_Create(&module);
 }
