@@ -37,8 +37,9 @@
 extern "C" {
 #endif
 
-/* One more row error: answer_offsets descend or leave [0, n]. */
-enum { LS_ROW_ERR_BAD_OFFSETS = 16 };
+/* Further row errors: answer_offsets descend or leave [0, n]; a wait inside a
+ * kernel ran out (outputs are then undefined; no input should cause it). */
+enum { LS_ROW_ERR_BAD_OFFSETS = 16, LS_ROW_ERR_STALLED = 32 };
 
 /* Floats per row that the losses leave for their backward passes. */
 #define LS_TOKEN_STATS 32

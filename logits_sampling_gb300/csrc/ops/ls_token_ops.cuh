@@ -22,7 +22,8 @@ struct alignas(16) TokenStats {
   int32_t up;             // the entry of the gradient from above that belongs to the row
   float term;             // preference: weight * (lp - ref)
   float w;                // preference: the weight of a row that counts
-  float pad[23];
+  float dirty;            // not 0: the row may hold NaNs
+  float pad[22];
 };
 static_assert(sizeof(TokenStats) == sizeof(float) * LS_TOKEN_STATS, "the header's size of a row's stats");
 
@@ -56,10 +57,17 @@ struct Moments {
   float m, s, e;
 };
 
+// 2^(d c): the product's rounding, up to 2^-24 of an exponent of 20 or 30, would
+// stay in every sum that is moved to another reference.
+__device__ __forceinline__ float factor(float d, float c) {
+  const float y = d * c;
+  return y > -200.f ? ex2(y) * fmaf(fmaf(d, c, -y), kLn2, 1.f) : 0.f;
+}
+
 // The same set against a maximum m >= a.m.  A NaN in a.s stays one.
 __device__ __forceinline__ Moments rebase(const Moments& a, float m, float c) {
   if (!(a.m > kNegInf)) return Moments{m, a.s, a.e};
-  const float f = rel_exp(a.m, m, c);
+  const float f = a.m == m ? 1.f : factor(a.m - m, c);
   const float d = a.m == m ? 0.f : (a.m - m) * c;
   return Moments{m, a.s * f, f > 0.f ? f * (a.e + d * a.s) : 0.f};
 }
@@ -86,63 +94,122 @@ __device__ __forceinline__ bool lift_ok(float c) { return c >= 5.4210109e-20f &&
 // y of one entry by subtraction, NaN and -inf at kFloorExp.
 __device__ __forceinline__ float rel_log(float v, float m, float c) { return v == m ? 0.f : fmaxf((v - m) * c, kFloorExp); }
 
-// A warp's running maximum and each thread's S and E (as OnlineSum; the E of a
-// fast maximum counts y = v c - r, short of the true one by delta = m c - r).
+// A warp's reference (as OnlineSum's) and each thread's S and E.
+// ExpAgainst with its `scale`, 2^-delta, from a series: delta, what m c lost to its
+// rounding, is below 2^-8, and the instruction is off by 2^-23 at 0 where all rows
+// with the same maximum would share it.
+struct Reference : ExpAgainst {
+  float delta;
+  __device__ __forceinline__ void at(float m_, float c_, bool lift) {
+    m = m_;
+    c = c_;
+    r = m * c;
+    fast = fabsf(r) < 65536.f && (!lift || lift_ok(c));
+    delta = fast ? fmaf(m, c, -r) : 0.f;
+    const float t = -delta * kLn2;
+    scale = fmaf(t, fmaf(t, fmaf(t, 0.16666667f, 0.5f), 1.f), 1.f);
+  }
+};
+
+// The sum of a unit's pairs, in a tree, before it meets what has been added up so
+// far: term by term a row's many small entries were lost to a large sum's rounding
+// (2e-7 of S on average, the same in every row).
+template <int kN>
+__device__ __forceinline__ f32x2 sum_pairs(f32x2 (&t)[kN]) {
+#pragma unroll
+  for (int d = kN / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int q = 0; q < d; ++q) t[q] = add2(t[q], t[q + d]);
+  return t[0];
+}
+
 template <bool kEntropy>
 struct RowSum;
 
 template <>
-struct RowSum<false> : OnlineSum {
-  __device__ __forceinline__ Moments moments() const { return Moments{x.m, sum(), 0.f}; }
+struct RowSum<false> {
+  Reference x;
+  f32x2 s0;
+  __device__ __forceinline__ void init(float c) {
+    x.at(kNegInf, c, false);
+    s0 = 0ull;
+  }
+  // Before units of maximum um in this lane are added (all lanes call).
+  __device__ __forceinline__ void raise(float um) {
+    um = warp_max(um);  // NaN compares false below
+    if (um > x.m) {
+      const float was = x.m, d0 = x.scale;
+      x.at(um, x.c, false);
+      const float g = was > kNegInf ? d0 * factor(was - um, x.c) / x.scale : 0.f;
+      s0 = mul2(s0, pack2(g, g));
+    }
+  }
+  template <typename TIn>
+  __device__ __forceinline__ void add_fast(uint32_t (&w)[8]) {  // against a reference that is `fast`
+    f32x2 t[Unit<TIn>::kN / 2];
+#pragma unroll
+    for (int q = 0; q < Unit<TIn>::kN / 2; ++q) t[q] = x.pair_fast(Unit<TIn>::pair(w, q));
+    s0 = add2(s0, sum_pairs(t));
+  }
+  template <typename TIn>
+  __device__ __forceinline__ void add(uint32_t (&w)[8]) {  // no NaN among them
+    if (x.fast) {
+      add_fast<TIn>(w);
+    } else if (x.m > kNegInf) {
+#pragma unroll
+      for (int q = 0; q < Unit<TIn>::kN / 2; ++q) s0 = add2(s0, x.pair_slow(Unit<TIn>::pair(w, q)));
+    }
+  }
+  __device__ __forceinline__ Moments moments() const {
+    float a, b;
+    unpack2(s0, a, b);
+    return Moments{x.m, (a + b) * x.scale, 0.f};
+  }
 };
 
+// E counts y = v c - r, short of the true exponent by delta.
 template <>
 struct RowSum<true> {
-  ExpAgainst x;
-  float delta;
-  f32x2 s0, s1, e0;
-  __device__ __forceinline__ void against(float m, float c) {
-    x.init(m, c);
-    x.fast = x.fast && lift_ok(c);
-    if (!x.fast) x.scale = 1.f;
-    delta = x.fast ? fmaf(m, c, -x.r) : 0.f;
-  }
+  Reference x;
+  f32x2 s0, e0;
   __device__ __forceinline__ void init(float c) {
-    against(kNegInf, c);
-    s0 = s1 = e0 = 0ull;
+    x.at(kNegInf, c, true);
+    s0 = e0 = 0ull;
   }
   __device__ __forceinline__ void raise(float um) {
     um = warp_max(um);
     if (um > x.m) {
-      const float was = x.m, d0 = delta, f = was > kNegInf ? x.scale * rel_exp(was, um, x.c) : 0.f;
-      against(um, x.c);
-      const float g = f / x.scale;
+      const float was = x.m, d0 = x.delta, z0 = x.scale;
+      x.at(um, x.c, true);
+      const float g = was > kNegInf ? z0 * factor(was - um, x.c) / x.scale : 0.f;
       if (g > 0.f) {
-        const float k = (was - um) * x.c - d0 + delta;
-        e0 = fma2(add2(s0, s1), pack2(k, k), e0);
+        const float k = (was - um) * x.c - d0 + x.delta;
+        e0 = fma2(s0, pack2(k, k), e0);
       }
       s0 = mul2(s0, pack2(g, g));
-      s1 = mul2(s1, pack2(g, g));
       e0 = g > 0.f ? mul2(e0, pack2(g, g)) : 0ull;
     }
   }
   template <typename TIn>
+  __device__ __forceinline__ void add_fast(uint32_t (&w)[8]) {
+    lift<TIn>(w);
+    const f32x2 c2 = pack2(x.c, x.c), r2 = pack2(-x.r, -x.r);
+    f32x2 t[Unit<TIn>::kN / 2], e = 0ull;
+#pragma unroll
+    for (int q = 0; q < Unit<TIn>::kN / 2; ++q) {
+      const f32x2 y = fma2(Unit<TIn>::pair(w, q), c2, r2);
+      float a, b;
+      unpack2(y, a, b);
+      t[q] = pack2(ex2(a), ex2(b));
+      e = fma2(t[q], y, e);
+    }
+    s0 = add2(s0, sum_pairs(t));
+    e0 = add2(e0, e);
+  }
+  template <typename TIn>
   __device__ __forceinline__ void add(uint32_t (&w)[8]) {
     if (x.fast) {
-      lift<TIn>(w);
-      const f32x2 c2 = pack2(x.c, x.c), r2 = pack2(-x.r, -x.r);
-#pragma unroll
-      for (int q = 0; q < Unit<TIn>::kN / 2; ++q) {
-        const f32x2 y = fma2(Unit<TIn>::pair(w, q), c2, r2);
-        float a, b;
-        unpack2(y, a, b);
-        const f32x2 t = pack2(ex2(a), ex2(b));
-        if (q & 1)
-          s1 = add2(s1, t);
-        else
-          s0 = add2(s0, t);
-        e0 = fma2(t, y, e0);
-      }
+      add_fast<TIn>(w);
     } else if (x.m > kNegInf) {
 #pragma unroll
       for (int q = 0; q < Unit<TIn>::kN / 2; ++q) {
@@ -158,12 +225,140 @@ struct RowSum<true> {
   }
   __device__ __forceinline__ Moments moments() const {
     float a, b, p, q;
-    unpack2(add2(s0, s1), a, b);
+    unpack2(s0, a, b);
     unpack2(e0, p, q);
     const float s = a + b;
-    return Moments{x.m, s * x.scale, (p + q - delta * s) * x.scale};
+    return Moments{x.m, s * x.scale, (p + q - x.delta * s) * x.scale};
   }
 };
+
+// A run's stages: [0, all), of which [from, to) lie wholly in the row.
+template <typename TIn, int T>
+struct Stages {
+  typedef Run<TIn, T> R;
+  typedef typename R::Stage Stage;
+  static constexpr int kBytes = R::kStep * 32;
+  int all, from, to;
+  const char* base;  // this thread's first unit of stage 0
+  __device__ __forceinline__ void init(const R& run) {
+    all = (run.n + R::kStep - 1) / R::kStep;
+    from = run.f > 0 ? 1 : 0;
+    to = max(run.l / R::kStep, from);
+    base = run.base + (int)threadIdx.x * 32;
+  }
+  // A stage within [from, to).
+  template <int kHow>
+  __device__ __forceinline__ void load(int s, Stage& w) const {
+    const char* p = base + (int64_t)s * kBytes;
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) load_as<kHow>(p + k * T * 32, w[k]);
+  }
+};
+
+// Stages that stay in shared memory between two passes: the last `n` whole ones of
+// a run.  A thread reads back what it wrote: [stage][unit][half][thread].
+template <int T>
+struct Kept {
+  uint4* mine;  // this thread's first 16 bytes
+  int n;
+  typedef uint32_t Stage[kStage][8];
+  __device__ __forceinline__ void put(int s, const Stage& v) const {
+    uint4* const at = mine + (size_t)s * (kStage * 2 * T);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      at[2 * k * T] = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+      at[(2 * k + 1) * T] = make_uint4(v[k][4], v[k][5], v[k][6], v[k][7]);
+    }
+  }
+  __device__ __forceinline__ void get(int s, Stage& v) const {
+    const uint4* const at = mine + (size_t)s * (kStage * 2 * T);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      const uint4 lo = at[2 * k * T], hi = at[(2 * k + 1) * T];
+      v[k][0] = lo.x, v[k][1] = lo.y, v[k][2] = lo.z, v[k][3] = lo.w;
+      v[k][4] = hi.x, v[k][5] = hi.y, v[k][6] = hi.z, v[k][7] = hi.w;
+    }
+  }
+};
+
+// Adds a run up; `a` holds its first whole stage.  A warp takes the maximum of
+// that stage (0 where it has none) as its reference and adds up all that follow
+// against it, without looking for larger ones: for two entries two conversions,
+// one multiplication, two exponentials and one addition, and no branch.  A sum is
+// as exact against a reference away from the maximum as long as it stays within
+// [kLeastSum, kMostSum]; where it does not (or shows a NaN) the row is taken
+// again, `careful`: with a reference that rises with the maximum and NaNs read as
+// -inf, as the row's ends are always taken.  An entropy's E / S is a mean of
+// exponents and loses digits to a distant reference (6e-6 of H on N(0, 3) rows with
+// a head at 20, 1e-7 with the maximum): there the reference follows the maximum.
+constexpr float kMostSum = 1.0995116e12f, kLeastSum = 9.094947e-13f;  // 2^40, 2^-40
+
+template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
+__device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
+                                        RowSum<kEntropy>& acc, float c, bool careful, const Kept<T>& kept) {
+  typedef typename Run<TIn, T>::Stage Stage;
+  acc.init(c);
+  Stage b;
+#pragma unroll 1
+  for (int s = 0; s < st.all; ++s) {
+    if (!careful && s == st.from) s = st.to;
+    if (s >= st.all) break;
+    run.template prefetch<LOAD_PLAIN>(s * Run<TIn, T>::kStep + (int)threadIdx.x, b);
+    float um = kNegInf;
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      Unit<TIn>::clean(b[k]);
+      um = fmaxf(um, Unit<TIn>::max(b[k]));
+    }
+    acc.raise(um);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) acc.template add<TIn>(b[k]);
+  }
+  if (careful || st.from >= st.to) return;
+  {
+    float um = kNegInf;
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(a[k]));
+    acc.raise(um);
+    if (!(acc.x.m > kNegInf)) acc.raise(0.f);
+  }
+  bool fast = acc.x.fast;
+  auto add = [&](Stage& v) {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) acc.template add_fast<TIn>(v[k]);
+  };
+  const char* in = st.base + (int64_t)st.from * Stages<TIn, T>::kBytes;
+  int left = st.to - st.from;
+  auto step = [&](Stage& v, Stage& w) {
+    in += Stages<TIn, T>::kBytes;
+    if (left > 1) {
+      if (kKeep && left - 1 <= kept.n) {
+#pragma unroll
+        for (int k = 0; k < kStage; ++k) load_as<LOAD_PLAIN>(in + k * T * 32, w[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kStage; ++k) load_as<kHow>(in + k * T * 32, w[k]);
+      }
+    }
+    if (kKeep && left <= kept.n) kept.put(left - 1, v);
+    if (kEntropy) {
+      float um = kNegInf;
+#pragma unroll
+      for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(v[k]));
+      acc.raise(um);
+      fast = fast && acc.x.fast;
+    }
+    add(v);
+    return --left > 0;
+  };
+#pragma unroll 1
+  for (;;) {
+    if (!step(a, b)) break;
+    if (!step(b, a)) break;
+  }
+  if (!fast) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
+}
+__device__ __forceinline__ bool sum_ok(float s) { return s < kMostSum && s > kLeastSum; }  // NaN compares false
 
 // The block's moments from each warp's maximum and thread's sums, in every
 // thread; the order of the sums is fixed.  `red` holds one per warp.
@@ -181,6 +376,31 @@ __device__ __forceinline__ Moments block_moments(Moments t, float c, Moments* re
     if (kEntropy) r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, o);
   }
   return r;
+}
+
+// The moments of a row whose CTAs have theirs, in the first warp of each; `parts`
+// belongs to this CTA, careful becomes whether any of them was.  All threads call.
+struct alignas(16) Part {
+  Moments m;
+  float careful;
+};
+template <bool kEntropy>
+__device__ __forceinline__ void cluster_moments(Moments& r, bool& careful, float c, Part* parts, int C, int rank) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  cluster_wait();  // every CTA of the cluster runs
+  if (tid < C) {
+    const uint32_t to = peer_addr(smem_addr(parts + rank), tid);
+    peer_store2(to, r.m, r.s);
+    peer_store2(to + 8, r.e, careful ? 1.f : 0.f);
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (tid >= 32) return;
+  const Part p = lane < C ? parts[lane] : Part{{kNegInf, 0.f, 0.f}, 0.f};
+  r = rebase(p.m, warp_max(p.m.m), c);
+  r.s = warp_reduce(r.s, OpAddF());
+  if (kEntropy) r.e = warp_reduce(r.e, OpAddF());
+  careful = __any_sync(0xFFFFFFFFu, p.careful != 0.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -206,23 +426,50 @@ __device__ __forceinline__ void skip_row(const TokenArgs& a, int64_t i) {
   }
 }
 
+// What a row's scalars need beside its moments, loaded before the row is streamed.
+struct RowInputs {
+  int32_t id;
+  float w, x;        // weight, the token's logit (NaN as -inf)
+  float A, old, ref; // where the operator has them
+};
+template <typename TIn>
+__device__ __forceinline__ void load_inputs(const TokenArgs& a, int64_t i, RowInputs& in) {  // id and w are known
+  const typename Elem<TIn>::Raw* row = static_cast<const typename Elem<TIn>::Raw*>(a.logits) + i * a.row_stride;
+  in.x = guard(Elem<TIn>::get(row[in.id]));
+  in.A = a.kind == KIND_POLICY ? a.policy.advantages[i] : 0.f;
+  in.old = a.policy.old_log_probs ? a.policy.old_log_probs[i] : 0.f;
+  in.ref = a.policy.ref_log_probs ? a.policy.ref_log_probs[i] : 0.f;
+}
+
 // a - b of two log-probs, 0 where both are -inf.
 __device__ __forceinline__ float log_ratio(float a, float b) { return a == kNegInf && b == kNegInf ? 0.f : a - b; }
 
-// The loss's slopes and outputs of row i from its moments and its token's logit
-// (one thread).
-__device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, const Moments& r, float x, float w,
-                                                 bool entropy) {
+// The loss's slopes and outputs of row i from its moments (one thread; `write`:
+// this one stores the outputs).
+__device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, const Moments& r, const RowInputs& in,
+                                                 bool entropy, bool dirty, bool write = true) {
+  const float x = in.x, w = in.w;
   TokenStats st;
   st.M = r.m;
   st.S = r.s;
-  const float lnS = logf(r.s);
-  st.H = entropy ? lnS - kLn2 * (r.e / r.s) : quiet_nan();  // a gradient of what was not computed shows
-  st.lp = (x == r.m ? 0.f : (x - r.m) / a.temperature) - lnS;
+  // In base-2 exponents, S = 2^k s: lp = ln 2 ((x - M) c - k - log2 s), c the factor
+  // that the sum was made with, so that its rounding moves x and S alike (against
+  // (x - M) / T it would be a bias of every row); (x - M) c from both products'
+  // exact parts.  H likewise.
+  const int k = (int)(__float_as_uint(r.s) >> 23 & 255u) - 127;
+  const float log2s = log2f(__uint_as_float((__float_as_uint(r.s) & 0x7FFFFFu) | 0x3F800000u));
+  const float c = kLog2e / a.temperature, p = x * c, q = r.m * c;
+  if (fabsf(p) < 1e30f && fabsf(q) < 1e30f) {
+    const float y = p - q, z = y - p, lo = (p - (y - z)) - (q + z) + (fmaf(x, c, -p) - fmaf(r.m, c, -q));
+    st.lp = kLn2 * (((y - (float)k) + lo) - log2s);
+  } else {
+    st.lp = (x == r.m ? 0.f : (x - r.m) / a.temperature) - kLn2 * ((float)k + log2s);
+  }
+  st.H = entropy ? kLn2 * (((float)k - r.e / r.s) + log2s) : quiet_nan();  // a gradient of what was not computed shows
   if (r.m == kNegInf) {
     st.lp = quiet_nan();
     st.H = quiet_nan();
-    if (a.error_word) atomicOr(a.error_word, LS_ROW_ERR_NO_FINITE);
+    if (write && a.error_word) atomicOr(a.error_word, LS_ROW_ERR_NO_FINITE);
   }
   st.g_lp = st.g_H = st.term = st.w = 0.f;
   st.up = (int32_t)i;
@@ -232,8 +479,8 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     if (a.out_entropy) a.out_entropy[i] = st.H;
   } else if (a.kind == KIND_POLICY) {
     const ls_policy& p = a.policy;
-    const float A = p.advantages[i];
-    const float ratio = p.old_log_probs ? expf(log_ratio(st.lp, p.old_log_probs[i])) : st.lp == st.lp ? 1.f : st.lp;
+    const float A = in.A;
+    const float ratio = p.old_log_probs ? expf(log_ratio(st.lp, in.old)) : st.lp == st.lp ? 1.f : st.lp;
     float s = 0.f, slope = 0.f;
     if (A != 0.f) {
       const float u = ratio * A, v = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * A;
@@ -246,7 +493,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     }
     float kl = 0.f, kl_slope = 0.f;
     if (p.ref_log_probs) {
-      const float d = log_ratio(p.ref_log_probs[i], st.lp);
+      const float d = log_ratio(in.ref, st.lp);
       if (p.kl == LS_KL_K1) {
         kl = -d;
         kl_slope = 1.f;
@@ -266,104 +513,170 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     }
     if (p.entropy_coef != 0.f) loss -= p.entropy_coef * st.H;
     if (r.m == kNegInf) loss = slope = quiet_nan();  // also where A is 0
-    a.out_loss[i] = w * loss;
+    if (write) a.out_loss[i] = w * loss;
     st.g_lp = w * slope;
     st.g_H = p.entropy_coef != 0.f ? -w * p.entropy_coef : 0.f;
-    if (a.out_metrics) a.out_metrics[i] = make_float4(st.lp, entropy ? st.H : 0.f, kl, ratio);
+    if (write && a.out_metrics) a.out_metrics[i] = make_float4(st.lp, entropy ? st.H : 0.f, kl, ratio);
   } else {
     st.w = w;
-    st.term = w * (a.policy.ref_log_probs ? log_ratio(st.lp, a.policy.ref_log_probs[i]) : st.lp);
+    st.term = w * (a.policy.ref_log_probs ? log_ratio(st.lp, in.ref) : st.lp);
   }
-  if (a.out_stats) {
+  if (write && a.out_stats) {
     float4* out = reinterpret_cast<float4*>(a.out_stats + i);
     out[0] = make_float4(st.M, st.S, st.H, st.lp);
     out[1] = make_float4(st.g_lp, st.g_H, __int_as_float(st.up), st.term);
-    out[2] = make_float4(st.w, 0.f, 0.f, 0.f);
+    out[2] = make_float4(st.w, dirty || entropy ? 1.f : 0.f, 0.f, 0.f);  // with entropies NaNs go unseen
   }
   return st;
 }
 
 // ---------------------------------------------------------------------------
-// The gradient of a unit
+// The gradient
 // ---------------------------------------------------------------------------
-// d_j = e_j (k0 + k1 y_j), e_j = 2^y_j over x.scale where x is fast.
+template <bool kV>
+struct Bool {
+  static constexpr bool value = kV;
+};
+
+// d_j = e_j (k0 + k1 y_j), e_j = 2^y_j over x.scale where x is fast, for every
+// entry but the token's, which is at_id.
 struct RowGradient {
-  ExpAgainst x;
+  Reference x;
   float k0, k1;
-  float at_id;  // the token's entry
-  bool entropy;
+  float at_id;
+  bool lifted;  // with an entropy term, or where the row may hold NaNs
   // g_lp, g_H: the row's slopes times the gradient from above.
-  __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float T) {
+  __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float T, bool dirty) {
     const float c = kLog2e / T;
-    x.init(st.M, c);
-    entropy = g_H != 0.f;
-    if (entropy && !lift_ok(c)) {
-      x.fast = false;
-      x.scale = 1.f;
-    }
+    const bool entropy = g_H != 0.f;
+    lifted = entropy || dirty;
+    x.at(st.M, c, lifted);
     const float lnS = logf(st.S), over = x.scale / (st.S * T);
     k1 = entropy ? -g_H * kLn2 * over : 0.f;
     k0 = -(g_lp + (entropy ? g_H * (st.H - lnS) : 0.f)) * over;
-    if (entropy && x.fast) k0 -= k1 * fmaf(st.M, c, -x.r);  // pair_fast's y is short of the true one by this
+    k0 -= k1 * x.delta;  // pair_fast's y is short of the true one by this
     const float q = expf(st.lp);
     at_id = g_lp * -expm1f(st.lp);  // 1 - q
     if (entropy && q > 0.f) at_id -= g_H * q * (st.lp + st.H);
     at_id /= T;
-    if (st.M == kNegInf) k0 = quiet_nan();
+    if (st.M == kNegInf) k0 = at_id = quiet_nan();
   }
-  // The unit's entries become their gradients; `at`: the token's place in it, kN and above: none.
-  template <typename TIn>
-  __device__ __forceinline__ void apply(uint32_t (&w)[8], uint32_t at) const {
-    constexpr int kN = Unit<TIn>::kN;
-    const f32x2 a0 = pack2(k0, k0);
+  // The unit's entries become their gradients, x being fast.
+  template <typename TIn, bool kLift>
+  __device__ __forceinline__ void apply_fast(uint32_t (&w)[8]) const {
+    const f32x2 a0 = pack2(k0, k0), a1 = pack2(k1, k1), c2 = pack2(x.c, x.c), r2 = pack2(-x.r, -x.r);
+    if (kLift) lift<TIn>(w);
     uint32_t o[8];
-    if (x.fast && !entropy) {
-      Unit<TIn>::clean(w);
 #pragma unroll
-      for (int q = 0; q < kN / 2; ++q) {
-        float a, b;
-        unpack2(mul2(x.pair_fast(Unit<TIn>::pair(w, q)), a0), a, b);
-        Unit<TIn>::set_pair(o, q, a, b);
-      }
+    for (int q = 0; q < Unit<TIn>::kN / 2; ++q) {
+      const f32x2 y = fma2(Unit<TIn>::pair(w, q), c2, r2);
+      float a, b;
+      unpack2(y, a, b);
+      unpack2(mul2(pack2(ex2(a), ex2(b)), kLift ? fma2(y, a1, a0) : a0), a, b);
+      Unit<TIn>::set_pair(o, q, a, b);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = o[q];
+  }
+  // Any unit.
+  template <typename TIn>
+  __device__ __forceinline__ void apply(uint32_t (&w)[8]) const {
+    Unit<TIn>::clean(w);
+    if (x.fast && !lifted) {
+      apply_fast<TIn, false>(w);
     } else if (x.fast) {
-      lift<TIn>(w);
-      const f32x2 a1 = pack2(k1, k1), c2 = pack2(x.c, x.c), r2 = pack2(-x.r, -x.r);
-#pragma unroll
-      for (int q = 0; q < kN / 2; ++q) {
-        const f32x2 y = fma2(Unit<TIn>::pair(w, q), c2, r2);
-        float a, b;
-        unpack2(y, a, b);
-        unpack2(mul2(pack2(ex2(a), ex2(b)), fma2(y, a1, a0)), a, b);
-        Unit<TIn>::set_pair(o, q, a, b);
-      }
+      apply_fast<TIn, true>(w);
     } else {
+      uint32_t o[8];
 #pragma unroll
-      for (int q = 0; q < kN / 2; ++q) {
+      for (int q = 0; q < Unit<TIn>::kN / 2; ++q) {
         float a, b;
         unpack2(Unit<TIn>::pair(w, q), a, b);
         a = rel_log(a, x.m, x.c);
         b = rel_log(b, x.m, x.c);
         Unit<TIn>::set_pair(o, q, ex2(a) * fmaf(a, k1, k0), ex2(b) * fmaf(b, k1, k0));
       }
-    }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) w[q] = o[q];
-    if (at < (uint32_t)kN) {
-#pragma unroll
-      for (int q = 0; q < kN / 2; ++q) {
-        float a = Unit<TIn>::kN == 16 ? __uint_as_float(w[q] << 16) : __uint_as_float(w[2 * q & 7]);
-        float b = Unit<TIn>::kN == 16 ? __uint_as_float(w[q] & 0xFFFF0000u) : __uint_as_float(w[(2 * q + 1) & 7]);
-        if ((int)(at >> 1) == q) {
-          if (at & 1)
-            b = at_id;
-          else
-            a = at_id;
-        }
-        Unit<TIn>::set_pair(w, q, a, b);
-      }
+      for (int q = 0; q < 8; ++q) w[q] = o[q];
     }
   }
 };
+
+// Writes a run's gradients but the token's, from its first stage to its last or
+// (kBack) the other way; `a` holds the first of the whole ones that are not kept.
+template <bool kBack, bool kLift, typename TIn, int T>
+__device__ __forceinline__ void gradient_sweep(const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a, const RowGradient& g,
+                                               char* out, const Kept<T>& kept) {
+  typedef typename Run<TIn, T>::Stage Stage;
+  constexpr int kBytes = kBack ? -Stages<TIn, T>::kBytes : Stages<TIn, T>::kBytes;
+  const int64_t first = (int64_t)(kBack ? st.to - 1 : st.from) * Stages<TIn, T>::kBytes;
+  out += first;
+  Stage b;
+  int held = 0;
+  if (kBack) {
+    held = min(kept.n, st.to - st.from);
+#pragma unroll 1
+    for (int s = 0; s < held; ++s) {
+      kept.get(s, b);
+#pragma unroll
+      for (int k = 0; k < kStage; ++k) {
+        g.template apply_fast<TIn, kLift>(b[k]);
+        store32(out + k * T * 32, b[k]);
+      }
+      out += kBytes;
+    }
+  }
+  const char* in = st.base + (first + (int64_t)held * kBytes);
+  int left = st.to - st.from - held;
+  auto step = [&](Stage& v, Stage& w) {
+    in += kBytes;
+    if (left > 1) {
+#pragma unroll
+      for (int k = 0; k < kStage; ++k) load_as<LOAD_PLAIN>(in + k * T * 32, w[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      g.template apply_fast<TIn, kLift>(v[k]);
+      store32(out + k * T * 32, v[k]);
+    }
+    out += kBytes;
+    return --left > 0;
+  };
+#pragma unroll 1
+  while (left > 0) {
+    if (!step(a, b)) break;
+    step(b, a);
+  }
+}
+template <bool kBack, typename TIn, int T>
+__device__ __forceinline__ void gradient_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
+                                             const RowGradient& shared, typename Elem<TIn>::Raw* grad, const Kept<T>& kept) {
+  const RowGradient g = shared;
+  const bool same = run.aligned_with(grad), slow = !g.x.fast || !same;
+  // the row's ends, and whatever else is not aligned with its gradient or far from fp32's range
+#pragma unroll 1
+  for (int s = 0; s < st.all; ++s) {
+    if (!slow && s == st.from) s = st.to;
+    if (s >= st.all) break;
+    const int u = s * Run<TIn, T>::kStep + (int)threadIdx.x;
+    typename Run<TIn, T>::Stage v;
+    run.template prefetch<LOAD_PLAIN>(u, v);
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      g.template apply<TIn>(v[k]);
+      if (u + k * T < run.n) run.store(grad, same, u + k * T, v[k]);
+    }
+  }
+  if (slow) return;
+  char* const out = reinterpret_cast<char*>(grad + run.j0) + (int)threadIdx.x * 32;
+  if (g.lifted)
+    gradient_sweep<kBack, true>(st, a, g, out, kept);
+  else
+    gradient_sweep<kBack, false>(st, a, g, out, kept);
+}
+
+// ls_token_grad.cu: loss and gradient from one call.
+ls_status token_grad(const TokenArgs& a, ls_dtype dtype, bool entropy, cudaStream_t st);
 
 }  // namespace ops
 }  // namespace lsg

@@ -1,95 +1,53 @@
 // ls_tokens.cu -- the operators of include/ls_token_ops.h: log-probs of given
 // tokens, the policy loss and the preference loss, with their gradients.
 //
-// token_kernel: a CTA per row streams it once for its maximum, sum and entropy
-// term, works out the operator's scalars and, in the call that gives loss and
-// gradient, reads the row again.  pair_kernel: a CTA per pair of answers sums
-// their rows' terms and leaves each row's slope.  token_backward_kernel: one sweep
-// over the logits with the two slopes that a forward call left of each row.
+// token_kernel: a row over a CTA, or over a cluster where there are few, streamed
+// once for its sum and entropy term; the operator's scalars follow in the same
+// launch.  pair_kernel: a CTA per pair of answers sums their rows' terms and leaves
+// each row's slope.  token_backward_kernel: one sweep over the logits with the two
+// slopes that a forward call left of each row, for all three operators.  Loss and
+// gradient from one call are in ls_token_grad.cu.
 #include "ls_token_ops.cuh"
 
 namespace lsg {
 namespace ops {
 
-constexpr int kTokenThreads = 256;
-
-template <typename TIn, bool kEntropy, bool kGrad>
-__global__ void __launch_bounds__(kTokenThreads, 4) token_kernel(const TokenArgs a, int upc) {
-  constexpr int T = kTokenThreads;
-  using E = Elem<TIn>;
-  using Raw = typename E::Raw;
-  constexpr int kFirst = kGrad ? LOAD_KEEP : LOAD_ONCE;
+template <typename TIn, bool kEntropy, int T>
+__global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, int upc) {
   __shared__ Moments red[T / 32];
-  __shared__ TokenStats sh;
+  __shared__ Part parts[kMaxCluster];
   const int tid = threadIdx.x;
-  const int64_t i = blockIdx.x;
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  const int64_t i = blockIdx.x / (unsigned)C;
   wait_for_previous();
   Run<TIn, T> run;
-  run.init(a.logits, i, a.row_stride, a.vocab, upc, 0);
-  Raw* grad = kGrad ? static_cast<Raw*>(a.out_grad) + i * a.grad_stride : nullptr;
-  int32_t id;
-  float w;
-  if (!counts(a, i, id, w)) {
-    if (kGrad) {
-      const bool same = run.aligned_with(grad);
-      uint32_t z[8] = {};
-      for (int u = tid; u < run.n; u += T) run.store(grad, same, u, z);
-    }
-    if (tid == 0) skip_row(a, i);
-    return;
-  }
+  run.init(a.logits, i, a.row_stride, a.vocab, upc, rank);
+  Stages<TIn, T> st;
+  st.init(run);
   typename Run<TIn, T>::Stage first;
-  run.template prefetch<kFirst>(tid, first);
-  const float x = guard(E::get(run.row[id]));
+  if (st.from < st.to) st.template load<LOAD_ONCE>(st.from, first);
+  RowInputs in;
+  if (!counts(a, i, in.id, in.w)) {
+    if (tid == 0 && rank == 0) skip_row(a, i);
+    return;  // every CTA of the row leaves here, before any cluster barrier
+  }
+  if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
+  load_inputs<TIn>(a, i, in);
   const float c = kLog2e / a.temperature;
-  RowSum<kEntropy> acc;
   Moments r;
-  // NaN logits, without entropies: the first pass takes them as they come, and a
-  // row whose sum is NaN is taken again with each of them read as -inf.
-  bool dirty = false;
+  bool careful = false;
 #pragma unroll 1
   for (;;) {
-    acc.init(c);
-    run.template stream<kFirst>(first, [&](int, typename Run<TIn, T>::Stage& v) {
-      float um = kNegInf;
-#pragma unroll
-      for (int k = 0; k < kStage; ++k) {
-        if (!kEntropy && dirty) Unit<TIn>::clean(v[k]);
-        um = fmaxf(um, Unit<TIn>::max(v[k]));
-      }
-      acc.raise(um);
-#pragma unroll
-      for (int k = 0; k < kStage; ++k) acc.template add<TIn>(v[k]);
-    });
+    RowSum<kEntropy> acc;
+    sum_run<LOAD_ONCE, false>(run, st, first, acc, c, careful, Kept<T>{nullptr, 0});
     r = block_moments<T / 32, kEntropy>(acc.moments(), c, red);
-    if (kEntropy || dirty || r.s == r.s) break;  // the same in every thread
-    dirty = true;
-    run.template prefetch<kFirst>(tid, first);
+    if (careful || sum_ok(r.s)) break;  // the same in every thread
+    careful = true;
     __syncthreads();  // red is read
   }
   let_next_start();
-  if (tid == 0) sh = finish_row(a, i, r, x, w, kEntropy);
-  if (kGrad) {
-    // From the row's end: what was read last is the likeliest to be in L2.
-    run.template prefetch<LOAD_PLAIN>(run.last_stage(), first);
-    __syncthreads();
-    const uint32_t place = (uint32_t)run.place(id);
-    RowGradient g;
-    g.init(sh, sh.g_lp, sh.g_H, a.temperature);
-    const bool same = run.aligned_with(grad);
-    run.template stream_back<LOAD_PLAIN>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
-      const bool whole = run.whole(u) && same;
-#pragma unroll
-      for (int k = 0; k < kStage; ++k) {
-        const int uk = u + k * T;
-        g.template apply<TIn>(v[k], place - (uint32_t)uk * Unit<TIn>::kN);
-        if (whole)
-          store32(grad + run.index(uk), v[k]);
-        else if (uk < run.n)
-          run.store(grad, same, uk, v[k]);
-      }
-    });
-  }
+  if (C > 1) cluster_moments<kEntropy>(r, careful, c, parts, C, rank);
+  if (tid == 0 && rank == 0) finish_row(a, i, r, in, kEntropy, careful);
 }
 
 // The sums of a pair's two answers, its loss, and the slope of each of its rows.
@@ -200,10 +158,10 @@ struct TokenBackArgs {
 
 constexpr int kTokenBackRun = 2048;  // units of a CTA's run
 
-template <typename TIn>
-__global__ void __launch_bounds__(kTokenThreads, 4) token_backward_kernel(const TokenBackArgs a, int runs, int upc) {
-  constexpr int T = kTokenThreads;
+template <typename TIn, int T>
+__global__ void __launch_bounds__(T, 1024 / T) token_backward_kernel(const TokenBackArgs a, int runs, int upc) {
   using Raw = typename Elem<TIn>::Raw;
+  __shared__ RowGradient g;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)runs;
   wait_for_previous();
@@ -211,7 +169,6 @@ __global__ void __launch_bounds__(kTokenThreads, 4) token_backward_kernel(const 
   Run<TIn, T> run;
   run.init(a.logits, i, a.row_stride, a.vocab, upc, (int)(blockIdx.x % (unsigned)runs));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
-  const bool same = run.aligned_with(grad);
   const float4* in = reinterpret_cast<const float4*>(a.stats + i);
   const float4 s0 = in[0], s1 = in[1];
   TokenStats st;
@@ -219,62 +176,93 @@ __global__ void __launch_bounds__(kTokenThreads, 4) token_backward_kernel(const 
   st.S = s0.y;
   st.H = s0.z;
   st.lp = s0.w;
+  const bool dirty = in[2].y != 0.f;
   const int32_t up = __float_as_int(s1.z);
   const bool has = up >= 0 && up < a.ups;  // stats of another call do not lead out of bounds
   // a slope of 0 counts nothing, whatever the gradient from above
   const float g_lp = s1.x == 0.f ? 0.f : s1.x * (!a.up_lp ? a.none_lp : has ? a.up_lp[up] : quiet_nan());
   const float g_H = s1.y == 0.f ? 0.f : s1.y * (!a.up_H ? a.none_H : has ? a.up_H[up] : quiet_nan());
   if (g_lp == 0.f && g_H == 0.f) {
+    const bool same = run.aligned_with(grad);
     uint32_t z[8] = {};
     for (int u = tid; u < run.n; u += T) run.store(grad, same, u, z);
     return;
   }
+  Stages<TIn, T> stages;
+  stages.init(run);
   typename Run<TIn, T>::Stage first;
-  run.template prefetch<LOAD_PLAIN>(tid, first);
-  const uint32_t place = (uint32_t)run.place(a.ids[i]);  // -1, past every unit, in another CTA's run
-  RowGradient g;
-  g.init(st, g_lp, g_H, a.temperature);
-  run.template stream<LOAD_PLAIN>(first, [&](int u, typename Run<TIn, T>::Stage& v) {
-    const bool whole = run.whole(u) && same;
-#pragma unroll
-    for (int k = 0; k < kStage; ++k) {
-      const int uk = u + k * T;
-      g.template apply<TIn>(v[k], place - (uint32_t)uk * Unit<TIn>::kN);
-      if (whole)
-        store32(grad + run.index(uk), v[k]);
-      else if (uk < run.n)
-        run.store(grad, same, uk, v[k]);
-    }
-  });
+  if (stages.from < stages.to) stages.template load<LOAD_PLAIN>(stages.from, first);
+  const int32_t id = a.ids[i];
+  if (tid == 0) g.init(st, g_lp, g_H, a.temperature, dirty);
+  __syncthreads();
+  gradient_run<false>(run, stages, first, g, grad, Kept<T>{nullptr, 0});
+  if (run.place(id) >= 0) {  // in this CTA's run: the same in every thread
+    __syncthreads();
+    if (tid == 0) grad[id] = Elem<TIn>::put(g.at_id);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-template <bool kEntropy, bool kGrad>
-static ls_status launch_tokens(const TokenArgs& a, ls_dtype dtype, cudaStream_t st) {
-  const int upc = (int)row_units(a.vocab, dtype);
-  const dim3 grid((unsigned)a.n);
-  return dtype == LS_DTYPE_BF16
-             ? launch_kernel(token_kernel<bf16_tag, kEntropy, kGrad>, grid, kTokenThreads, 1, 0, st, a, upc)
-             : launch_kernel(token_kernel<float, kEntropy, kGrad>, grid, kTokenThreads, 1, 0, st, a, upc);
+// How a batch is laid out on the SMs, which hold 1024 threads of these kernels
+// each.  Measured, us (threads of a CTA x CTAs of a row):
+//   few rows of 128 KB and more: a row over as many CTAs as find room at once.  8
+//     rows of 256 KB 256x8 4.1, 256x4 4.7, 256x1 6.6; 64 of them 6.8, 6.9, 10.4; of 64
+//     KB 5.1, 4.2, 4.2
+//   else one CTA per row, the largest for which every row has its own at once; when
+//     there are more rows than that, the smallest.  304 x 256 KB 512x1 14.1, 256x1
+//     15.3, 128x1 19.3; 400 21.0, 18.1, 21.5; 672 30.7, 32.7, 29.3; 2048 79.4, 78.9,
+//     76.9
+struct ForwardPlan {
+  int threads, ctas;
+};
+static ForwardPlan forward_plan(int32_t n, int64_t bytes) {
+  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
+  if (bytes <= 16 * 1024) return {128, 1};
+  if (n <= 128 && bytes >= 128 * 1024) {
+    int c = 1;
+    while (c < kMaxCluster && n * c * 2 <= 512) c *= 2;
+    return {256, c};
+  }
+  return {n <= 2 * sms ? 512 : n <= 4 * sms ? 256 : 128, 1};
+}
+
+template <typename TIn, bool kEntropy>
+static ls_status pick_forward(const TokenArgs& a, ls_dtype dtype, cudaStream_t st) {
+  const int64_t units = row_units(a.vocab, dtype);
+  const ForwardPlan p = forward_plan(a.n, units * 32);
+  const int upc = (int)((units + p.ctas - 1) / p.ctas);
+  if ((int64_t)a.n * p.ctas > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)a.n * p.ctas);
+  return p.threads == 128   ? launch_kernel(token_kernel<TIn, kEntropy, 128>, grid, 128, p.ctas, 0, st, a, upc)
+         : p.threads == 256 ? launch_kernel(token_kernel<TIn, kEntropy, 256>, grid, 256, p.ctas, 0, st, a, upc)
+                            : launch_kernel(token_kernel<TIn, kEntropy, 512>, grid, 512, p.ctas, 0, st, a, upc);
 }
 
 static ls_status forward(const TokenArgs& a, ls_dtype dtype, bool entropy, cudaStream_t st) {
-  return entropy ? launch_tokens<true, false>(a, dtype, st) : launch_tokens<false, false>(a, dtype, st);
+  if (dtype == LS_DTYPE_BF16)
+    return entropy ? pick_forward<bf16_tag, true>(a, dtype, st) : pick_forward<bf16_tag, false>(a, dtype, st);
+  return entropy ? pick_forward<float, true>(a, dtype, st) : pick_forward<float, false>(a, dtype, st);
+}
+
+template <typename TIn, int T>
+static ls_status launch_backward(const TokenBackArgs& a, int64_t units, int32_t n, cudaStream_t st) {
+  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
+  const int upc = (units + kTokenBackRun - 1) / kTokenBackRun * n >= 8 * sms ? kTokenBackRun : T * kStage;
+  const int64_t runs = (units + upc - 1) / upc;
+  if (runs * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  return launch_kernel(token_backward_kernel<TIn, T>, dim3((unsigned)(runs * n)), T, 1, 0, st, a, (int)runs, upc);
 }
 
 static ls_status backward(const TokenBackArgs& a, ls_dtype dtype, int32_t n, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t units = row_units(a.vocab, dtype);
-  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
-  const int upc = (units + kTokenBackRun - 1) / kTokenBackRun * n >= 8 * sms ? kTokenBackRun : kTokenThreads * kStage;
-  const int64_t runs = (units + upc - 1) / upc;
-  if (runs * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(runs * n));
-  return dtype == LS_DTYPE_BF16
-             ? launch_kernel(token_backward_kernel<bf16_tag>, grid, kTokenThreads, 1, 0, st, a, (int)runs, upc)
-             : launch_kernel(token_backward_kernel<float>, grid, kTokenThreads, 1, 0, st, a, (int)runs, upc);
+  if (units <= 512)  // 16 KB
+    return dtype == LS_DTYPE_BF16 ? launch_backward<bf16_tag, 128>(a, units, n, st)
+                                  : launch_backward<float, 128>(a, units, n, st);
+  return dtype == LS_DTYPE_BF16 ? launch_backward<bf16_tag, 256>(a, units, n, st)
+                                : launch_backward<float, 256>(a, units, n, st);
 }
 
 static bool finite(float v) { return v - v == 0.f; }
@@ -406,9 +394,7 @@ ls_status ls_policy_loss_grad(const void* logits, ls_dtype dtype, int64_t vocab,
   a.out_grad = out_grad;
   a.grad_stride = grad_stride;
   a.error_word = error_word;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return policy->entropy || policy->entropy_coef != 0.f ? launch_tokens<true, true>(a, dtype, st)
-                                                        : launch_tokens<false, true>(a, dtype, st);
+  return token_grad(a, dtype, policy->entropy || policy->entropy_coef != 0.f, static_cast<cudaStream_t>(stream));
 }
 
 ls_status ls_preference_loss(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, int32_t n,

@@ -68,16 +68,20 @@ def _check_gradient(got, rows, g_lp, g_H, dtype, what, tol_g=None):
         _near(got[i], d, tol + R.HALF_STEP[dtype] * (np.abs(d) + tol), f"{what}, row {i}")
 
 
-def _score(dev, x, ids, T, dtype, rng, what="", out=None):
-    """token_log_probs with and without entropies, and every kind of gradient."""
+def _score(dev, x, ids, T, dtype, rng, what="", some=None):
+    """token_log_probs with and without entropies, and every kind of gradient (of rows `some`: all)."""
     import logits_sampling_gb300 as ls
     n = len(ids)
-    rows = _rows(x, ids, T, dtype)
+    some = range(n) if some is None else some
+    rows = [None] * n
+    for i in some:
+        rows[i] = _rows(x[i:i + 1], ids[i:i + 1], T, dtype)[0]
     idd = _dev(ids, np.int32)
     lp0, none, stats0 = ls.token_log_probs(dev, idd, temperature=T)
     lp1, h, stats1 = ls.token_log_probs(dev, idd, temperature=T, entropy=True)
     assert none is None and stats0.shape == (n, ls.TOKEN_STATS)
-    for i, row in enumerate(rows):
+    for i in some:
+        row = rows[i]
         for lp in (lp0, lp1):
             _near(float(lp[i]), 0.0 if row is None else row.lp, 0.0 if row is None or not row.some else row.tol_lp,
                   f"{what} lp {i}")
@@ -85,8 +89,10 @@ def _score(dev, x, ids, T, dtype, rng, what="", out=None):
     g_lp, g_H = rng.standard_normal(n).astype(np.float32), rng.standard_normal(n).astype(np.float32)
     zero = np.zeros(n)
     for stats, a, b in ((stats0, g_lp, None), (stats1, g_lp, g_H), (stats1, None, g_H)):
-        got = ls.token_log_probs_backward(dev, idd, stats, _dev(a), _dev(b), temperature=T, out=out)
-        _check_gradient(_f64(got), rows, zero if a is None else a, zero if b is None else b, dtype, f"{what} gradient")
+        got = ls.token_log_probs_backward(dev, idd, stats, _dev(a), _dev(b), temperature=T)
+        at = list(some)
+        _check_gradient(_f64(got[at]), [rows[i] for i in at], (zero if a is None else a)[at], (zero if b is None else b)[at],
+                        dtype, f"{what} gradient")
 
 
 def _normal(rng, n, V, scale=3.0):
@@ -105,20 +111,17 @@ def test_score_sizes(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n,V", [(1, 128256), (3, 262144), (700, 1001), (200, 32003), (9, 400001)])
+@pytest.mark.parametrize("n,V", [(1, 128256), (3, 262144), (700, 1001), (200, 32003), (9, 400001), (1300, 9001),
+                                 (400, 40003)])
 def test_score_batches(dtype, n, V):
     rng = np.random.default_rng(n + V)
     dev, x = _logits(_normal(rng, n, V), dtype, 3, 5)
-    _score(dev, x, rng.integers(0, V, n), 1.0, dtype, rng, f"{n} x {V}")
+    _score(dev, x, rng.integers(0, V, n), 1.0, dtype, rng, f"{n} x {V}", some=range(0, n, max(1, n // 100)))
 
 
-@pytest.mark.parametrize("dtype", DTYPES)
-def test_score_special_rows(dtype):
-    """NaN, infinities, the type's lowest value as a mask, rows that leave one entry or none, far and equal values."""
-    import logits_sampling_gb300 as ls
+def _special(rng, dtype, V):
+    """20 rows of special values, and their tokens."""
     import torch
-    rng = np.random.default_rng(5)
-    V = 3001
     lowest = float(torch.finfo(torch.float32 if dtype == "f32" else torch.bfloat16).min)
     x = _normal(rng, 20, V)
     ids = rng.integers(0, V, 20)
@@ -149,6 +152,17 @@ def test_score_special_rows(dtype):
     x[19, ::2] = np.nan
     x[19, 1::2] = -np.inf
     x[19, 2] = 1.0
+    return x, ids
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_score_special_rows(dtype):
+    """NaN, infinities, the type's lowest value as a mask, rows that leave one entry or none, far and equal values."""
+    import logits_sampling_gb300 as ls
+    import torch
+    rng = np.random.default_rng(5)
+    V = 3001
+    x, ids = _special(rng, dtype, V)
     dev, xs = _logits(x, dtype, 2, 6)
     for T in (1.0, 0.05, 30.0):
         _score(dev, xs, ids, T, dtype, rng, f"T {T}")
@@ -159,6 +173,31 @@ def test_score_special_rows(dtype):
     keep = [i for i in range(20) if i not in (5, 6)]
     ls.token_log_probs(dev[keep], _dev(ids[keep], np.int32), error_word=err)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [20, 140, 320, 620])
+def test_score_special_long_rows(dtype, n):
+    """The same in rows of many stages, for each layout of a batch; and rows whose maximum is far above what the first
+    stages hold, below their reference, or all in one place."""
+    rng = np.random.default_rng(50)
+    V = 70001
+    x = _normal(rng, n, V)
+    x[:20], ids20 = _special(rng, dtype, V)
+    ids = rng.integers(0, V, n)
+    ids[:20] = ids20
+    if n > 20:
+        x[20, 60000:60010] = 33.0               # sums far above 1
+        x[21, 69000] = 90.0                     # past what a sum against the first stage may hold
+        x[22, :50000] = -np.inf                 # nothing in the first stages
+        x[23, :] = -np.inf
+        x[23, 69990:] = -300.0                  # far below the reference of a warp that has none
+        x[24, :50000] = -200.0
+        x[25, 100] = 500.0
+        ids[20:26] = 60003, 69000, 60000, 69995, 60001, 100
+    dev, xs = _logits(x, dtype, 2, 6)
+    some = list(range(26)) if n > 20 else list(range(20))
+    _score(dev, xs, ids, 1.0, dtype, rng, f"{n} rows", some=some)
 
 
 @pytest.mark.parametrize("T", [1e-30, 1e-7, 1e9, 1e25, 3e38])
@@ -291,13 +330,15 @@ def test_policy_terms(dtype, kw):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n,V", [(700, 1000), (161, 32000), (6, 262144), (310, 16391)])
-def test_policy_batches(dtype, n, V):
+@pytest.mark.parametrize("n,V", [(700, 1000), (161, 32000), (6, 262144), (310, 16391), (130, 400001), (311, 90001)])
+@pytest.mark.parametrize("eta", [0.0, 0.01])
+def test_policy_batches(dtype, n, V, eta):
     rng = np.random.default_rng(n)
-    dev, x = _logits(_normal(rng, n, V), dtype)
+    dev, x = _logits(_normal(rng, n, V), dtype, *((0, 0) if V % 2 == 0 else (1, 2)))
     ids = rng.integers(0, V, n)
-    rows = _rows(x, ids, 1.0, dtype)
-    _policy(dev, ids, rows, _policy_inputs(rng, rows), dtype, 1.0, f"{n} x {V}", eta=0.01)
+    at = set(range(0, n, max(1, n // 50)))
+    rows = _rows(x, ids, 1.0, dtype, [i in at for i in range(n)])
+    _policy(dev, ids, rows, _policy_inputs(rng, rows), dtype, 1.0, f"{n} x {V}", eta=eta)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -6,7 +6,10 @@ Tolerances, with eps = 2^-24 (half a step of fp32) and y = (x - M) / T:
             are rounded three times (3 eps |y|), the exponential is off by at
             most 2^-22, and every time the running maximum rises (at most once
             per stage of 512 units, and twice when threads and CTAs are joined)
-            the sums are multiplied by one more such factor
+            the sums are multiplied by one more such factor; where a sum is made
+            against a reference g below the maximum instead, it is not multiplied
+            but each exponent is g larger: 3 eps g, which is below the 2^-22 (stages
+            + 4) of those factors for g up to 5
   sum       added up by a thread over its entries, then over the threads: one
             rounding per addition of a thread, and 16 more
   ln S      relative error of S, and its own two roundings
