@@ -24,8 +24,8 @@
  *
  * A row does not count where ids[i] lies outside [0, vocab) (padding, rejected
  * drafts), where weights[i] is 0, and, in the preference loss, outside the
- * answers: it is not read, its outputs are 0 and its gradient is 0 whatever the
- * gradient from above holds.  A row that counts and has no entry above -inf
+ * answers: whatever it holds, its outputs are 0, and its gradient is 0 whatever
+ * the gradient from above holds.  A row that counts and has no entry above -inf
  * gives NaN and sets LS_ROW_ERR_NO_FINITE in *error_word.
  */
 #ifndef LS_TOKEN_OPS_H
@@ -37,12 +37,11 @@
 extern "C" {
 #endif
 
-/* Further row errors: answer_offsets descend or leave [0, n]; a wait inside a
- * kernel ran out (outputs are then undefined; no input should cause it). */
-enum { LS_ROW_ERR_BAD_OFFSETS = 16, LS_ROW_ERR_STALLED = 32 };
+/* One more row error: answer_offsets descend or leave [0, n]. */
+enum { LS_ROW_ERR_BAD_OFFSETS = 16 };
 
 /* Floats per row that the losses leave for their backward passes. */
-#define LS_TOKEN_STATS 32
+#define LS_TOKEN_STATS 12
 /* Floats per row of a policy loss's metrics: lp, H (0 unless it was asked for), the KL estimate, the ratio. */
 #define LS_POLICY_METRICS 4
 
@@ -54,7 +53,7 @@ enum { LS_ROW_ERR_BAD_OFFSETS = 16, LS_ROW_ERR_STALLED = 32 };
  *   out_log_probs  device float[n]
  *   out_entropy    device float[n], or NULL: no entropies
  *   out_stats      device float[LS_TOKEN_STATS * n], 16-byte aligned: what the
- *                  backward pass needs, and the call's own scratch
+ *                  backward pass needs
  */
 ls_status ls_token_log_probs(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, int32_t n,
                              const int32_t* ids, float temperature, float* out_log_probs, float* out_entropy,
@@ -155,7 +154,7 @@ typedef struct {
  * over its rows (divided by the sum of weights[i]; 0 where that is 0),
  * u = s(chosen) - s(rejected) and h = beta u - margin: the loss of each pair.
  * A difference of two log-probs of -inf is 0.  A pair with bad offsets gives
- * NaN, gradient 0 and LS_ROW_ERR_BAD_OFFSETS; rows in no answer are not read.
+ * NaN, gradient 0 and LS_ROW_ERR_BAD_OFFSETS.
  *
  *   out_loss        device float[pairs]
  *   out_log_ratios  device float[2 * pairs]: s of each answer, or NULL

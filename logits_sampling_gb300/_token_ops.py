@@ -8,7 +8,7 @@ preference are autograd functions over them."""
 import ctypes
 
 LS_ROW_ERR_BAD_OFFSETS = 16
-TOKEN_STATS = 32  # LS_TOKEN_STATS
+TOKEN_STATS = 12  # LS_TOKEN_STATS
 POLICY_METRICS = ("log_prob", "entropy", "kl", "ratio")  # columns of a policy loss's metrics
 CALLS = ("token_log_probs", "token_log_probs_backward", "policy_loss", "policy_loss_backward", "policy_loss_grad",
          "preference_loss", "preference_loss_backward")

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
   Stages<TIn, T> st;
   st.init(run);
   typename Run<TIn, T>::Stage first;
-  if (st.from < st.to) st.template load<LOAD_KEEP>(st.from, first);
+  if (st.whole > 0) st.template load<LOAD_KEEP>(0, first);
   Raw* const grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
   RowInputs in;
   if (!counts(a, i, in.id, in.w)) {
@@ -53,11 +53,11 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
   }
   let_next_start();
   // from the run's end: what was read last is the likeliest to be in L2
-  if (st.from < st.to - keep) st.template load<LOAD_PLAIN>(st.to - 1 - keep, first);
+  if (st.whole > keep) st.template load<LOAD_PLAIN>(st.whole - 1 - keep, first);
   if (C > 1) cluster_moments<kEntropy>(r, careful, c, parts, C, rank);
   if (tid == 0) {
     const TokenStats s = finish_row(a, i, r, in, kEntropy, careful, rank == 0);
-    g.init(s, s.g_lp, s.g_H, a.temperature, careful || kEntropy);
+    g.init(s, s.g_lp, s.g_H, a.temperature);
   }
   __syncthreads();
   gradient_run<true>(run, st, first, g, grad, kept);

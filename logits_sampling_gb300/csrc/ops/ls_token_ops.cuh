@@ -17,13 +17,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // What a forward call leaves of a row (LS_TOKEN_STATS floats).
 struct alignas(16) TokenStats {
-  float M, S, H, lp;      // maximum, sum exp((x - M) / T), entropy, log-prob of the token
+  float M, over;          // reference of the sum, 1 / (S T)
+  float id_lp, id_H;      // the token's gradient: g_lp * id_lp - g_H * id_H
   float g_lp, g_H;        // the loss's slopes; both 0: the row does not count
   int32_t up;             // the entry of the gradient from above that belongs to the row
-  float term;             // preference: weight * (lp - ref)
-  float w;                // preference: the weight of a row that counts
+  float mean;             // H - ln S
   float dirty;            // not 0: the row may hold NaNs
-  float pad[22];
+  float term, w;          // preference: weight * (lp - ref), the weight of a row that counts
+  float pad;
 };
 static_assert(sizeof(TokenStats) == sizeof(float) * LS_TOKEN_STATS, "the header's size of a row's stats");
 
@@ -232,26 +233,47 @@ struct RowSum<true> {
   }
 };
 
-// A run's stages: [0, all), of which [from, to) lie wholly in the row.
+// A run's stages.  They begin at its first whole unit, so that [0, whole) of them
+// lie wholly in the row however it is aligned; what is left (units at the run's
+// end, and the row's first unit where it is not whole) makes up the stages [whole,
+// all): one, seldom two.
 template <typename TIn, int T>
 struct Stages {
   typedef Run<TIn, T> R;
   typedef typename R::Stage Stage;
   static constexpr int kBytes = R::kStep * 32;
-  int all, from, to;
+  int all, whole;
   const char* base;  // this thread's first unit of stage 0
   __device__ __forceinline__ void init(const R& run) {
     all = (run.n + R::kStep - 1) / R::kStep;
-    from = run.f > 0 ? 1 : 0;
-    to = max(run.l / R::kStep, from);
-    base = run.base + (int)threadIdx.x * 32;
+    whole = max(run.l - run.f, 0) / R::kStep;
+    base = run.base + (run.f + (int)threadIdx.x) * 32;
   }
-  // A stage within [from, to).
+  // A whole stage.
   template <int kHow>
   __device__ __forceinline__ void load(int s, Stage& w) const {
     const char* p = base + (int64_t)s * kBytes;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) load_as<kHow>(p + k * T * 32, w[k]);
+  }
+  // Unit k of this thread in any stage, -1: none.
+  __device__ __forceinline__ static int unit(const R& run, int s, int k) {
+    const int v = s * R::kStep + k * T + (int)threadIdx.x;
+    return v >= run.n ? -1 : v + run.f < run.n ? v + run.f : 0;
+  }
+  // Any stage; units past the run as -inf.
+  __device__ __forceinline__ static void load_any(const R& run, int s, Stage& w) {
+#pragma unroll
+    for (int k = 0; k < kStage; ++k) {
+      const int u = unit(run, s, k);
+      if (u >= 0) {
+        run.template load<LOAD_PLAIN>(u, w[k]);
+      } else {
+        const uint32_t none = Elem<TIn>::kBytes == 2 ? 0xFF80FF80u : 0xFF800000u;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[k][q] = none;
+      }
+    }
   }
 };
 
@@ -289,8 +311,9 @@ struct Kept {
 // [kLeastSum, kMostSum]; where it does not (or shows a NaN) the row is taken
 // again, `careful`: with a reference that rises with the maximum and NaNs read as
 // -inf, as the row's ends are always taken.  An entropy's E / S is a mean of
-// exponents and loses digits to a distant reference (6e-6 of H on N(0, 3) rows with
-// a head at 20, 1e-7 with the maximum): there the reference follows the maximum.
+// exponents and loses digits to a distant reference (1.4e-6 of H in 1024 x 262144
+// fp32 with a head at 20, 1e-7 with the maximum; 149.6 and 150.2 us): there the
+// reference follows the maximum.
 constexpr float kMostSum = 1.0995116e12f, kLeastSum = 9.094947e-13f;  // 2^40, 2^-40
 
 template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
@@ -300,10 +323,8 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
   acc.init(c);
   Stage b;
 #pragma unroll 1
-  for (int s = 0; s < st.all; ++s) {
-    if (!careful && s == st.from) s = st.to;
-    if (s >= st.all) break;
-    run.template prefetch<LOAD_PLAIN>(s * Run<TIn, T>::kStep + (int)threadIdx.x, b);
+  for (int s = careful ? 0 : st.whole; s < st.all; ++s) {
+    st.load_any(run, s, b);
     float um = kNegInf;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) {
@@ -314,7 +335,7 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add<TIn>(b[k]);
   }
-  if (careful || st.from >= st.to) return;
+  if (careful || st.whole == 0) return;
   {
     float um = kNegInf;
 #pragma unroll
@@ -327,8 +348,8 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add_fast<TIn>(v[k]);
   };
-  const char* in = st.base + (int64_t)st.from * Stages<TIn, T>::kBytes;
-  int left = st.to - st.from;
+  const char* in = st.base;
+  int left = st.whole;
   auto step = [&](Stage& v, Stage& w) {
     in += Stages<TIn, T>::kBytes;
     if (left > 1) {
@@ -450,37 +471,43 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
                                                  bool entropy, bool dirty, bool write = true) {
   const float x = in.x, w = in.w;
   TokenStats st;
+  float lp, H;
   st.M = r.m;
-  st.S = r.s;
   // In base-2 exponents, S = 2^k s: lp = ln 2 ((x - M) c - k - log2 s), c the factor
   // that the sum was made with, so that its rounding moves x and S alike (against
   // (x - M) / T it would be a bias of every row); (x - M) c from both products'
   // exact parts.  H likewise.
   const int k = (int)(__float_as_uint(r.s) >> 23 & 255u) - 127;
   const float log2s = log2f(__uint_as_float((__float_as_uint(r.s) & 0x7FFFFFu) | 0x3F800000u));
-  const float c = kLog2e / a.temperature, p = x * c, q = r.m * c;
+  const float T = a.temperature, c = kLog2e / T, p = x * c, q = r.m * c;
   if (fabsf(p) < 1e30f && fabsf(q) < 1e30f) {
     const float y = p - q, z = y - p, lo = (p - (y - z)) - (q + z) + (fmaf(x, c, -p) - fmaf(r.m, c, -q));
-    st.lp = kLn2 * (((y - (float)k) + lo) - log2s);
+    lp = kLn2 * (((y - (float)k) + lo) - log2s);
   } else {
-    st.lp = (x == r.m ? 0.f : (x - r.m) / a.temperature) - kLn2 * ((float)k + log2s);
+    lp = (x == r.m ? 0.f : (x - r.m) / T) - kLn2 * ((float)k + log2s);
   }
-  st.H = entropy ? kLn2 * (((float)k - r.e / r.s) + log2s) : quiet_nan();  // a gradient of what was not computed shows
+  const float mean = entropy ? -kLn2 * (r.e / r.s) : quiet_nan();  // a gradient of what was not computed shows
+  H = entropy ? kLn2 * (((float)k - r.e / r.s) + log2s) : quiet_nan();
   if (r.m == kNegInf) {
-    st.lp = quiet_nan();
-    st.H = quiet_nan();
+    lp = H = quiet_nan();
     if (write && a.error_word) atomicOr(a.error_word, LS_ROW_ERR_NO_FINITE);
   }
+  const float q_id = expf(lp);
+  st.over = r.m == kNegInf ? quiet_nan() : 1.f / (r.s * T);
+  st.id_lp = -expm1f(lp) / T;  // 1 - q
+  st.id_H = q_id > 0.f ? q_id * (lp + H) / T : q_id;
+  st.mean = mean;
+  st.dirty = dirty || entropy ? 1.f : 0.f;  // with entropies NaNs go unseen
   st.g_lp = st.g_H = st.term = st.w = 0.f;
   st.up = (int32_t)i;
   if (a.kind == KIND_SCORE) {
     st.g_lp = st.g_H = 1.f;
-    a.out_loss[i] = st.lp;
-    if (a.out_entropy) a.out_entropy[i] = st.H;
+    a.out_loss[i] = lp;
+    if (a.out_entropy) a.out_entropy[i] = H;
   } else if (a.kind == KIND_POLICY) {
     const ls_policy& p = a.policy;
     const float A = in.A;
-    const float ratio = p.old_log_probs ? expf(log_ratio(st.lp, in.old)) : st.lp == st.lp ? 1.f : st.lp;
+    const float ratio = p.old_log_probs ? expf(log_ratio(lp, in.old)) : lp == lp ? 1.f : lp;
     float s = 0.f, slope = 0.f;
     if (A != 0.f) {
       const float u = ratio * A, v = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * A;
@@ -493,7 +520,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     }
     float kl = 0.f, kl_slope = 0.f;
     if (p.ref_log_probs) {
-      const float d = log_ratio(in.ref, st.lp);
+      const float d = log_ratio(in.ref, lp);
       if (p.kl == LS_KL_K1) {
         kl = -d;
         kl_slope = 1.f;
@@ -511,21 +538,21 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
       loss += p.kl_coef * kl;
       slope += p.kl_coef * kl_slope;
     }
-    if (p.entropy_coef != 0.f) loss -= p.entropy_coef * st.H;
+    if (p.entropy_coef != 0.f) loss -= p.entropy_coef * H;
     if (r.m == kNegInf) loss = slope = quiet_nan();  // also where A is 0
     if (write) a.out_loss[i] = w * loss;
     st.g_lp = w * slope;
     st.g_H = p.entropy_coef != 0.f ? -w * p.entropy_coef : 0.f;
-    if (write && a.out_metrics) a.out_metrics[i] = make_float4(st.lp, entropy ? st.H : 0.f, kl, ratio);
+    if (write && a.out_metrics) a.out_metrics[i] = make_float4(lp, entropy ? H : 0.f, kl, ratio);
   } else {
     st.w = w;
-    st.term = w * (a.policy.ref_log_probs ? log_ratio(st.lp, in.ref) : st.lp);
+    st.term = w * (a.policy.ref_log_probs ? log_ratio(lp, in.ref) : lp);
   }
   if (write && a.out_stats) {
     float4* out = reinterpret_cast<float4*>(a.out_stats + i);
-    out[0] = make_float4(st.M, st.S, st.H, st.lp);
-    out[1] = make_float4(st.g_lp, st.g_H, __int_as_float(st.up), st.term);
-    out[2] = make_float4(st.w, dirty || entropy ? 1.f : 0.f, 0.f, 0.f);  // with entropies NaNs go unseen
+    out[0] = make_float4(st.M, st.over, st.id_lp, st.id_H);
+    out[1] = make_float4(st.g_lp, st.g_H, __int_as_float(st.up), st.mean);
+    out[2] = make_float4(st.dirty, st.term, st.w, 0.f);
   }
   return st;
 }
@@ -546,20 +573,18 @@ struct RowGradient {
   float at_id;
   bool lifted;  // with an entropy term, or where the row may hold NaNs
   // g_lp, g_H: the row's slopes times the gradient from above.
-  __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float T, bool dirty) {
-    const float c = kLog2e / T;
-    const bool entropy = g_H != 0.f;
-    lifted = entropy || dirty;
-    x.at(st.M, c, lifted);
-    const float lnS = logf(st.S), over = x.scale / (st.S * T);
-    k1 = entropy ? -g_H * kLn2 * over : 0.f;
-    k0 = -(g_lp + (entropy ? g_H * (st.H - lnS) : 0.f)) * over;
-    k0 -= k1 * x.delta;  // pair_fast's y is short of the true one by this
-    const float q = expf(st.lp);
-    at_id = g_lp * -expm1f(st.lp);  // 1 - q
-    if (entropy && q > 0.f) at_id -= g_H * q * (st.lp + st.H);
-    at_id /= T;
-    if (st.M == kNegInf) k0 = at_id = quiet_nan();
+  __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float T) {
+    lifted = g_H != 0.f || st.dirty != 0.f;
+    x.at(st.M, kLog2e / T, lifted);
+    const float over = st.over * x.scale;
+    k1 = 0.f;
+    k0 = -g_lp * over;
+    at_id = g_lp * st.id_lp;
+    if (g_H != 0.f) {
+      k1 = -g_H * kLn2 * over;
+      k0 = -(g_lp + g_H * st.mean) * over - k1 * x.delta;  // pair_fast's y is short of the true one by delta
+      at_id -= g_H * st.id_H;
+    }
   }
   // The unit's entries become their gradients, x being fast.
   template <typename TIn, bool kLift>
@@ -605,16 +630,16 @@ struct RowGradient {
 // Writes a run's gradients but the token's, from its first stage to its last or
 // (kBack) the other way; `a` holds the first of the whole ones that are not kept.
 template <bool kBack, bool kLift, typename TIn, int T>
-__device__ __forceinline__ void gradient_sweep(const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a, const RowGradient& g,
-                                               char* out, const Kept<T>& kept) {
+__device__ __forceinline__ void gradient_sweep(const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
+                                               const RowGradient& g, char* out, const Kept<T>& kept) {
   typedef typename Run<TIn, T>::Stage Stage;
   constexpr int kBytes = kBack ? -Stages<TIn, T>::kBytes : Stages<TIn, T>::kBytes;
-  const int64_t first = (int64_t)(kBack ? st.to - 1 : st.from) * Stages<TIn, T>::kBytes;
+  const int64_t first = (int64_t)(kBack ? st.whole - 1 : 0) * Stages<TIn, T>::kBytes;
   out += first;
   Stage b;
   int held = 0;
   if (kBack) {
-    held = min(kept.n, st.to - st.from);
+    held = min(kept.n, st.whole);
 #pragma unroll 1
     for (int s = 0; s < held; ++s) {
       kept.get(s, b);
@@ -627,7 +652,7 @@ __device__ __forceinline__ void gradient_sweep(const Stages<TIn, T>& st, typenam
     }
   }
   const char* in = st.base + (first + (int64_t)held * kBytes);
-  int left = st.to - st.from - held;
+  int left = st.whole - held;
   auto step = [&](Stage& v, Stage& w) {
     in += kBytes;
     if (left > 1) {
@@ -649,26 +674,25 @@ __device__ __forceinline__ void gradient_sweep(const Stages<TIn, T>& st, typenam
   }
 }
 template <bool kBack, typename TIn, int T>
-__device__ __forceinline__ void gradient_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
-                                             const RowGradient& shared, typename Elem<TIn>::Raw* grad, const Kept<T>& kept) {
+__device__ __forceinline__ void gradient_run(const Run<TIn, T>& run, const Stages<TIn, T>& st,
+                                             typename Run<TIn, T>::Stage& a, const RowGradient& shared,
+                                             typename Elem<TIn>::Raw* grad, const Kept<T>& kept) {
   const RowGradient g = shared;
   const bool same = run.aligned_with(grad), slow = !g.x.fast || !same;
-  // the row's ends, and whatever else is not aligned with its gradient or far from fp32's range
+  // what the whole stages leave; all of a row that is not aligned with its gradient or far from fp32's range
 #pragma unroll 1
-  for (int s = 0; s < st.all; ++s) {
-    if (!slow && s == st.from) s = st.to;
-    if (s >= st.all) break;
-    const int u = s * Run<TIn, T>::kStep + (int)threadIdx.x;
+  for (int s = slow ? 0 : st.whole; s < st.all; ++s) {
     typename Run<TIn, T>::Stage v;
-    run.template prefetch<LOAD_PLAIN>(u, v);
+    st.load_any(run, s, v);
 #pragma unroll
     for (int k = 0; k < kStage; ++k) {
       g.template apply<TIn>(v[k]);
-      if (u + k * T < run.n) run.store(grad, same, u + k * T, v[k]);
+      const int u = st.unit(run, s, k);
+      if (u >= 0) run.store(grad, same, u, v[k]);
     }
   }
   if (slow) return;
-  char* const out = reinterpret_cast<char*>(grad + run.j0) + (int)threadIdx.x * 32;
+  char* const out = reinterpret_cast<char*>(grad + run.j0) + (run.f + (int)threadIdx.x) * 32;
   if (g.lifted)
     gradient_sweep<kBack, true>(st, a, g, out, kept);
   else

@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, i
   Stages<TIn, T> st;
   st.init(run);
   typename Run<TIn, T>::Stage first;
-  if (st.from < st.to) st.template load<LOAD_ONCE>(st.from, first);
+  if (st.whole > 0) st.template load<LOAD_ONCE>(0, first);
   RowInputs in;
   if (!counts(a, i, in.id, in.w)) {
     if (tid == 0 && rank == 0) skip_row(a, i);
@@ -51,7 +51,19 @@ __global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, i
 }
 
 // The sums of a pair's two answers, its loss, and the slope of each of its rows.
+// Terms cancel, so they are added with what each addition loses (Knuth's two-sum):
+// fp64 took 9.6 us where this takes 6.9, for one pair of 22 rows and its row kernel.
 constexpr int kPairThreads = 256;
+
+struct Exact {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v, float low = 0.f) {
+    const float s = hi + v, b = s - hi, lost = (hi - (s - b)) + (v - b);
+    hi = s;
+    lo += (lost == lost ? lost : 0.f) + low;  // an infinite sum loses nothing
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
+};
 
 struct PairArgs {
   ls_preference p;
@@ -64,13 +76,15 @@ struct PairArgs {
 
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   constexpr int kW = kPairThreads / 32;
-  __shared__ double red[4][kW];
+  __shared__ Exact red[4][kW];
   const int tid = threadIdx.x, lane = tid & 31;
   const int32_t p = (int32_t)blockIdx.x;
+  const int32_t* at = a.p.answer_offsets + 2 * (int64_t)p;
+  // after a row kernel, which has waited for whatever wrote them, the offsets are there
+  if (a.n == 0) wait_for_previous();
+  const int32_t lo = at[0], mid = at[1], hi = at[2];
   wait_for_previous();
   let_next_start();
-  const int32_t* at = a.p.answer_offsets + 2 * (int64_t)p;
-  const int32_t lo = at[0], mid = at[1], hi = at[2];
   if (lo < 0 || mid < lo || hi < mid || hi > a.n) {
     if (tid == 0) {
       a.out_loss[p] = quiet_nan();
@@ -79,19 +93,23 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
     }
     return;
   }
-  double v[4] = {0.0, 0.0, 0.0, 0.0};  // sum and weight of the chosen, of the rejected answer
+  Exact v[4] = {};  // sum and weight of the chosen, of the rejected answer
+  float mine = 0.f;  // the weight of this thread's first row
   for (int64_t i = lo + tid; i < hi; i += kPairThreads) {
     const float term = a.stats[i].term, w = a.stats[i].w;
-    const bool first = i < mid;
-    v[0] += first ? term : 0.f;
-    v[1] += first ? w : 0.f;
-    v[2] += first ? 0.f : term;
-    v[3] += first ? 0.f : w;
+    if (i < lo + kPairThreads) mine = w;
+    const int k = i < mid ? 0 : 2;
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      v[q].add(k == q ? term : 0.f);
+      v[q + 1].add(k == q ? w : 0.f);
+    }
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[q] += __shfl_xor_sync(0xFFFFFFFFu, v[q], o);
+    for (int o = 16; o > 0; o >>= 1)
+      v[q].add(__shfl_xor_sync(0xFFFFFFFFu, v[q].hi, o), __shfl_xor_sync(0xFFFFFFFFu, v[q].lo, o));
     if (lane == 0) red[q][tid >> 5] = v[q];
   }
   __syncthreads();
@@ -99,24 +117,28 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   for (int q = 0; q < 4; ++q) {
     v[q] = red[q][0];
 #pragma unroll
-    for (int k = 1; k < kW; ++k) v[q] += red[q][k];
+    for (int k = 1; k < kW; ++k) v[q].add(red[q][k].hi, red[q][k].lo);
   }
   float over[2] = {1.f, 1.f};
   if (a.p.average) {
-    over[0] = v[1] != 0.0 ? (float)(1.0 / v[1]) : 0.f;
-    over[1] = v[3] != 0.0 ? (float)(1.0 / v[3]) : 0.f;
-    v[0] = v[1] != 0.0 ? v[0] / v[1] : 0.0;
-    v[2] = v[3] != 0.0 ? v[2] / v[3] : 0.0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float w = v[2 * k + 1].value();
+      over[k] = w != 0.f ? 1.f / w : 0.f;
+      v[2 * k] = Exact{w != 0.f ? v[2 * k].value() / w : 0.f, 0.f};
+    }
   }
-  const float u = (float)(v[0] - v[2]), beta = a.p.beta;
-  const float h = (float)((double)beta * (v[0] - v[2]) - (double)a.p.margin);
+  const float s[2] = {v[0].value(), v[2].value()};
+  v[0].add(-v[2].hi, -v[2].lo);
+  const float u = v[0].value(), beta = a.p.beta;
+  const float h = fmaf(beta, u, -a.p.margin);
   float loss, slope;  // of u
   if (a.p.kind == LS_PREFERENCE_SIGMOID) {
-    const float e = a.p.label_smoothing, tail = log1pf(expf(-fabsf(h)));
-    const float down = 1.f / (1.f + expf(h)), up = 1.f / (1.f + expf(-h));  // sigma(-h), sigma(h)
+    const float e = a.p.label_smoothing, small = expf(-fabsf(h)), tail = log1pf(small);
+    const float far = 1.f / (1.f + small), near = small * far;  // sigma(|h|), sigma(-|h|)
     loss = (1.f - e) * (fmaxf(-h, 0.f) + tail);
     if (e > 0.f) loss += e * (fmaxf(h, 0.f) + tail);
-    slope = beta * (e * up - (1.f - e) * down);
+    slope = beta * (e * (h > 0.f ? far : near) - (1.f - e) * (h > 0.f ? near : far));
     if (h != h) loss = slope = h;
   } else if (a.p.kind == LS_PREFERENCE_HINGE) {
     loss = h != h ? h : fmaxf(1.f - h, 0.f);
@@ -129,12 +151,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   if (tid == 0) {
     a.out_loss[p] = loss;
     if (a.out_log_ratios) {
-      a.out_log_ratios[2 * (int64_t)p] = (float)v[0];
-      a.out_log_ratios[2 * (int64_t)p + 1] = (float)v[2];
+      a.out_log_ratios[2 * (int64_t)p] = s[0];
+      a.out_log_ratios[2 * (int64_t)p + 1] = s[1];
     }
   }
   for (int64_t i = lo + tid; i < hi; i += kPairThreads) {
-    const float w = a.stats[i].w;
+    const float w = i < lo + kPairThreads ? mine : a.stats[i].w;
     a.stats[i].g_lp = w == 0.f ? 0.f : i < mid ? slope * w * over[0] : -slope * w * over[1];
     a.stats[i].up = p;
   }
@@ -156,12 +178,21 @@ struct TokenBackArgs {
   int64_t grad_stride;
 };
 
-constexpr int kTokenBackRun = 2048;  // units of a CTA's run
+// CTAs of 128 threads with runs of four stages (32 KB), fewer where that would
+// leave SMs without a second wave.  2048 x 128256 bf16, one row in four of them
+// without a gradient, with runs of 1 / 2 / 4 stages 162 / 144 / 141 us; without such
+// rows 164 / 153 / 154 (the measured copy rate); one row 1.8 / 2.1 / 2.7; 256 threads
+// the same.  Each run pays for a row's scalars again, 44 bytes and twenty operations;
+// working them out from the row's sum here instead of in the forward pass took 333 x
+// 32000 from 7.2 to 8.7 us.
+constexpr int kBackThreads = 128;
+constexpr int kBackRun = 4;  // stages at most
 
-template <typename TIn, int T>
-__global__ void __launch_bounds__(T, 1024 / T) token_backward_kernel(const TokenBackArgs a, int runs, int upc) {
+template <typename TIn>
+__global__ void __launch_bounds__(kBackThreads, 1024 / kBackThreads)
+    token_backward_kernel(const TokenBackArgs a, int runs, int upc) {
+  constexpr int T = kBackThreads;
   using Raw = typename Elem<TIn>::Raw;
-  __shared__ RowGradient g;
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (unsigned)runs;
   wait_for_previous();
@@ -169,15 +200,22 @@ __global__ void __launch_bounds__(T, 1024 / T) token_backward_kernel(const Token
   Run<TIn, T> run;
   run.init(a.logits, i, a.row_stride, a.vocab, upc, (int)(blockIdx.x % (unsigned)runs));
   Raw* grad = static_cast<Raw*>(a.out_grad) + i * a.grad_stride;
+  Stages<TIn, T> stages;
+  stages.init(run);
+  typename Run<TIn, T>::Stage first;
+  // before the row's scalars are known, but where rows may wait: one without a gradient is not read there
+  const bool early = upc < kBackRun * T * kStage;
+  if (early && stages.whole > 0) stages.template load<LOAD_PLAIN>(0, first);
   const float4* in = reinterpret_cast<const float4*>(a.stats + i);
   const float4 s0 = in[0], s1 = in[1];
   TokenStats st;
   st.M = s0.x;
-  st.S = s0.y;
-  st.H = s0.z;
-  st.lp = s0.w;
-  const bool dirty = in[2].y != 0.f;
-  const int32_t up = __float_as_int(s1.z);
+  st.over = s0.y;
+  st.id_lp = s0.z;
+  st.id_H = s0.w;
+  st.mean = s1.w;
+  st.dirty = in[2].x;
+  const int32_t id = a.ids[i], up = __float_as_int(s1.z);
   const bool has = up >= 0 && up < a.ups;  // stats of another call do not lead out of bounds
   // a slope of 0 counts nothing, whatever the gradient from above
   const float g_lp = s1.x == 0.f ? 0.f : s1.x * (!a.up_lp ? a.none_lp : has ? a.up_lp[up] : quiet_nan());
@@ -188,13 +226,9 @@ __global__ void __launch_bounds__(T, 1024 / T) token_backward_kernel(const Token
     for (int u = tid; u < run.n; u += T) run.store(grad, same, u, z);
     return;
   }
-  Stages<TIn, T> stages;
-  stages.init(run);
-  typename Run<TIn, T>::Stage first;
-  if (stages.from < stages.to) stages.template load<LOAD_PLAIN>(stages.from, first);
-  const int32_t id = a.ids[i];
-  if (tid == 0) g.init(st, g_lp, g_H, a.temperature, dirty);
-  __syncthreads();
+  if (!early && stages.whole > 0) stages.template load<LOAD_PLAIN>(0, first);
+  RowGradient g;
+  g.init(st, g_lp, g_H, a.temperature);
   gradient_run<false>(run, stages, first, g, grad, Kept<T>{nullptr, 0});
   if (run.place(id) >= 0) {  // in this CTA's run: the same in every thread
     __syncthreads();
@@ -246,23 +280,19 @@ static ls_status forward(const TokenArgs& a, ls_dtype dtype, bool entropy, cudaS
   return entropy ? pick_forward<float, true>(a, dtype, st) : pick_forward<float, false>(a, dtype, st);
 }
 
-template <typename TIn, int T>
-static ls_status launch_backward(const TokenBackArgs& a, int64_t units, int32_t n, cudaStream_t st) {
-  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
-  const int upc = (units + kTokenBackRun - 1) / kTokenBackRun * n >= 8 * sms ? kTokenBackRun : T * kStage;
-  const int64_t runs = (units + upc - 1) / upc;
-  if (runs * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
-  return launch_kernel(token_backward_kernel<TIn, T>, dim3((unsigned)(runs * n)), T, 1, 0, st, a, (int)runs, upc);
-}
-
 static ls_status backward(const TokenBackArgs& a, ls_dtype dtype, int32_t n, void* stream) {
+  constexpr int kStep = kBackThreads * kStage;  // units of a stage
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t units = row_units(a.vocab, dtype);
-  if (units <= 512)  // 16 KB
-    return dtype == LS_DTYPE_BF16 ? launch_backward<bf16_tag, 128>(a, units, n, st)
-                                  : launch_backward<float, 128>(a, units, n, st);
-  return dtype == LS_DTYPE_BF16 ? launch_backward<bf16_tag, 256>(a, units, n, st)
-                                : launch_backward<float, 256>(a, units, n, st);
+  const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
+  int upc = kBackRun * kStep;
+  while (upc > kStep && (units + upc - 1) / upc * n < 16 * sms) upc /= 2;
+  const int64_t runs = (units + upc - 1) / upc;
+  if (runs * n > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(runs * n));
+  return dtype == LS_DTYPE_BF16
+             ? launch_kernel(token_backward_kernel<bf16_tag>, grid, kBackThreads, 1, 0, st, a, (int)runs, upc)
+             : launch_kernel(token_backward_kernel<float>, grid, kBackThreads, 1, 0, st, a, (int)runs, upc);
 }
 
 static bool finite(float v) { return v - v == 0.f; }
@@ -310,7 +340,8 @@ static TokenArgs rows_of(const void* logits, int64_t vocab, int64_t row_stride, 
 // The three backward calls: what stands for a missing gradient differs.
 static ls_status backward_call(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, int32_t n,
                                const int32_t* ids, float temperature, const float* stats, const float* up_lp,
-                               const float* up_H, int32_t ups, float none, void* out_grad, int64_t grad_stride, void* stream) {
+                               const float* up_H, int32_t ups, float none, void* out_grad, int64_t grad_stride,
+                               void* stream) {
   if (n < 0) return LS_ERR_INVALID_ARG;
   if (n == 0) return LS_OK;
   if (!rows_ok(logits, dtype, vocab, row_stride, ids, temperature) || !stats || !aligned16(stats) ||

@@ -240,8 +240,8 @@ PyObject* distill_loss_grad(PyObject*, PyObject* const* args, Py_ssize_t positio
 
 // bind(LSError, addresses of the C functions in the order of the headers)
 PyObject* bind(PyObject*, PyObject* args) {
-  void* const to[] = {&f_process, &f_top,    &f_loss,            &f_backward,    &f_grad,       &f_score,
-                      &f_score_backward, &f_policy, &f_policy_backward, &f_policy_grad, &f_preference, &f_preference_backward};
+  void* const to[] = {&f_process, &f_top, &f_loss, &f_backward, &f_grad, &f_score, &f_score_backward, &f_policy,
+                      &f_policy_backward, &f_policy_grad, &f_preference, &f_preference_backward};
   constexpr int kCount = sizeof(to) / sizeof(to[0]);
   if (PyTuple_GET_SIZE(args) != 1 + kCount) {
     PyErr_SetString(PyExc_TypeError, "bind() takes LSError and the address of each call");
@@ -301,8 +301,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_row_ops_c",
 
 PyMODINIT_FUNC PyInit__row_ops_c() {
   s_marshalled = PyUnicode_InternFromString("_marshalled");
-  for (Names* n : {&n_process, &n_top, &n_loss, &n_backward, &n_grad, &n_score, &n_score_backward, &n_policy, &n_policy_backward,
-                   &n_policy_grad, &n_preference, &n_preference_backward})
+  for (Names* n : {&n_process, &n_top, &n_loss, &n_backward, &n_grad, &n_score, &n_score_backward, &n_policy,
+                   &n_policy_backward, &n_policy_grad, &n_preference, &n_preference_backward})
     for (int i = 0; i < n->count; ++i) n->name[i] = PyUnicode_InternFromString(n->text[i]);
   return PyModule_Create(&module);
 }

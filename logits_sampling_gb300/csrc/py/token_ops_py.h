@@ -86,7 +86,7 @@ constexpr const char* doc_score =
     "token_log_probs(logits, ids, temperature=1.0, entropy=False, out=None, out_entropy=None, out_stats=None,\n"
     "                error_word=None, stream=None) -> (log_probs, entropy, stats)\n\n"
     "ls_token_log_probs: the log-prob of token ids[i] (int32 [n]) under each row (float32 [n]), the row's entropy\n"
-    "(float32 [n], None unless asked for) and what token_log_probs_backward needs (float32 [n, 32]).";
+    "(float32 [n], None unless asked for) and what token_log_probs_backward needs (float32 [n, 12]).";
 
 Names n_score_backward = {"token_log_probs_backward", 8, 3,
                           {"logits", "ids", "stats", "grad_log_probs", "grad_entropy", "temperature", "out", "stream"}};
@@ -168,7 +168,7 @@ constexpr const char* doc_policy =
     "            clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, kl='k3', entropy_coef=0.0, entropy=False,\n"
     "            out=None, out_metrics=None, out_stats=None, error_word=None, stream=None) -> (loss, metrics, stats)\n\n"
     "ls_policy_loss: the loss per row (float32 [n]), its metrics (float32 [n, 4]: log-prob, entropy, KL, ratio) and\n"
-    "what policy_loss_backward needs (float32 [n, 32]).";
+    "what policy_loss_backward needs (float32 [n, 12]).";
 
 Names n_policy_backward = {"policy_loss_backward", 7, 3,
                            {"logits", "ids", "stats", "grad_loss", "temperature", "out", "stream"}};
@@ -208,8 +208,8 @@ PyObject* loss_backward(const Names& names, const char* what, bool per_row, PyOb
 PyObject* policy_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t positional, PyObject* keywords) {
   return loss_backward(n_policy_backward, "ls_policy_loss_backward", true, args, positional, keywords,
                        [](const Back& b, const Output& grad, void* stream) {
-                         return f_policy_backward(b.m.p, b.m.dtype, b.m.vocab, b.m.stride, b.n, b.ids, b.temperature, b.stats,
-                                                  b.grad_loss, grad.p, grad.stride, stream);
+                         return f_policy_backward(b.m.p, b.m.dtype, b.m.vocab, b.m.stride, b.n, b.ids, b.temperature,
+                                                  b.stats, b.grad_loss, grad.p, grad.stride, stream);
                        });
 }
 PyObject* preference_loss_backward(PyObject*, PyObject* const* args, Py_ssize_t positional, PyObject* keywords) {
@@ -227,7 +227,8 @@ constexpr const char* doc_preference_backward =
     "ls_preference_loss_backward: the gradient, [n, vocab] of the logits' type; grad_loss has an entry per pair; out may\n"
     "be the logits themselves.";
 
-Names n_policy_grad = {"policy_loss_grad", 19, 3, {POLICY_NAMES, "out_loss", "out_grad", "out_metrics", "error_word", "stream"}};
+Names n_policy_grad = {"policy_loss_grad", 19, 3,
+                       {POLICY_NAMES, "out_loss", "out_grad", "out_metrics", "error_word", "stream"}};
 PyObject* policy_loss_grad(PyObject*, PyObject* const* args, Py_ssize_t positional, PyObject* keywords) {
   return entry([&]() -> PyObject* {
     PyObject* o[kMostArgs];
@@ -304,7 +305,7 @@ constexpr const char* doc_preference =
     "                loss='sigmoid', label_smoothing=0.0, margin=0.0, average=False, out=None, out_log_ratios=None,\n"
     "                out_stats=None, error_word=None, stream=None) -> (loss, log_ratios, stats)\n\n"
     "ls_preference_loss: the loss per pair (float32 [pairs]), the log-ratio of each answer (float32 [2 * pairs], chosen\n"
-    "and rejected in turn) and what preference_loss_backward needs (float32 [n, 32]).  answer_offsets int32\n"
+    "and rejected in turn) and what preference_loss_backward needs (float32 [n, 12]).  answer_offsets int32\n"
     "[2 * pairs + 1]: pair p's chosen answer are the rows [offsets[2p], offsets[2p + 1]), its rejected one those up to\n"
     "offsets[2p + 2].";
 

@@ -118,7 +118,7 @@ def test_preference_refusals(lib):
 def _arguments():
     """Per call: what it needs, and every further tensor that it may be given, all on device 0."""
     x, ids, vec, word = Claimed((N, V)), Claimed((N,), I32), Claimed((N,)), Claimed((1,), I32)
-    stats, off, metrics = Claimed((N, 32)), Claimed((5,), I32), Claimed((N, 4))
+    stats, off, metrics = Claimed((N, 12)), Claimed((5,), I32), Claimed((N, 4))
     rows = {"logits": x, "ids": ids}
     policy = {"old_log_probs": vec, "ref_log_probs": vec, "weights": vec, "out_metrics": metrics, "error_word": word}
     return {
