@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
   if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
   load_inputs<TIn>(a, i, in);
   const Kept<T> kept{dyn_smem + tid, keep};
-  const float c = kLog2e / a.temperature;
+  const float c = a.c;
   Moments r;
   bool careful = false;
 #pragma unroll 1
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
   if (C > 1) cluster_moments<kEntropy>(r, careful, c, parts, C, rank);
   if (tid == 0) {
     const TokenStats s = finish_row(a, i, r, in, kEntropy, careful, rank == 0);
-    g.init(s, s.g_lp, s.g_H, a.temperature);
+    g.init(s, s.g_lp, s.g_H, c);
   }
   __syncthreads();
   gradient_run<true>(run, st, first, g, grad, kept);

@@ -35,7 +35,7 @@ struct TokenArgs {
   int64_t vocab, row_stride;
   int32_t n;
   const int32_t* ids;
-  float temperature;
+  float temperature, c, inv_T;  // c = log2(e) / T
   int kind;
   ls_policy policy;            // of a preference loss: weights and ref_log_probs only
   const int32_t* offsets;      // preference
@@ -479,24 +479,27 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   // exact parts.  H likewise.
   const int k = (int)(__float_as_uint(r.s) >> 23 & 255u) - 127;
   const float log2s = log2f(__uint_as_float((__float_as_uint(r.s) & 0x7FFFFFu) | 0x3F800000u));
-  const float T = a.temperature, c = kLog2e / T, p = x * c, q = r.m * c;
+  const float c = a.c, p = x * c, q = r.m * c;
   if (fabsf(p) < 1e30f && fabsf(q) < 1e30f) {
     const float y = p - q, z = y - p, lo = (p - (y - z)) - (q + z) + (fmaf(x, c, -p) - fmaf(r.m, c, -q));
     lp = kLn2 * (((y - (float)k) + lo) - log2s);
   } else {
-    lp = (x == r.m ? 0.f : (x - r.m) / T) - kLn2 * ((float)k + log2s);
+    lp = (x == r.m ? 0.f : (x - r.m) / a.temperature) - kLn2 * ((float)k + log2s);
   }
-  const float mean = entropy ? -kLn2 * (r.e / r.s) : quiet_nan();  // a gradient of what was not computed shows
-  H = entropy ? kLn2 * (((float)k - r.e / r.s) + log2s) : quiet_nan();
+  st.mean = H = quiet_nan();  // a gradient of what was not computed shows
+  if (entropy) {
+    const float y = r.e / r.s;
+    st.mean = -kLn2 * y;
+    H = kLn2 * (((float)k - y) + log2s);
+  }
   if (r.m == kNegInf) {
     lp = H = quiet_nan();
     if (write && a.error_word) atomicOr(a.error_word, LS_ROW_ERR_NO_FINITE);
   }
-  const float q_id = expf(lp);
-  st.over = r.m == kNegInf ? quiet_nan() : 1.f / (r.s * T);
-  st.id_lp = -expm1f(lp) / T;  // 1 - q
-  st.id_H = q_id > 0.f ? q_id * (lp + H) / T : q_id;
-  st.mean = mean;
+  st.over = r.m == kNegInf ? quiet_nan() : __frcp_rn(r.s * a.temperature);
+  st.id_lp = -expm1f(lp) * a.inv_T;  // 1 - q
+  st.id_H = quiet_nan();
+  if (entropy) st.id_H = lp == kNegInf ? 0.f : expf(lp) * (lp + H) * a.inv_T;
   st.dirty = dirty || entropy ? 1.f : 0.f;  // with entropies NaNs go unseen
   st.g_lp = st.g_H = st.term = st.w = 0.f;
   st.up = (int32_t)i;
@@ -572,10 +575,10 @@ struct RowGradient {
   float k0, k1;
   float at_id;
   bool lifted;  // with an entropy term, or where the row may hold NaNs
-  // g_lp, g_H: the row's slopes times the gradient from above.
-  __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float T) {
+  // g_lp, g_H: the row's slopes times the gradient from above; c = log2(e) / T.
+  __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float c) {
     lifted = g_H != 0.f || st.dirty != 0.f;
-    x.at(st.M, kLog2e / T, lifted);
+    x.at(st.M, c, lifted);
     const float over = st.over * x.scale;
     k1 = 0.f;
     k0 = -g_lp * over;

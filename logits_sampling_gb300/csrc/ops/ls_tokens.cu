@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, i
   }
   if (C > 1) cluster_arrive();  // the peers' shared memory may be written once all have arrived
   load_inputs<TIn>(a, i, in);
-  const float c = kLog2e / a.temperature;
+  const float c = a.c;
   Moments r;
   bool careful = false;
 #pragma unroll 1
@@ -168,7 +168,7 @@ struct TokenBackArgs {
   const void* logits;
   int64_t vocab, row_stride;
   const int32_t* ids;
-  float temperature;
+  float c;  // log2(e) / T
   const TokenStats* stats;
   const float* up_lp;  // the gradient from above, by stats.up
   const float* up_H;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kBackThreads, 1024 / kBackThreads)
   }
   if (!early && stages.whole > 0) stages.template load<LOAD_PLAIN>(0, first);
   RowGradient g;
-  g.init(st, g_lp, g_H, a.temperature);
+  g.init(st, g_lp, g_H, a.c);
   gradient_run<false>(run, stages, first, g, grad, Kept<T>{nullptr, 0});
   if (run.place(id) >= 0) {  // in this CTA's run: the same in every thread
     __syncthreads();
@@ -333,6 +333,8 @@ static TokenArgs rows_of(const void* logits, int64_t vocab, int64_t row_stride, 
   a.n = n;
   a.ids = ids;
   a.temperature = temperature;
+  a.c = kLog2e / temperature;
+  a.inv_T = 1.f / temperature;
   a.kind = kind;
   return a;
 }
@@ -347,7 +349,7 @@ static ls_status backward_call(const void* logits, ls_dtype dtype, int64_t vocab
   if (!rows_ok(logits, dtype, vocab, row_stride, ids, temperature) || !stats || !aligned16(stats) ||
       !grad_ok(logits, dtype, vocab, row_stride, n, out_grad, grad_stride))
     return LS_ERR_INVALID_ARG;
-  const TokenBackArgs a{logits, vocab, row_stride, ids,  temperature, reinterpret_cast<const TokenStats*>(stats),
+  const TokenBackArgs a{logits, vocab, row_stride, ids,  kLog2e / temperature, reinterpret_cast<const TokenStats*>(stats),
                         up_lp,  up_H,  ups,        none, none,        out_grad,
                         grad_stride};
   return backward(a, dtype, n, stream);
