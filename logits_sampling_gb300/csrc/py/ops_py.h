@@ -5,7 +5,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -164,8 +165,9 @@ struct Output {
   at::ScalarType type = at::kFloat;
   void make(const Matrix& m) {
     if (given) return;
-    // without a turn through the dispatcher
-    made = at::detail::empty_cuda(shape, type, m.t->device(), std::nullopt);
+    // without a turn through the dispatcher; the logits' device is the current one
+    made = at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
+                                     c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
     p = made.data_ptr();
   }
   // A new reference.  To autograd a caller's tensor has been written in place: a
