@@ -389,10 +389,13 @@ __device__ __forceinline__ Moments block_moments(Moments t, float c, Moments* re
   if (kEntropy) t.e = warp_reduce(t.e, OpAddF());
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
   __syncthreads();
-  Moments r = red[threadIdx.x & (kWarps - 1)];
+  constexpr int kLanes = kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : 16;  // that hold one, again and again over the warp
+  static_assert(kWarps <= 16, "");
+  const int at = threadIdx.x & (kLanes - 1);
+  Moments r = at < kWarps ? red[at] : Moments{kNegInf, 0.f, 0.f};
   r = rebase(r, warp_max(r.m), c);
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) {
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
     r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
     if (kEntropy) r.e += __shfl_xor_sync(0xFFFFFFFFu, r.e, o);
   }

@@ -244,22 +244,27 @@ __global__ void __launch_bounds__(kBackThreads, 1024 / kBackThreads)
 //   few rows of 128 KB and more: a row over as many CTAs as find room at once.  8
 //     rows of 256 KB 256x8 4.1, 256x4 4.7, 256x1 6.6; 64 of them 6.8, 6.9, 10.4; of 64
 //     KB 5.1, 4.2, 4.2
-//   else one CTA per row, the largest for which every row has its own at once; when
-//     there are more rows than that, the smallest.  304 x 256 KB 512x1 14.1, 256x1
-//     15.3, 128x1 19.3; 400 21.0, 18.1, 21.5; 672 30.7, 32.7, 29.3; 2048 79.4, 78.9,
-//     76.9
+//   else one CTA per row, the largest for which every row has its own at once.
+//     Rows of 256 KB with 512 / 256 / 192 / 128 threads: 304 of them 14.3, 15.6, 16.9,
+//     20.1; 608 25.9, 24.7, 25.3, 26.9; 760 34.6, 36.2, 30.2, 31.5; 1216 48.8, 46.6,
+//     49.0, 46.2
+//   more rows than that: 128 or 192 threads, whichever leaves the last wave
+//     fuller.  1400 63.3 with 128, 53.4 with 192; 2048 76.4, 77.5 (waves of .68, .70)
 struct ForwardPlan {
   int threads, ctas;
 };
 static ForwardPlan forward_plan(int32_t n, int64_t bytes) {
   const int sms = device_attr<cudaDevAttrMultiProcessorCount>();
-  if (bytes <= 16 * 1024) return {128, 1};
+  if (bytes <= 16 * 1024 || sms <= 0) return {128, 1};
   if (n <= 128 && bytes >= 128 * 1024) {
     int c = 1;
     while (c < kMaxCluster && n * c * 2 <= 512) c *= 2;
     return {256, c};
   }
-  return {n <= 2 * sms ? 512 : n <= 4 * sms ? 256 : 128, 1};
+  if (n <= 5 * sms) return {n <= 2 * sms ? 512 : n <= 4 * sms ? 256 : 192, 1};
+  // the rows of the last wave, in sixty-fourths of one
+  const auto last = [&](int per_sm) { return (int)((int64_t)((n - 1) % (per_sm * sms) + 1) * 64 / (per_sm * sms)); };
+  return {n > 8 * sms && last(5) > last(8) + 4 ? 192 : 128, 1};
 }
 
 template <typename TIn, bool kEntropy>
@@ -270,6 +275,7 @@ static ls_status pick_forward(const TokenArgs& a, ls_dtype dtype, cudaStream_t s
   if ((int64_t)a.n * p.ctas > 0x7FFFFFFFll) return LS_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)a.n * p.ctas);
   return p.threads == 128   ? launch_kernel(token_kernel<TIn, kEntropy, 128>, grid, 128, p.ctas, 0, st, a, upc)
+         : p.threads == 192 ? launch_kernel(token_kernel<TIn, kEntropy, 192>, grid, 192, p.ctas, 0, st, a, upc)
          : p.threads == 256 ? launch_kernel(token_kernel<TIn, kEntropy, 256>, grid, 256, p.ctas, 0, st, a, upc)
                             : launch_kernel(token_kernel<TIn, kEntropy, 512>, grid, 512, p.ctas, 0, st, a, upc);
 }

@@ -176,7 +176,7 @@ def test_score_special_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("n", [20, 140, 320, 620])
+@pytest.mark.parametrize("n", [20, 140, 320, 620, 800])
 def test_score_special_long_rows(dtype, n):
     """The same in rows of many stages, for each layout of a batch; and rows whose maximum is far above what the first
     stages hold, below their reference, or all in one place."""
