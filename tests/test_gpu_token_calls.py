@@ -179,3 +179,43 @@ def test_refusals_on_the_device():
     g, = torch.autograd.grad(ls.score(leaf, ids)[0].sum(), leaf, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()                                                   # no second derivatives
+
+
+@pytest.mark.parametrize("op", ["score", "policy", "preference"])
+def test_autograd_in_a_captured_graph(op):
+    """Forward and backward captured (no eager graph of the leaf is alive then), replayed on new values."""
+    import logits_sampling_gb300 as ls
+    import torch
+    n, V = 12, 2003
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    leaf = torch.empty(n, V, device="cuda").normal_(generator=gen).requires_grad_()
+    ids = torch.randint(V, (n,), generator=gen, device="cuda").to(torch.int32)
+    adv = torch.empty(n, device="cuda").normal_(generator=gen)
+    off = _dev([0, 4, 7, 9, 12], np.int32)
+
+    def total():
+        if op == "score":
+            lp, h = ls.score(leaf, ids, entropy=True)
+            return (adv * lp).sum() + h.sum()
+        return ls.policy(leaf, ids, adv, adv - 6.0)[0].sum() if op == "policy" else ls.preference(leaf, ids, off)[0].sum()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        total().backward()
+    torch.cuda.current_stream().wait_stream(side)
+    leaf.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        value = total()
+        value.backward()
+    captured = leaf.grad
+    with torch.no_grad():
+        leaf.copy_(leaf.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    got, got_grad = value.detach().clone(), captured.clone()
+    leaf.grad = None
+    want = total()
+    want.backward()
+    assert torch.equal(got, want.detach()) and torch.equal(got_grad, leaf.grad)
