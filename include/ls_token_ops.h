@@ -106,7 +106,10 @@ typedef struct {
  *   loss[i] = weights[i] * (-s + kl_coef * KL - entropy_coef * H)
  * The gradient goes through u where u <= v and the bound of dual_clip does not
  * hold, through KL and through H.  A = 0 gives s = 0 whatever r is.  A log-ratio
- * of two log-probs of -inf (a token that both sides exclude) is 0.
+ * of two log-probs of -inf (a token that both sides exclude) is 0.  Ratio and KL
+ * are those of lp as it is returned in fp32: where old and ref are what the same
+ * rows gave before, they are 1 and 0.  Where the loss is infinite (a token that one
+ * side alone excludes) its gradient is not finite.
  *
  *   out_loss     device float[n]
  *   out_metrics  device float[LS_POLICY_METRICS * n], 16-byte aligned, or NULL

@@ -58,11 +58,25 @@ struct Moments {
   float m, s, e;
 };
 
-// 2^(d c): the product's rounding, up to 2^-24 of an exponent of 20 or 30, would
-// stay in every sum that is moved to another reference.
+// 2^(d c) for what a whole sum is multiplied by: the product's rounding, up to 2^-24
+// of an exponent of 20 or 30, is taken into account, and the exponential is e^z's
+// series for |z| <= ln 2 / 2 (z^8 / 8! is 5e-9), because the instruction is low on
+// average: 5.05e-8 of its result over 16.8 million exponents in [-20, 0], 1.42e-7 at
+// most.
+constexpr float kExpLow = 5.05e-8f;
 __device__ __forceinline__ float factor(float d, float c) {
   const float y = d * c;
-  return y > -200.f ? ex2(y) * fmaf(fmaf(d, c, -y), kLn2, 1.f) : 0.f;
+  if (!(y > -126.f)) return 0.f;
+  const float n = rintf(y), z = ((y - n) + fmaf(d, c, -y)) * kLn2;
+  float e = 1.f / 5040.f;
+  e = fmaf(e, z, 1.f / 720.f);
+  e = fmaf(e, z, 1.f / 120.f);
+  e = fmaf(e, z, 1.f / 24.f);
+  e = fmaf(e, z, 1.f / 6.f);
+  e = fmaf(e, z, 0.5f);
+  e = fmaf(e, z, 1.f);
+  e = fmaf(e, z, 1.f);
+  return e * __int_as_float(((int)n + 127) << 23);
 }
 
 // The same set against a maximum m >= a.m.  A NaN in a.s stays one.
@@ -465,8 +479,16 @@ __device__ __forceinline__ void load_inputs(const TokenArgs& a, int64_t i, RowIn
   in.ref = a.policy.ref_log_probs ? a.policy.ref_log_probs[i] : 0.f;
 }
 
-// a - b of two log-probs, 0 where both are -inf.
-__device__ __forceinline__ float log_ratio(float a, float b) { return a == kNegInf && b == kNegInf ? 0.f : a - b; }
+// a + rest - b of two log-probs, 0 where both are -inf.
+__device__ __forceinline__ float log_ratio(float a, float rest, float b) {
+  return a == kNegInf && b == kNegInf ? 0.f : (a - b) + rest;
+}
+// RN(a + b); what the rounding lost is added to `lost` (Knuth's two-sum).
+__device__ __forceinline__ float two_sum(float a, float b, float& lost) {
+  const float s = a + b, v = s - a;
+  lost += (a - (s - v)) + (b - v);
+  return s;
+}
 
 // The loss's slopes and outputs of row i from its moments (one thread; `write`:
 // this one stores the outputs).
@@ -478,14 +500,21 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   st.M = r.m;
   // In base-2 exponents, S = 2^k s: lp = ln 2 ((x - M) c - k - log2 s), c the factor
   // that the sum was made with, so that its rounding moves x and S alike (against
-  // (x - M) / T it would be a bias of every row); (x - M) c from both products'
-  // exact parts.  H likewise.
+  // (x - M) / T it would be a bias of every row).  With what each step loses kept
+  // (two-sums, products' remainders): an answer's ratio is a sum of differences of
+  // log-probs, in which the rounding of lp itself, up to 1e-6, would be the largest
+  // error.  A sum's terms but the maximum's own, 1, are low by kExpLow on average.
   const int k = (int)(__float_as_uint(r.s) >> 23 & 255u) - 127;
   const float log2s = log2f(__uint_as_float((__float_as_uint(r.s) & 0x7FFFFFu) | 0x3F800000u));
   const float c = a.c, p = x * c, q = r.m * c;
+  float rest = 0.f;  // of lp
   if (fabsf(p) < 1e30f && fabsf(q) < 1e30f) {
-    const float y = p - q, z = y - p, lo = (p - (y - z)) - (q + z) + (fmaf(x, c, -p) - fmaf(r.m, c, -q));
-    lp = kLn2 * (((y - (float)k) + lo) - log2s);
+    float lo = fmaf(x, c, -p) - fmaf(r.m, c, -q) - kExpLow * kLog2e * (1.f - 1.f / r.s);
+    const float y = two_sum(p, -q, lo), z = two_sum(y, -(float)k, lo), t = two_sum(z, -log2s, lo);
+    const float v = kLn2 * t;
+    lo = fmaf(kLn2, t, -v) + fmaf(-1.9046543e-9f, t, kLn2 * lo);  // ln 2 less kLn2
+    lp = v + lo;
+    rest = (v - lp) + lo;
   } else {
     lp = (x == r.m ? 0.f : (x - r.m) / a.temperature) - kLn2 * ((float)k + log2s);
   }
@@ -513,7 +542,8 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   } else if (a.kind == KIND_POLICY) {
     const ls_policy& p = a.policy;
     const float A = in.A;
-    const float ratio = p.old_log_probs ? expf(log_ratio(lp, in.old)) : lp == lp ? 1.f : lp;
+    // from lp as it is returned: a policy that has not moved has ratio 1 and KL 0
+    const float ratio = p.old_log_probs ? expf(log_ratio(lp, 0.f, in.old)) : lp == lp ? 1.f : lp;
     float s = 0.f, slope = 0.f;
     if (A != 0.f) {
       const float u = ratio * A, v = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * A;
@@ -526,7 +556,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     }
     float kl = 0.f, kl_slope = 0.f;
     if (p.ref_log_probs) {
-      const float d = log_ratio(in.ref, lp);
+      const float d = -log_ratio(lp, 0.f, in.ref);
       if (p.kl == LS_KL_K1) {
         kl = -d;
         kl_slope = 1.f;
@@ -552,7 +582,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     if (write && a.out_metrics) a.out_metrics[i] = make_float4(lp, entropy ? H : 0.f, kl, ratio);
   } else {
     st.w = w;
-    st.term = w * (a.policy.ref_log_probs ? log_ratio(lp, in.ref) : lp);
+    st.term = w * (a.policy.ref_log_probs ? log_ratio(lp, rest, in.ref) : lp);
   }
   if (write && a.out_stats) {
     float4* out = reinterpret_cast<float4*>(a.out_stats + i);
