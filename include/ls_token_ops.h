@@ -156,7 +156,8 @@ typedef struct {
  * ls_preference_loss -- with s(answer) = sum of weights[i] * (lp_i - ref_i)
  * over its rows (divided by the sum of weights[i]; 0 where that is 0),
  * u = s(chosen) - s(rejected) and h = beta u - margin: the loss of each pair.
- * A difference of two log-probs of -inf is 0.  A pair with bad offsets gives
+ * A difference of two log-probs of -inf is 0.  A pair whose offsets descend,
+ * or leave [0, n] or what the list's first and last offset span, gives
  * NaN, gradient 0 and LS_ROW_ERR_BAD_OFFSETS.
  *
  *   out_loss        device float[pairs]

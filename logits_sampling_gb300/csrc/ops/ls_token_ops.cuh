@@ -52,8 +52,9 @@ struct TokenArgs {
 // ---------------------------------------------------------------------------
 // One pass: maximum, sum and entropy term
 // ---------------------------------------------------------------------------
-// (M, S, E) of a set of entries: S = sum 2^y, E = sum y 2^y, y = (x - M) c <= 0,
-// c = log2(e) / T.  H = ln S - ln 2 * E / S.
+// (M, S, E) of a set of entries: S = sum 2^y, E = sum y 2^y, y = (x - M) c, c =
+// log2(e) / T, against a reference M (their maximum, or what is used in its place).
+// H = ln S - ln 2 * E / S.
 struct Moments {
   float m, s, e;
 };
@@ -109,7 +110,6 @@ __device__ __forceinline__ bool lift_ok(float c) { return c >= 5.4210109e-20f &&
 // y of one entry by subtraction, NaN and -inf at kFloorExp.
 __device__ __forceinline__ float rel_log(float v, float m, float c) { return v == m ? 0.f : fmaxf((v - m) * c, kFloorExp); }
 
-// A warp's reference (as OnlineSum's) and each thread's S and E.
 // ExpAgainst with its `scale`, 2^-delta, from a series: delta, what m c lost to its
 // rounding, is below 2^-8, and the instruction is off by 2^-23 at 0 where all rows
 // with the same maximum would share it.
@@ -138,6 +138,7 @@ __device__ __forceinline__ f32x2 sum_pairs(f32x2 (&t)[kN]) {
   return t[0];
 }
 
+// A warp's reference and each thread's S and E.
 template <bool kEntropy>
 struct RowSum;
 

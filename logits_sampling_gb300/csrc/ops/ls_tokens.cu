@@ -84,9 +84,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   // after a row kernel, which has waited for whatever wrote them, the offsets are there
   if (a.n == 0) wait_for_previous();
   const int32_t lo = at[0], mid = at[1], hi = at[2];
+  // the row kernel has looked at rows from the list's first to its last offset only
+  const int32_t least = max(a.p.answer_offsets[0], 0), most = min(a.p.answer_offsets[2 * (int64_t)a.p.pairs], a.n);
   wait_for_previous();
   let_next_start();
-  if (lo < 0 || mid < lo || hi < mid || hi > a.n) {
+  if (lo < least || mid < lo || hi < mid || hi > most) {
     if (tid == 0) {
       a.out_loss[p] = quiet_nan();
       if (a.out_log_ratios) a.out_log_ratios[2 * (int64_t)p] = a.out_log_ratios[2 * (int64_t)p + 1] = quiet_nan();

@@ -458,14 +458,17 @@ def test_preference_bad_offsets():
     dev, _ = _logits(_normal(rng, 12, 300), "f32")
     idd = _dev(rng.integers(0, 300, 12), np.int32)
     good = ls.preference_loss(dev, idd, _dev([0, 2, 4, 6, 8], np.int32))
-    for bad in ([0, 2, 4, 3, 8], [0, 2, 4, 6, 13], [0, 2, 4, 20, 8], [0, 2, 4, -5, 8], [0, 2, 4, 2 ** 31 - 1, -2 ** 31]):
+    for bad in ([0, 2, 4, 3, 8], [0, 2, 4, 6, 13], [0, 2, 4, 20, 8], [0, 2, 4, -5, 8], [0, 2, 4, 2 ** 31 - 1, -2 ** 31],
+                [0, 2, 4, 3, 3], [0, 2, 4, 4, 1]):
         err = torch.zeros(1, dtype=torch.int32, device="cuda")
         loss, ratios, stats = ls.preference_loss(dev, idd, _dev(bad, np.int32), error_word=err)
         assert int(err) == ls.LS_ROW_ERR_BAD_OFFSETS and torch.isnan(loss[1]) and torch.isnan(ratios[2:]).all()
         grad = ls.preference_loss_backward(dev, idd, stats)
         assert not grad[4:].any()
-        if bad[-1] > 4:  # rows 0 to 3 lie within the answers' range
+        if bad[-1] >= 4:  # rows 0 to 3 lie within what the list spans
             assert torch.equal(loss[0], good[0][0]) and grad[:4].any(-1).all()
+        else:
+            assert torch.isnan(loss[0]) and not grad.any()
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     for bad in ([-1, 2, 4], [5, 3, 8], [2, 9, 5]):
         loss, _, stats = ls.preference_loss(dev, idd, _dev(bad, np.int32), error_word=err)
