@@ -66,10 +66,8 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
   }
   __syncthreads();
   gradient_run<true>(run, st, first, g, grad, kept);
-  if (run.place(in.id) >= 0) {  // the same in every thread
-    __syncthreads();
-    if (tid == 0) grad[in.id] = E::put(g.at_id);
-  }
+  const int place = run.place(in.id);  // the thread that has written it writes it again
+  if (place >= 0 && tid == st.owner(run, place)) grad[in.id] = E::put(g.at_id);
 }
 
 // How a batch is laid out on the SMs, which hold 1024 threads of these kernels

@@ -276,6 +276,11 @@ struct Stages {
     const int v = s * R::kStep + k * T + (int)threadIdx.x;
     return v >= run.n ? -1 : v + run.f < run.n ? v + run.f : 0;
   }
+  // The thread that visits a place of the run (Run::place).
+  __device__ __forceinline__ static int owner(const R& run, int place) {
+    const int v = place / R::kN - run.f;
+    return (v >= 0 ? v : run.n - 1) % T;
+  }
   // Any stage; units past the run as -inf.
   __device__ __forceinline__ static void load_any(const R& run, int s, Stage& w) {
 #pragma unroll

@@ -238,10 +238,8 @@ __global__ void __launch_bounds__(kBackThreads, 1024 / kBackThreads)
   RowGradient g;
   g.init(st, g_lp, g_H, a.c);
   gradient_run<false>(run, stages, first, g, grad, Kept<T>{nullptr, 0});
-  if (run.place(id) >= 0) {  // in this CTA's run: the same in every thread
-    __syncthreads();
-    if (tid == 0) grad[id] = Elem<TIn>::put(g.at_id);
-  }
+  const int place = run.place(id);  // the thread that has written it writes it again
+  if (place >= 0 && tid == stages.owner(run, place)) grad[id] = Elem<TIn>::put(g.at_id);
 }
 
 // ---------------------------------------------------------------------------
