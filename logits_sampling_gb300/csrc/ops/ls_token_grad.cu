@@ -10,9 +10,9 @@ namespace lsg {
 namespace ops {
 
 // Bound by DRAM and by what does not overlap on an SM with two rows: 2048 x 128256
-// bf16 184 us (5.7 TB/s on one read and one write; 13 % of the second reads miss L2,
-// which makes 6.0), 1024 x 262144 fp32 with entropies 415 (5.2 TB/s; the exchange of
-// four CTAs and the row's scalars are a quarter of the stalls). The two calls take 230
+// bf16 180 us (5.8 TB/s on one read and one write; 13 % of the second reads miss L2,
+// which makes 6.2), 1024 x 262144 fp32 with entropies 393 (5.5 TB/s; the exchange of
+// a row's CTAs and its scalars are a quarter of the stalls). The two calls take 230
 // and 459.
 template <typename TIn, bool kEntropy, int T>
 __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs a, int upc, int keep) {
@@ -73,29 +73,33 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
 // How a batch is laid out on the SMs, which hold 1024 threads of these kernels
 // each.  Measured, us (threads of a CTA x CTAs of a row):
 //   few rows: a row over as many CTAs as find room at once.  64 rows of 256 KB
-//     256x8 11.6, 256x4 12.0, 512x2 12.2, 512x1 15.4; of 64 KB (runs below 16 KB do
-//     not pay) 256x4 6.7, 256x8 7.5, 512x1 7.0
+//     256x8 11.5, 256x4 11.7, 512x2 11.8, 512x1 14.9; 8 of them 6.1, 7.2, 9.1, 11.8.
+//     Rows of 64 KB: 64 of them 256x4 5.7, 512x1 6.0, 256x2 6.3, 256x8 6.8; 128 of
+//     them 512x1 7.4, 256x2 8.2, 256x4 8.3; of 32 KB 64 of them 512x1 4.8, 256x2 5.4
 //   more: one CTA per row, 512 threads so that fewer rows share L2 between their two
-//     reads, 256 where rows are short and many.  304 x 256 KB 512x1 30.7, 256x1
-//     34.4; 2048 x 256 KB 183, 211; 152 x 64 KB 8.1, 8.8; 1024 x 64 KB 36, 28.5; 2048
-//     x 128 KB 99, 97
-//   rows above 320 KB: over the fewest CTAs that keep a share below that.  1024 x 1
-//     MB 512x4 415, 512x2 448, 512x1 459; 1024 x 512 KB 512x2 193, 512x1 213
-// Kept in shared memory, of 256 KB rows: nothing 190.6, 32 KB 186.8, 64 KB 184.3, 96
-// KB 182.9; what is left of L1 has to hold the loads in flight.
+//     reads, 256 where rows are short and many.  304 rows of 256 KB 512x1 30.5, 256x1
+//     34.4; 2048 180, 210; of 64 KB 304 rows 11.6, 11.4; 1024 35, 28; of 128 KB 2048
+//     99, 96
+//   rows above 320 KB over the fewest CTAs of 512 that keep a share below that, above
+//     640 KB over twice as many of 256 (four rows' CTAs to an SM instead of two while
+//     one waits for its peers).  1024 x 512 KB 512x2 197, 512x1 211, 512x4 224; 1024 x
+//     1 MB 256x8 393, 512x4 402, 512x2 436, 512x1 457
+// Kept in shared memory, of 2048 rows of 256 KB: nothing 190.6, 32 KB 185.7, 64 KB
+// 182.7, 96 KB 180.2; what is left of L1 has to hold the loads in flight.
 struct GradPlan {
   int threads, ctas, keep;
 };
 static GradPlan grad_plan(int32_t n, int64_t bytes) {
   if (bytes <= 16 * 1024) return {128, 1, 0};
-  if (n <= 128) {
-    int c = 1;
-    while (c < kMaxCluster && n * c * 2 <= 512 && bytes / (2 * c) >= 16 * 1024) c *= 2;
+  int c = 1;
+  if ((n <= 64 && bytes >= 48 * 1024) || (n <= 128 && bytes >= 128 * 1024)) {
+    const int most = bytes >= 128 * 1024 ? 512 : 256;
+    while (c < kMaxCluster && n * c * 2 <= most && bytes / (2 * c) >= 15 * 1024) c *= 2;
     return {256, c, 2};
   }
-  int c = 1;
-  while (c < kMaxCluster && bytes / c > 320 * 1024) c *= 2;
   if (n > 304 && bytes <= 160 * 1024) return {256, 1, 2};
+  while (c < kMaxCluster && bytes / c > 320 * 1024) c *= 2;
+  if (c == 4) return {256, 8, 2};
   return {512, c, c == 1 ? 3 : 2};
 }
 
