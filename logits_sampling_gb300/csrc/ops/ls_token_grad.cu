@@ -97,7 +97,7 @@ static GradPlan grad_plan(int32_t n, int64_t bytes) {
     while (c < kMaxCluster && n * c * 2 <= most && bytes / (2 * c) >= 15 * 1024) c *= 2;
     return {256, c, 2};
   }
-  if (n > 304 && bytes <= 160 * 1024) return {256, 1, 2};
+  if (n > 2 * device_attr<cudaDevAttrMultiProcessorCount>() && bytes <= 160 * 1024) return {256, 1, 2};
   while (c < kMaxCluster && bytes / c > 320 * 1024) c *= 2;
   if (c == 4) return {256, 8, 2};
   return {512, c, c == 1 ? 3 : 2};
