@@ -92,6 +92,26 @@ def test_in_place_for_every_layout(dtype, n, V):
             assert (around == 77).all()  # the padding between the rows is as it was
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,V", [(50, 2003), (400, 30001), (7, 70003)])
+def test_in_place_where_rows_touch(dtype, n, V):
+    """Contiguous rows of odd length share their first and last 32 bytes with their neighbours."""
+    import logits_sampling_gb300 as ls
+    import torch
+    rng = np.random.default_rng(4)
+    x, _ = _logits(_normal(rng, n, V), dtype)
+    ids, adv = _dev(rng.integers(0, V, n), np.int32), _dev(rng.standard_normal(n))
+    ids[::3] = torch.tensor([0, V - 1], device="cuda").repeat(n)[:len(ids[::3])].to(torch.int32)  # at the edges
+    want = ls.policy_loss_grad(x, ids, adv)[1]
+    _, _, stats = ls.policy_loss(x, ids, adv)
+    back = ls.policy_loss_backward(x, ids, stats)
+    for f, g in ((lambda y: ls.policy_loss_grad(y, ids, adv, out_grad=y)[1], want),
+                 (lambda y: ls.policy_loss_backward(y, ids, stats, out=y), back)):
+        for _ in range(3):
+            y = x.clone()
+            assert torch.equal(f(y), g)
+
+
 def test_rows_far_apart():
     """Rows that begin past 2^31 entries of their buffer, read and written."""
     import logits_sampling_gb300 as ls
