@@ -324,17 +324,30 @@ struct Kept {
 };
 
 // Adds a run up; `a` holds its first whole stage.  A warp takes the maximum of
-// that stage (0 where it has none) as its reference and adds up all that follow
-// against it, without looking for larger ones: for two entries two conversions,
-// one multiplication, two exponentials and one addition, and no branch.  A sum is
-// as exact against a reference away from the maximum as long as it stays within
-// [kLeastSum, kMostSum]; where it does not (or shows a NaN) the row is taken
-// again, `careful`: with a reference that rises with the maximum and NaNs read as
-// -inf, as the row's ends are always taken.  An entropy's E / S is a mean of
-// exponents and loses digits to a distant reference (1.4e-6 of H in 1024 x 262144
+// that stage (of the first that holds an entry above -inf) as its reference and adds
+// up all that follow against it, without looking for larger ones: for two entries two
+// conversions, one multiplication, two exponentials and one addition, and no branch
+// but one per stage for a warp that has found no entry yet.  A reference is always an
+// entry of the row, so a sum against the largest of them is at least 1.  A sum does
+// against a reference below the maximum as long as it stays within kMostSum (an exponent of
+// up to 40 is rounded to 2^-19, 7e-7 of its term); where it does not (or shows a NaN) the
+// row is taken again, `careful`: with a reference that rises with the maximum and
+// NaNs read as -inf, as the row's ends are always taken.  An entropy's E / S is a mean
+// of exponents and loses digits to a distant reference (1.4e-6 of H in 1024 x 262144
 // fp32 with a head at 20, 1e-7 with the maximum; 149.6 and 150.2 us): there the
 // reference follows the maximum.
-constexpr float kMostSum = 1.0995116e12f, kLeastSum = 9.094947e-13f;  // 2^40, 2^-40
+constexpr float kMostSum = 1.0995116e12f, kLeastSum = 0.5f;  // 2^40; below any sum that holds its reference's own 1
+
+// Whether a stage holds nothing but -inf (NaNs are something).
+template <typename TIn>
+__device__ __forceinline__ bool none(const uint32_t (&v)[kStage][8]) {
+  uint32_t other = 0u;
+#pragma unroll
+  for (int k = 0; k < kStage; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) other |= v[k][q] ^ (Elem<TIn>::kBytes == 2 ? 0xFF80FF80u : 0xFF800000u);
+  return other == 0u;
+}
 
 template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
 __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
@@ -361,9 +374,8 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
 #pragma unroll
     for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(a[k]));
     acc.raise(um);
-    if (!(acc.x.m > kNegInf)) acc.raise(0.f);
   }
-  bool fast = acc.x.fast;
+  bool found = acc.x.m > kNegInf, fast = !found || acc.x.fast, odd = false;
   auto add = [&](Stage& v) {
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add_fast<TIn>(v[k]);
@@ -382,14 +394,18 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
       }
     }
     if (kKeep && left <= kept.n) kept.put(left - 1, v);
-    if (kEntropy) {
+    if (kEntropy || !found) {
       float um = kNegInf;
 #pragma unroll
       for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(v[k]));
       acc.raise(um);
-      fast = fast && acc.x.fast;
+      found = acc.x.m > kNegInf;
+      fast = fast && (!found || acc.x.fast);
     }
-    add(v);
+    if (found)
+      add(v);
+    else
+      odd = odd || !none<TIn>(v);
     return --left > 0;
   };
 #pragma unroll 1
@@ -397,7 +413,7 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
     if (!step(a, b)) break;
     if (!step(b, a)) break;
   }
-  if (!fast) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
+  if (!fast || odd) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
 }
 __device__ __forceinline__ bool sum_ok(float s) { return s < kMostSum && s > kLeastSum; }  // NaN compares false
 
@@ -509,13 +525,14 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   // (x - M) / T it would be a bias of every row).  With what each step loses kept
   // (two-sums, products' remainders): an answer's ratio is a sum of differences of
   // log-probs, in which the rounding of lp itself, up to 1e-6, would be the largest
-  // error.  A sum's terms but the maximum's own, 1, are low by kExpLow on average.
+  // error.  A sum's terms but the maximum's own, 1, are low by kExpLow on average; S
+  // holds that 1, but for what it is short of it by rounding.
   const int k = (int)(__float_as_uint(r.s) >> 23 & 255u) - 127;
   const float log2s = log2f(__uint_as_float((__float_as_uint(r.s) & 0x7FFFFFu) | 0x3F800000u));
   const float c = a.c, p = x * c, q = r.m * c;
   float rest = 0.f;  // of lp
   if (fabsf(p) < 1e30f && fabsf(q) < 1e30f) {
-    float lo = fmaf(x, c, -p) - fmaf(r.m, c, -q) - kExpLow * kLog2e * (1.f - 1.f / r.s);
+    float lo = fmaf(x, c, -p) - fmaf(r.m, c, -q) - kExpLow * kLog2e * fmaxf(1.f - 1.f / r.s, 0.f);
     const float y = two_sum(p, -q, lo), z = two_sum(y, -(float)k, lo), t = two_sum(z, -log2s, lo);
     const float v = kLn2 * t;
     lo = fmaf(kLn2, t, -v) + fmaf(-1.9046543e-9f, t, kLn2 * lo);  // ln 2 less kLn2
