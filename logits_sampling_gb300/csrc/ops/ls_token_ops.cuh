@@ -328,10 +328,11 @@ struct Kept {
 // up all that follow against it, without looking for larger ones: for two entries two
 // conversions, one multiplication, two exponentials and one addition, and no branch
 // but one per stage for a warp that has found no entry yet.  A reference is always an
-// entry of the row, so a sum against the largest of them is at least 1.  A sum does
-// against a reference below the maximum as long as it stays within kMostSum (an exponent of
-// up to 40 is rounded to 2^-19, 7e-7 of its term); where it does not (or shows a NaN) the
-// row is taken again, `careful`: with a reference that rises with the maximum and
+// entry of the row, so a sum against the largest of them is at least 1.  A thread's sum
+// does against a reference below the maximum as long as it stays within kMostSum (an
+// exponent of up to 40 is rounded to 2^-19, 7e-7 of its term; and a warp's sum of 2^126
+// times its reference would count 0 beside another warp's reference above that); where
+// it does not (or shows a NaN) the row is taken again, `careful`: with a reference that rises with the maximum and
 // NaNs read as -inf, as the row's ends are always taken.  An entropy's E / S is a mean
 // of exponents and loses digits to a distant reference (1.4e-6 of H in 1024 x 262144
 // fp32 with a head at 20, 1e-7 with the maximum; 149.6 and 150.2 us): there the
@@ -413,7 +414,13 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
     if (!step(a, b)) break;
     if (!step(b, a)) break;
   }
-  if (!fast || odd) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
+  bool most = true;
+  if (!kEntropy) {  // each thread's: another warp's reference may hide what is past it
+    float lo, hi;
+    unpack2(acc.s0, lo, hi);
+    most = lo + hi < kMostSum;
+  }
+  if (!fast || odd || !most) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
 }
 __device__ __forceinline__ bool sum_ok(float s) { return s < kMostSum && s > kLeastSum; }  // NaN compares false
 
