@@ -332,11 +332,11 @@ struct Kept {
 // does against a reference below the maximum as long as it stays within kMostSum (an
 // exponent of up to 40 is rounded to 2^-19, 7e-7 of its term; and a warp's sum of 2^126
 // times its reference would count 0 beside another warp's reference above that); where
-// it does not (or shows a NaN) the row is taken again, `careful`: with a reference that rises with the maximum and
-// NaNs read as -inf, as the row's ends are always taken.  An entropy's E / S is a mean
-// of exponents and loses digits to a distant reference (1.4e-6 of H in 1024 x 262144
-// fp32 with a head at 20, 1e-7 with the maximum; 149.6 and 150.2 us): there the
-// reference follows the maximum.
+// it does not, or where there is a NaN, the row is taken again, `careful`: with a
+// reference that rises with the maximum and NaNs read as -inf, as the row's ends are
+// always taken.  An entropy's E / S is a mean of exponents and loses digits to a distant
+// reference (1.4e-6 of H in 1024 x 262144 fp32 with a head at 20, 1e-7 with the maximum;
+// 149.6 and 150.2 us): there the reference follows the maximum.
 constexpr float kMostSum = 1.0995116e12f, kLeastSum = 0.5f;  // 2^40; below any sum that holds its reference's own 1
 
 // Whether a stage holds nothing but -inf (NaNs are something).
@@ -350,18 +350,33 @@ __device__ __forceinline__ bool none(const uint32_t (&v)[kStage][8]) {
   return other == 0u;
 }
 
+// Whether a unit holds a NaN.
+template <typename TIn>
+__device__ __forceinline__ bool has_nan(const uint32_t (&w)[8]) {
+  uint32_t clean[8], other = 0u;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) clean[q] = w[q];
+  Unit<TIn>::clean(clean);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) other |= clean[q] ^ w[q];
+  return other != 0u;
+}
+
 template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
 __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
                                         RowSum<kEntropy>& acc, float c, bool careful, const Kept<T>& kept) {
   typedef typename Run<TIn, T>::Stage Stage;
   acc.init(c);
   Stage b;
+  // a NaN that the sum does not show: the backward pass has other runs, and has to know of it
+  bool odd = false;
 #pragma unroll 1
   for (int s = careful ? 0 : st.whole; s < st.all; ++s) {
     st.load_any(run, s, b);
     float um = kNegInf;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) {
+      if (!kEntropy && !careful) odd = odd || has_nan<TIn>(b[k]);
       Unit<TIn>::clean(b[k]);
       um = fmaxf(um, Unit<TIn>::max(b[k]));
     }
@@ -369,14 +384,18 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add<TIn>(b[k]);
   }
-  if (careful || st.whole == 0) return;
+  if (careful) return;
+  if (st.whole == 0) {
+    if (odd) acc.s0 = pack2(quiet_nan(), quiet_nan());
+    return;
+  }
   {
     float um = kNegInf;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(a[k]));
     acc.raise(um);
   }
-  bool found = acc.x.m > kNegInf, fast = !found || acc.x.fast, odd = false;
+  bool found = acc.x.m > kNegInf, fast = !found || acc.x.fast;
   auto add = [&](Stage& v) {
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add_fast<TIn>(v[k]);

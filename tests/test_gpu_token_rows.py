@@ -38,3 +38,25 @@ def test_sums_far_above_a_reference(dtype, n):
     _score(dev, xs, ids, 1.0, dtype, rng, f"{n} rows", some=range(20))
     rows = _rows(xs, ids, 1.0, dtype)
     _policy(dev, ids, rows, _policy_inputs(rng, rows), dtype, 1.0, f"{n} rows")
+
+
+@pytest.mark.parametrize("n,V", [(6, 9001), (320, 9001), (6, 14000), (700, 14000), (320, 33001), (700, 33001), (6, 70001),
+                                 (140, 70001), (1300, 40009)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_single_nans(dtype, n, V):
+    """One NaN in a row, wherever it lies: -inf, with gradient 0."""
+    rng = np.random.default_rng(V)
+    at = [0, 1, 17, V // 2, V - 20, V - 1, V - 700, 700, 5000, V - 5000]
+    at += rng.integers(0, V, 14).tolist()
+    x = np.zeros((n, V), np.float32)
+    x[:24] = _normal(rng, min(n, 24), V)
+    ids = np.full(n, -1)
+    some = range(min(n, 24))
+    for i in some:
+        x[i, at[i]] = np.nan
+        ids[i] = (at[i] + 3) % V
+    for offset in (0, 5):
+        dev, xs = _logits(x, dtype, offset, 4)
+        _score(dev, xs, ids, 1.0, dtype, rng, f"{n} x {V}", some=some)
+        rows = _rows(xs, ids, 1.0, dtype)
+        _policy(dev, ids, rows, _policy_inputs(rng, rows), dtype, 1.0, f"{n} x {V}")
