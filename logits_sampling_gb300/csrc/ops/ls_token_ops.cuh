@@ -168,7 +168,7 @@ struct RowSum<false> {
     s0 = add2(s0, sum_pairs(t));
   }
   template <typename TIn>
-  __device__ __forceinline__ void add(uint32_t (&w)[8]) {  // no NaN among them
+  __device__ __forceinline__ void add(uint32_t (&w)[8]) {  // a NaN among them shows, but where there is no reference yet
     if (x.fast) {
       add_fast<TIn>(w);
     } else if (x.m > kNegInf) {
@@ -350,25 +350,14 @@ __device__ __forceinline__ bool none(const uint32_t (&v)[kStage][8]) {
   return other == 0u;
 }
 
-// Whether a unit holds a NaN.
-template <typename TIn>
-__device__ __forceinline__ bool has_nan(const uint32_t (&w)[8]) {
-  uint32_t clean[8], other = 0u;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) clean[q] = w[q];
-  Unit<TIn>::clean(clean);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) other |= clean[q] ^ w[q];
-  return other != 0u;
-}
-
 template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
 __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
                                         RowSum<kEntropy>& acc, float c, bool careful, const Kept<T>& kept) {
   typedef typename Run<TIn, T>::Stage Stage;
   acc.init(c);
   Stage b;
-  // a NaN that the sum does not show: the backward pass has other runs, and has to know of it
+  // a NaN that the sum does not show, there being no reference: the backward pass, whose
+  // runs are others, has to know of it
   bool odd = false;
 #pragma unroll 1
   for (int s = careful ? 0 : st.whole; s < st.all; ++s) {
@@ -376,11 +365,11 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
     float um = kNegInf;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) {
-      if (!kEntropy && !careful) odd = odd || has_nan<TIn>(b[k]);
-      Unit<TIn>::clean(b[k]);
+      if (kEntropy || careful) Unit<TIn>::clean(b[k]);
       um = fmaxf(um, Unit<TIn>::max(b[k]));
     }
     acc.raise(um);
+    if (!kEntropy && !careful && !(acc.x.m > kNegInf)) odd = odd || !none<TIn>(b);
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add<TIn>(b[k]);
   }
