@@ -168,7 +168,7 @@ struct RowSum<false> {
     s0 = add2(s0, sum_pairs(t));
   }
   template <typename TIn>
-  __device__ __forceinline__ void add(uint32_t (&w)[8]) {  // a NaN among them shows, but where there is no reference yet
+  __device__ __forceinline__ void add(uint32_t (&w)[8]) {  // a NaN shows, but where there is no reference yet
     if (x.fast) {
       add_fast<TIn>(w);
     } else if (x.m > kNegInf) {
@@ -413,7 +413,7 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
     }
     if (found)
       add(v);
-    else
+    else if (!kEntropy)
       odd = odd || !none<TIn>(v);
     return --left > 0;
   };
@@ -645,11 +645,11 @@ struct RowGradient {
   Reference x;
   float k0, k1;
   float at_id;
-  bool lifted;  // with an entropy term, or where the row may hold NaNs
+  bool lifted;  // with an entropy term, or where the row may hold NaNs: exponents end at kFloorExp
   // g_lp, g_H: the row's slopes times the gradient from above; c = log2(e) / T.
   __device__ __forceinline__ void init(const TokenStats& st, float g_lp, float g_H, float c) {
     lifted = g_H != 0.f || st.dirty != 0.f;
-    x.at(st.M, c, lifted);
+    x.at(st.M, c, false);
     const float over = st.over * x.scale;
     k1 = 0.f;
     k0 = -g_lp * over;
@@ -658,20 +658,23 @@ struct RowGradient {
       k1 = -g_H * kLn2 * over;
       k0 = -(g_lp + g_H * st.mean) * over - k1 * x.delta;  // pair_fast's y is short of the true one by delta
       at_id -= g_H * st.id_H;
+      x.fast = x.fast && fabsf(k1) < 1e30f;  // k1 times any exponent is finite
     }
   }
   // The unit's entries become their gradients, x being fast.
   template <typename TIn, bool kLift>
   __device__ __forceinline__ void apply_fast(uint32_t (&w)[8]) const {
     const f32x2 a0 = pack2(k0, k0), a1 = pack2(k1, k1), c2 = pack2(x.c, x.c), r2 = pack2(-x.r, -x.r);
-    if (kLift) lift<TIn>(w);
     uint32_t o[8];
 #pragma unroll
     for (int q = 0; q < Unit<TIn>::kN / 2; ++q) {
-      const f32x2 y = fma2(Unit<TIn>::pair(w, q), c2, r2);
       float a, b;
-      unpack2(y, a, b);
-      unpack2(mul2(pack2(ex2(a), ex2(b)), kLift ? fma2(y, a1, a0) : a0), a, b);
+      unpack2(fma2(Unit<TIn>::pair(w, q), c2, r2), a, b);
+      if (kLift) {
+        a = fmaxf(a, kFloorExp);
+        b = fmaxf(b, kFloorExp);
+      }
+      unpack2(mul2(pack2(ex2(a), ex2(b)), kLift ? fma2(pack2(a, b), a1, a0) : a0), a, b);
       Unit<TIn>::set_pair(o, q, a, b);
     }
 #pragma unroll
@@ -693,7 +696,9 @@ struct RowGradient {
         unpack2(Unit<TIn>::pair(w, q), a, b);
         a = rel_log(a, x.m, x.c);
         b = rel_log(b, x.m, x.c);
-        Unit<TIn>::set_pair(o, q, ex2(a) * fmaf(a, k1, k0), ex2(b) * fmaf(b, k1, k0));
+        const f32x2 e = pack2(ex2(a), ex2(b));  // first: k1 may be too large for an entry without mass
+        unpack2(fma2(mul2(e, pack2(k1, k1)), pack2(a, b), mul2(e, pack2(k0, k0))), a, b);
+        Unit<TIn>::set_pair(o, q, a, b);
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) w[q] = o[q];

@@ -128,3 +128,32 @@ def test_mask_sample_and_score_below_zero(dtype):
         _near(float(lp[i]), row.lp, row.tol_lp, f"lp {i}")
         for m in (metrics, fused):  # the sampler's own bound on its log-prob is 1e-5
             _near(float(m[i, 3]), 1.0, 1.1e-5 + row.tol_lp, f"ratio {i}")
+
+
+@pytest.mark.parametrize("T,g_H,level", [(1.0, 1.0, -20.0), (1.0, 1e6, -5.0), (1e-5, 0.02, 0.0), (1e-5, 1.0, 0.0),
+                                         (0.01, 65536.0, 0.0), (1e-7, 1.0, 0.0), (1e-37, 1.0, 0.0)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_entropy_gradients_of_masked_entries(dtype, T, g_H, level):
+    """Steep entropy gradients: an entry without mass has gradient 0, whatever the slope."""
+    import logits_sampling_gb300 as ls
+    rng = np.random.default_rng(6)
+    T, V = float(np.float32(T)), 20001
+    for n in (24, 320):
+        for fill in (-np.inf, np.nan, -3e38, -50.0 if T < 1e-4 else -np.inf):
+            x = np.full((n, V), fill, np.float32)
+            ids = np.full(n, -1)
+            for i in range(6):
+                at = rng.choice(V, 7, replace=False)
+                x[i, at] = level - rng.uniform(0, 3, 7) * T
+                x[i, at[:2]] = level
+                ids[i] = at[i]
+            dev, xs = _logits(x, dtype, 3, 5)
+            rows = [_row(xs[i], ids[i], T, 4 if dtype == "f32" else 2) for i in range(6)]
+            up = np.full(n, g_H)
+            idd, gh = _dev(ids, np.int32), _dev(up)
+            _, _, stats = ls.token_log_probs(dev, idd, temperature=T, entropy=True)
+            grad = _f64(ls.token_log_probs_backward(dev, idd, stats, None, gh, temperature=T)[:6])
+            _, fused, _ = ls.policy_loss_grad(dev, idd, _dev(np.zeros(n)), weights=gh, entropy_coef=1.0, temperature=T)
+            fused = _f64(fused[:6])
+            for got, sign in ((grad, 1.0), (fused, -1.0)):
+                _check_gradient(got, rows, np.zeros(n), sign * up, dtype, f"{n} rows of {fill}")
