@@ -112,9 +112,17 @@ __device__ __forceinline__ float rel_log(float v, float m, float c) { return v =
 
 // ExpAgainst with its `scale`, 2^-delta, from a series: delta, what m c lost to its
 // rounding, is below 2^-8, and the instruction is off by 2^-23 at 0 where all rows
-// with the same maximum would share it.
+// with the same maximum would share it.  While there is no reference (m = -inf) r is 0:
+// what has been seen by then is -inf, which adds 0, or NaN, which shows.
 struct Reference : ExpAgainst {
   float delta;
+  __device__ __forceinline__ void none(float c_, bool lift) {
+    m = kNegInf;
+    c = c_;
+    r = delta = 0.f;
+    scale = 1.f;
+    fast = !lift || lift_ok(c);
+  }
   __device__ __forceinline__ void at(float m_, float c_, bool lift) {
     m = m_;
     c = c_;
@@ -147,7 +155,7 @@ struct RowSum<false> {
   Reference x;
   f32x2 s0;
   __device__ __forceinline__ void init(float c) {
-    x.at(kNegInf, c, false);
+    x.none(c, false);
     s0 = 0ull;
   }
   // Before units of maximum um in this lane are added (all lanes call).
@@ -168,7 +176,7 @@ struct RowSum<false> {
     s0 = add2(s0, sum_pairs(t));
   }
   template <typename TIn>
-  __device__ __forceinline__ void add(uint32_t (&w)[8]) {  // a NaN shows, but where there is no reference yet
+  __device__ __forceinline__ void add(uint32_t (&w)[8]) {
     if (x.fast) {
       add_fast<TIn>(w);
     } else if (x.m > kNegInf) {
@@ -189,7 +197,7 @@ struct RowSum<true> {
   Reference x;
   f32x2 s0, e0;
   __device__ __forceinline__ void init(float c) {
-    x.at(kNegInf, c, true);
+    x.none(c, true);
     s0 = e0 = 0ull;
   }
   __device__ __forceinline__ void raise(float um) {
@@ -339,52 +347,33 @@ struct Kept {
 // 149.6 and 150.2 us): there the reference follows the maximum.
 constexpr float kMostSum = 1.0995116e12f, kLeastSum = 0.5f;  // 2^40; below any sum that holds its reference's own 1
 
-// Whether a stage holds nothing but -inf (NaNs are something).
-template <typename TIn>
-__device__ __forceinline__ bool none(const uint32_t (&v)[kStage][8]) {
-  uint32_t other = 0u;
-#pragma unroll
-  for (int k = 0; k < kStage; ++k)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) other |= v[k][q] ^ (Elem<TIn>::kBytes == 2 ? 0xFF80FF80u : 0xFF800000u);
-  return other == 0u;
-}
-
 template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
 __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
                                         RowSum<kEntropy>& acc, float c, bool careful, const Kept<T>& kept) {
   typedef typename Run<TIn, T>::Stage Stage;
   acc.init(c);
   Stage b;
-  // a NaN that the sum does not show, there being no reference: the backward pass, whose
-  // runs are others, has to know of it
-  bool odd = false;
 #pragma unroll 1
   for (int s = careful ? 0 : st.whole; s < st.all; ++s) {
     st.load_any(run, s, b);
     float um = kNegInf;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) {
-      if (kEntropy || careful) Unit<TIn>::clean(b[k]);
+      if (kEntropy || careful) Unit<TIn>::clean(b[k]);  // else a NaN shows: the backward pass has to know of it
       um = fmaxf(um, Unit<TIn>::max(b[k]));
     }
     acc.raise(um);
-    if (!kEntropy && !careful && !(acc.x.m > kNegInf)) odd = odd || !none<TIn>(b);
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add<TIn>(b[k]);
   }
-  if (careful) return;
-  if (st.whole == 0) {
-    if (odd) acc.s0 = pack2(quiet_nan(), quiet_nan());
-    return;
-  }
+  if (careful || st.whole == 0) return;
   {
     float um = kNegInf;
 #pragma unroll
     for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(a[k]));
     acc.raise(um);
   }
-  bool found = acc.x.m > kNegInf, fast = !found || acc.x.fast;
+  bool fast = acc.x.fast;
   auto add = [&](Stage& v) {
 #pragma unroll
     for (int k = 0; k < kStage; ++k) acc.template add_fast<TIn>(v[k]);
@@ -403,18 +392,14 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
       }
     }
     if (kKeep && left <= kept.n) kept.put(left - 1, v);
-    if (kEntropy || !found) {
+    if (kEntropy || !(acc.x.m > kNegInf)) {
       float um = kNegInf;
 #pragma unroll
       for (int k = 0; k < kStage; ++k) um = fmaxf(um, Unit<TIn>::max(v[k]));
       acc.raise(um);
-      found = acc.x.m > kNegInf;
-      fast = fast && (!found || acc.x.fast);
+      fast = fast && acc.x.fast;
     }
-    if (found)
-      add(v);
-    else if (!kEntropy)
-      odd = odd || !none<TIn>(v);
+    add(v);
     return --left > 0;
   };
 #pragma unroll 1
@@ -428,7 +413,7 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
     unpack2(acc.s0, lo, hi);
     most = lo + hi < kMostSum;
   }
-  if (!fast || odd || !most) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
+  if (!fast || !most) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
 }
 __device__ __forceinline__ bool sum_ok(float s) { return s < kMostSum && s > kLeastSum; }  // NaN compares false
 
