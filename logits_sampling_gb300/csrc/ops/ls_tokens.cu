@@ -228,7 +228,9 @@ __global__ void __launch_bounds__(kBackThreads, 1024 / kBackThreads)
   // a slope of 0 counts nothing, whatever the gradient from above
   const float g_lp = s1.x == 0.f ? 0.f : s1.x * (!a.up_lp ? a.none_lp : has ? a.up_lp[up] : quiet_nan());
   const float g_H = s1.y == 0.f ? 0.f : s1.y * (!a.up_H ? a.none_H : has ? a.up_H[up] : quiet_nan());
-  if (g_lp == 0.f && g_H == 0.f) {
+  // an id that has left the vocabulary since the forward call: its place would be next to the row
+  const bool in_vocab = id >= 0 && (int64_t)id < a.vocab;
+  if (!in_vocab || (g_lp == 0.f && g_H == 0.f)) {
     const bool same = run.aligned_with(grad);
     uint32_t z[8] = {};
     for (int u = tid; u < run.n; u += T) run.store(grad, same, u, z);

@@ -60,3 +60,34 @@ def test_single_nans(dtype, n, V):
         _score(dev, xs, ids, 1.0, dtype, rng, f"{n} x {V}", some=some)
         rows = _rows(xs, ids, 1.0, dtype)
         _policy(dev, ids, rows, _policy_inputs(rng, rows), dtype, 1.0, f"{n} x {V}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("op", ["score", "policy", "preference"])
+def test_backward_with_tokens_that_have_changed(dtype, op):
+    """Ids that have left the vocabulary since the forward call: their rows do not count, and nothing next to a row is
+    written."""
+    import logits_sampling_gb300 as ls
+    rng = np.random.default_rng(8)
+    for V, n in ((1003, 9), (20001, 7)):
+        dev, _ = _logits(_normal(rng, n, V), dtype, 3, 6)
+        ids = _dev(rng.integers(0, V, n), np.int32)
+        one = _dev(np.ones(n))
+        if op == "score":
+            stats, back = ls.token_log_probs(dev, ids)[2], lambda i, o: ls.token_log_probs_backward(dev, i, stats, one, out=o)
+        elif op == "policy":
+            stats, back = ls.policy_loss(dev, ids, one)[2], lambda i, o: ls.policy_loss_backward(dev, i, stats, out=o)
+        else:
+            stats = ls.preference_loss(dev, ids, _dev([0, 3, n], np.int32))[2]
+            back = lambda i, o: ls.preference_loss_backward(dev, i, stats, out=o)  # noqa: E731
+        out, _ = _logits(np.zeros((n, V), np.float32), dtype, 3, 6)
+        whole = out.as_strided((n * (V + 6) + 4,), (1,), 0)
+        assert back(ids, out).any(1).all()
+        for far in (-1, -2, -3, V, V + 1, V + 5, V + 12, -2 ** 31, 2 ** 31 - 1):
+            whole.fill_(77.0)
+            token = np.full(n, far)
+            token[1] = int(ids[1])
+            got = back(_dev(token, np.int32), out)
+            assert (out.as_strided((n, 6), (V + 6, 1), out.storage_offset() + V)[:-1] == 77).all(), far
+            assert (whole[:3] == 77).all() and (whole[n * (V + 6) - 3:] == 77).all(), far
+            assert got[1].any() and not got[0].any() and not got[2:].any(), far
