@@ -158,7 +158,8 @@ typedef struct {
  * u = s(chosen) - s(rejected) and h = beta u - margin: the loss of each pair.
  * A difference of two log-probs of -inf is 0.  A pair whose offsets descend,
  * or leave [0, n] or what the list's first and last offset span, gives
- * NaN, gradient 0 and LS_ROW_ERR_BAD_OFFSETS.
+ * NaN, gradient 0 and LS_ROW_ERR_BAD_OFFSETS.  Where such a pair leaves a row in
+ * the answers of two others, its gradient is the first one's alone.
  *
  *   out_loss        device float[pairs]
  *   out_log_ratios  device float[2 * pairs]: s of each answer, or NULL

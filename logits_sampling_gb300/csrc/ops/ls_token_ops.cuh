@@ -19,13 +19,15 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct alignas(16) TokenStats {
   float M, over;          // reference of the sum, 1 / (S T)
   float id_lp, id_H;      // the token's gradient: g_lp * id_lp - g_H * id_H
-  float g_lp, g_H;        // the loss's slopes; both 0: the row does not count
-  int32_t up;             // the entry of the gradient from above that belongs to the row
+  float g_lp;             // the loss's slopes g_lp and g_H; both 0: the row does not count
+  int32_t up;             // the entry of the gradient from above that belongs to the row (kNoPair: none yet)
+  float g_H;
   float mean;             // H - ln S
   float dirty;            // not 0: the row may hold NaNs
   float term, w;          // preference: weight * (lp - ref), the weight of a row that counts
   float pad;
 };
+constexpr int32_t kNoPair = 0x7FFFFFFF;
 static_assert(sizeof(TokenStats) == sizeof(float) * LS_TOKEN_STATS, "the header's size of a row's stats");
 
 enum TokenKind { KIND_SCORE, KIND_POLICY, KIND_PREFERENCE };
@@ -557,7 +559,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   if (entropy) st.id_H = lp == kNegInf ? 0.f : expf(lp) * (lp + H) * a.inv_T;
   st.dirty = dirty || entropy ? 1.f : 0.f;  // with entropies NaNs go unseen
   st.g_lp = st.g_H = st.term = st.w = 0.f;
-  st.up = (int32_t)i;
+  st.up = a.kind == KIND_PREFERENCE ? kNoPair : (int32_t)i;
   if (a.kind == KIND_SCORE) {
     st.g_lp = st.g_H = 1.f;
     a.out_loss[i] = lp;
@@ -610,7 +612,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   if (write && a.out_stats) {
     float4* out = reinterpret_cast<float4*>(a.out_stats + i);
     out[0] = make_float4(st.M, st.over, st.id_lp, st.id_H);
-    out[1] = make_float4(st.g_lp, st.g_H, __int_as_float(st.up), st.mean);
+    out[1] = make_float4(st.g_lp, __int_as_float(st.up), st.g_H, st.mean);
     out[2] = make_float4(st.dirty, st.term, st.w, 0.f);
   }
   return st;

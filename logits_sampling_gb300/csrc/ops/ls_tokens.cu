@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   }
   for (int64_t i = lo + tid; i < hi; i += kPairThreads) {
     const float w = i < lo + kPairThreads ? mine : a.stats[i].w;
-    a.stats[i].g_lp = w == 0.f ? 0.f : i < mid ? slope * w * over[0] : -slope * w * over[1];
-    a.stats[i].up = p;
+    const float g = w == 0.f ? 0.f : i < mid ? slope * w * over[0] : -slope * w * over[1];
+    // of two pairs (a list that descends elsewhere may give a row to both) the first: the slope and the pair in one word
+    atomicMin(reinterpret_cast<unsigned long long*>(&a.stats[i].g_lp),
+              (unsigned long long)(uint32_t)p << 32 | __float_as_uint(g));
   }
 }
 
@@ -223,11 +225,11 @@ __global__ void __launch_bounds__(kBackThreads, 1024 / kBackThreads)
   st.id_H = s0.w;
   st.mean = s1.w;
   st.dirty = in[2].x;
-  const int32_t id = a.ids[i], up = __float_as_int(s1.z);
+  const int32_t id = a.ids[i], up = __float_as_int(s1.y);
   const bool has = up >= 0 && up < a.ups;  // stats of another call do not lead out of bounds
   // a slope of 0 counts nothing, whatever the gradient from above
   const float g_lp = s1.x == 0.f ? 0.f : s1.x * (!a.up_lp ? a.none_lp : has ? a.up_lp[up] : quiet_nan());
-  const float g_H = s1.y == 0.f ? 0.f : s1.y * (!a.up_H ? a.none_H : has ? a.up_H[up] : quiet_nan());
+  const float g_H = s1.z == 0.f ? 0.f : s1.z * (!a.up_H ? a.none_H : has ? a.up_H[up] : quiet_nan());
   // an id that has left the vocabulary since the forward call: its place would be next to the row
   const bool in_vocab = id >= 0 && (int64_t)id < a.vocab;
   if (!in_vocab || (g_lp == 0.f && g_H == 0.f)) {

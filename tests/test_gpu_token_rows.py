@@ -91,3 +91,25 @@ def test_backward_with_tokens_that_have_changed(dtype, op):
             assert (out.as_strided((n, 6), (V + 6, 1), out.storage_offset() + V)[:-1] == 77).all(), far
             assert (whole[:3] == 77).all() and (whole[n * (V + 6) - 3:] == 77).all(), far
             assert got[1].any() and not got[0].any() and not got[2:].any(), far
+
+
+def test_answers_that_overlap():
+    """A list that descends may give a row to two pairs: its pair is bad, and such a row's gradient is the first one's."""
+    import logits_sampling_gb300 as ls
+    import torch
+    rng = np.random.default_rng(9)
+    n, V = 900, 64
+    dev, _ = _logits(_normal(rng, n, V), "f32")
+    ids = _dev(rng.integers(0, V, n), np.int32)
+    first = ls.preference_loss(dev, ids, _dev([0, 300, 800, 800, 900], np.int32))
+    for bad in ([0, 300, 800, 900, 5, 500, 900], [0, 300, 800, 850, 0, 10, 790, 790, 900]):
+        pairs = len(bad) // 2
+        for _ in range(20):
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            loss, _, stats = ls.preference_loss(dev, ids, _dev(bad, np.int32), error_word=err)
+            assert int(err) == ls.LS_ROW_ERR_BAD_OFFSETS and torch.isnan(loss[1]) and torch.isfinite(loss[2:]).all()
+            assert torch.equal(loss[0], first[0][0])
+            up = torch.arange(1.0, pairs + 1, device="cuda")
+            got = ls.preference_loss_backward(dev, ids, stats, up)
+            want = ls.preference_loss_backward(dev, ids, first[2], torch.ones(2, device="cuda"))
+            assert torch.equal(got[:800], want[:800])
