@@ -103,9 +103,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   }
   Exact v[4] = {};  // sum and weight of the chosen, of the rejected answer
   float mine = 0.f;  // the weight of this thread's first row
-  for (int64_t i = lo + tid; i < hi; i += kPairThreads) {
+  const int64_t first = (int64_t)lo + tid;  // past 2^31 in the last rows of the largest batch
+  for (int64_t i = first; i < hi; i += kPairThreads) {
     const float term = a.stats[i].term, w = a.stats[i].w;
-    if (i < lo + kPairThreads) mine = w;
+    if (i == first) mine = w;
     const int k = i < mid ? 0 : 2;
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
       a.out_log_ratios[2 * (int64_t)p + 1] = s[1];
     }
   }
-  for (int64_t i = lo + tid; i < hi; i += kPairThreads) {
-    const float w = i < lo + kPairThreads ? mine : a.stats[i].w;
+  for (int64_t i = first; i < hi; i += kPairThreads) {
+    const float w = i == first ? mine : a.stats[i].w;
     const float g = w == 0.f ? 0.f : i < mid ? slope * w * over[0] : -slope * w * over[1];
     // of two pairs (a list that descends elsewhere may give a row to both) the first: the slope and the pair in one word
     atomicMin(reinterpret_cast<unsigned long long*>(&a.stats[i].g_lp),
