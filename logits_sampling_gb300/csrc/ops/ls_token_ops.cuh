@@ -25,7 +25,7 @@ struct alignas(16) TokenStats {
   float mean;             // H - ln S
   float dirty;            // not 0: the row may hold NaNs
   float term, w;          // preference: weight * (lp - ref), the weight of a row that counts
-  float pad;
+  float term_lo;          // what `term` has lost to its rounding
 };
 constexpr int32_t kNoPair = 0x7FFFFFFF;
 static_assert(sizeof(TokenStats) == sizeof(float) * LS_TOKEN_STATS, "the header's size of a row's stats");
@@ -503,10 +503,8 @@ __device__ __forceinline__ void load_inputs(const TokenArgs& a, int64_t i, RowIn
   in.ref = a.policy.ref_log_probs ? a.policy.ref_log_probs[i] : 0.f;
 }
 
-// a + rest - b of two log-probs, 0 where both are -inf.
-__device__ __forceinline__ float log_ratio(float a, float rest, float b) {
-  return a == kNegInf && b == kNegInf ? 0.f : (a - b) + rest;
-}
+// a - b of two log-probs, 0 where both are -inf.
+__device__ __forceinline__ float log_ratio(float a, float b) { return a == kNegInf && b == kNegInf ? 0.f : a - b; }
 // RN(a + b); what the rounding lost is added to `lost` (Knuth's two-sum).
 __device__ __forceinline__ float two_sum(float a, float b, float& lost) {
   const float s = a + b, v = s - a;
@@ -558,7 +556,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   st.id_H = quiet_nan();
   if (entropy) st.id_H = lp == kNegInf ? 0.f : expf(lp) * (lp + H) * a.inv_T;
   st.dirty = dirty || entropy ? 1.f : 0.f;  // with entropies NaNs go unseen
-  st.g_lp = st.g_H = st.term = st.w = 0.f;
+  st.g_lp = st.g_H = st.term = st.w = st.term_lo = 0.f;
   st.up = a.kind == KIND_PREFERENCE ? kNoPair : (int32_t)i;
   if (a.kind == KIND_SCORE) {
     st.g_lp = st.g_H = 1.f;
@@ -568,7 +566,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     const ls_policy& p = a.policy;
     const float A = in.A;
     // from lp as it is returned: a policy that has not moved has ratio 1 and KL 0
-    const float ratio = p.old_log_probs ? expf(log_ratio(lp, 0.f, in.old)) : lp == lp ? 1.f : lp;
+    const float ratio = p.old_log_probs ? expf(log_ratio(lp, in.old)) : lp == lp ? 1.f : lp;
     float s = 0.f, slope = 0.f;
     if (A != 0.f) {
       const float u = ratio * A, v = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * A;
@@ -581,7 +579,7 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     }
     float kl = 0.f, kl_slope = 0.f;
     if (p.ref_log_probs) {
-      const float d = -log_ratio(lp, 0.f, in.ref);
+      const float d = -log_ratio(lp, in.ref);
       if (p.kl == LS_KL_K1) {
         kl = -d;
         kl_slope = 1.f;
@@ -607,13 +605,17 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     if (write && a.out_metrics) a.out_metrics[i] = make_float4(lp, entropy ? H : 0.f, kl, ratio);
   } else {
     st.w = w;
-    st.term = w * (a.policy.ref_log_probs ? log_ratio(lp, rest, in.ref) : lp);
+    // w (lp + rest - ref); in.ref is 0 where there is none
+    const bool both = a.policy.ref_log_probs && lp == kNegInf && in.ref == kNegInf;
+    const float d = both ? 0.f : two_sum(lp, -in.ref, rest);
+    st.term = w * d;
+    st.term_lo = fabsf(st.term) < kPosInf ? fmaf(w, d, -st.term) + w * rest : 0.f;
   }
   if (write && a.out_stats) {
     float4* out = reinterpret_cast<float4*>(a.out_stats + i);
     out[0] = make_float4(st.M, st.over, st.id_lp, st.id_H);
     out[1] = make_float4(st.g_lp, __int_as_float(st.up), st.g_H, st.mean);
-    out[2] = make_float4(st.dirty, st.term, st.w, 0.f);
+    out[2] = make_float4(st.dirty, st.term, st.w, st.term_lo);
   }
   return st;
 }

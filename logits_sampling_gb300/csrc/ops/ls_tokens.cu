@@ -105,12 +105,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const PairArgs a) {
   float mine = 0.f;  // the weight of this thread's first row
   const int64_t first = (int64_t)lo + tid;  // past 2^31 in the last rows of the largest batch
   for (int64_t i = first; i < hi; i += kPairThreads) {
-    const float term = a.stats[i].term, w = a.stats[i].w;
+    const float term = a.stats[i].term, w = a.stats[i].w, term_lo = a.stats[i].term_lo;
     if (i == first) mine = w;
     const int k = i < mid ? 0 : 2;
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
-      v[q].add(k == q ? term : 0.f);
+      v[q].add(k == q ? term : 0.f, k == q ? term_lo : 0.f);
       v[q + 1].add(k == q ? w : 0.f);
     }
   }

@@ -113,3 +113,24 @@ def test_answers_that_overlap():
             got = ls.preference_loss_backward(dev, ids, stats, up)
             want = ls.preference_loss_backward(dev, ids, first[2], torch.ones(2, device="cuda"))
             assert torch.equal(got[:800], want[:800])
+
+
+def test_a_loss_without_reference_sums_unrounded_log_probs():
+    """1000 rows that allow 1069 ids against 1000 that allow 1070, all alike: their sums differ by 1000 ln(1070 / 1069).
+
+    A row's S is a whole number, and exact; the compensation of the exponentials' mean error is 5.05e-8 (1 - 1 / S) on
+    both sides; log2 of 1.044 is off by 2^-28 at most.  So a row's part of the difference is off by less than 1e-8, and
+    5e-8 is allowed.  Log-probs rounded to fp32, next to -7, would be off by -2.9e-7 in the one answer's rows and by
+    1.3e-7 in the other's.  The loss is u^2 but for 1 / (2 beta)."""
+    import logits_sampling_gb300 as ls
+    import torch
+    n, V = 2000, 2048
+    x = torch.full((n, V), -float("inf"), device="cuda")
+    x[:1000, :1069] = 0.0
+    x[1000:, :1070] = 0.0
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    beta = float(np.float32(2.0 ** 20))
+    loss, _, _ = ls.preference_loss(x, ids, _dev([0, 1000, 2000], np.int32), beta=beta, loss="ipo")
+    u = 1000 * np.log(1070 / 1069)
+    got = float(loss[0]) ** 0.5 + 0.5 / beta
+    assert abs(got - u) <= 1000 * 5e-8 + 4 * R.EPS * u, (got, u)
