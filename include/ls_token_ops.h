@@ -49,7 +49,7 @@ enum { LS_ROW_ERR_BAD_OFFSETS = 16 };
  * ls_token_log_probs -- out_log_probs[i] = lp, out_entropy[i] = H.
  *
  *   ids            device int32[n]
- *   temperature    finite, > 0
+ *   temperature    finite, > 0, and with log2(e) / temperature finite (4.3e-39 and more)
  *   out_log_probs  device float[n]
  *   out_entropy    device float[n], or NULL: no entropies
  *   out_stats      device float[LS_TOKEN_STATS * n], 16-byte aligned: what the

@@ -318,7 +318,8 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // The checks that the calls share.
 static bool rows_ok(const void* logits, ls_dtype dtype, int64_t vocab, int64_t row_stride, const int32_t* ids,
                     float temperature) {
-  return matrix_ok(logits, dtype, vocab, row_stride) && ids && temperature > 0.f && finite(temperature);
+  return matrix_ok(logits, dtype, vocab, row_stride) && ids && temperature > 0.f && finite(temperature) &&
+         finite(kLog2e / temperature);
 }
 static bool policy_ok(const ls_policy* p) {
   return p && p->advantages && p->clip_low >= 0.f && p->clip_low <= 1.f && p->clip_high >= 0.f &&
