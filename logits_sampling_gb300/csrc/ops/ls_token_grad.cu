@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
   if (st.whole > keep) st.template load<LOAD_PLAIN>(st.whole - 1 - keep, first);
   if (C > 1) cluster_moments<kEntropy>(r, careful, c, parts, C, rank);
   if (tid == 0) {
-    const TokenStats s = finish_row(a, i, r, in, kEntropy, careful, rank == 0);
+    const TokenStats s = finish_row<kEntropy, KIND_POLICY>(a, i, r, in, careful, rank == 0);
     g.init(s, s.g_lp, s.g_H, c);
   }
   __syncthreads();

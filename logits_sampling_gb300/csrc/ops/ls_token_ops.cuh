@@ -513,10 +513,12 @@ __device__ __forceinline__ float two_sum(float a, float b, float& lost) {
 }
 
 // The loss's slopes and outputs of row i from its moments (one thread; `write`:
-// this one stores the outputs).
+// this one stores the outputs).  kKind: the operator where a kernel has only one.
+template <bool kEntropy, int kKind = -1>
 __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, const Moments& r, const RowInputs& in,
-                                                 bool entropy, bool dirty, bool write = true) {
+                                                 bool dirty, bool write = true) {
   const float x = in.x, w = in.w;
+  const int kind = kKind >= 0 ? kKind : a.kind;
   TokenStats st;
   float lp, H;
   st.M = r.m;
@@ -542,10 +544,12 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     lp = (x == r.m ? 0.f : (x - r.m) / a.temperature) - kLn2 * ((float)k + log2s);
   }
   st.mean = H = quiet_nan();  // a gradient of what was not computed shows
-  if (entropy) {
-    const float y = r.e / r.s;
+  if (kEntropy) {  // ln 2 (k + log2 s - E / S), put together likewise; E's terms are all low, S's but the 1
+    const float over = 1.f / r.s, y = r.e * over;
+    float lo = kExpLow * (kLog2e * fmaxf(1.f - over, 0.f) - y * over) - fmaf(-y, r.s, r.e) * over;
+    const float z = two_sum((float)k, log2s, lo), t = two_sum(z, -y, lo), v = kLn2 * t;
     st.mean = -kLn2 * y;
-    H = kLn2 * (((float)k - y) + log2s);
+    H = v + (fmaf(kLn2, t, -v) + fmaf(-1.9046543e-9f, t, kLn2 * lo));
   }
   if (r.m == kNegInf) {
     lp = H = quiet_nan();
@@ -554,15 +558,15 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
   st.over = r.m == kNegInf ? quiet_nan() : __frcp_rn(r.s * a.temperature);
   st.id_lp = -expm1f(lp) * a.inv_T;  // 1 - q
   st.id_H = quiet_nan();
-  if (entropy) st.id_H = lp == kNegInf ? 0.f : expf(lp) * (lp + H) * a.inv_T;
-  st.dirty = dirty || entropy ? 1.f : 0.f;  // with entropies NaNs go unseen
+  if (kEntropy) st.id_H = lp == kNegInf ? 0.f : expf(lp) * (lp + H) * a.inv_T;
+  st.dirty = dirty || kEntropy ? 1.f : 0.f;  // with entropies NaNs go unseen
   st.g_lp = st.g_H = st.term = st.w = st.term_lo = 0.f;
-  st.up = a.kind == KIND_PREFERENCE ? kNoPair : (int32_t)i;
-  if (a.kind == KIND_SCORE) {
+  st.up = kind == KIND_PREFERENCE ? kNoPair : (int32_t)i;
+  if (kind == KIND_SCORE) {
     st.g_lp = st.g_H = 1.f;
     a.out_loss[i] = lp;
     if (a.out_entropy) a.out_entropy[i] = H;
-  } else if (a.kind == KIND_POLICY) {
+  } else if (kind == KIND_POLICY) {
     const ls_policy& p = a.policy;
     const float A = in.A;
     // from lp as it is returned: a policy that has not moved has ratio 1 and KL 0
@@ -602,8 +606,8 @@ __device__ __forceinline__ TokenStats finish_row(const TokenArgs& a, int64_t i, 
     if (write) a.out_loss[i] = w * loss;
     st.g_lp = w * slope;
     st.g_H = p.entropy_coef != 0.f ? -w * p.entropy_coef : 0.f;
-    if (write && a.out_metrics) a.out_metrics[i] = make_float4(lp, entropy ? H : 0.f, kl, ratio);
-  } else {
+    if (write && a.out_metrics) a.out_metrics[i] = make_float4(lp, kEntropy ? H : 0.f, kl, ratio);
+  } else if (!kEntropy) {  // a preference loss has no entropies
     st.w = w;
     // w (lp + rest - ref); in.ref is 0 where there is none
     const bool both = a.policy.ref_log_probs && lp == kNegInf && in.ref == kNegInf;

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, i
   }
   let_next_start();
   if (C > 1) cluster_moments<kEntropy>(r, careful, c, parts, C, rank);
-  if (tid == 0 && rank == 0) finish_row(a, i, r, in, kEntropy, careful);
+  if (tid == 0 && rank == 0) finish_row<kEntropy>(a, i, r, in, careful);
 }
 
 // The sums of a pair's two answers, its loss, and the slope of each of its rows.
