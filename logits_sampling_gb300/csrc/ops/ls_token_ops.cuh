@@ -338,16 +338,19 @@ struct Kept {
 // up all that follow against it, without looking for larger ones: for two entries two
 // conversions, one multiplication, two exponentials and one addition, and no branch
 // but one per stage for a warp that has found no entry yet.  A reference is always an
-// entry of the row, so a sum against the largest of them is at least 1.  A thread's sum
-// does against a reference below the maximum as long as it stays within kMostSum (an
-// exponent of up to 40 is rounded to 2^-19, 7e-7 of its term; and a warp's sum of 2^126
-// times its reference would count 0 beside another warp's reference above that); where
-// it does not, or where there is a NaN, the row is taken again, `careful`: with a
-// reference that rises with the maximum and NaNs read as -inf, as the row's ends are
-// always taken.  An entropy's E / S is a mean of exponents and loses digits to a distant
-// reference (1.4e-6 of H in 1024 x 262144 fp32 with a head at 20, 1e-7 with the maximum;
-// 149.6 and 150.2 us): there the reference follows the maximum.
-constexpr float kMostSum = 1.0995116e12f, kLeastSum = 0.5f;  // 2^40; below any sum that holds its reference's own 1
+// entry of the row, so a sum against the largest of them is at least 1.  A sum does
+// against a reference below the maximum as long as it stays within kMostSum, and each
+// thread's within kThreadSum (an exponent below 64 is rounded to 2^-18, so its term is
+// off by up to 1.3e-6; and past 2^126 a sum would count 0 beside a warp whose reference
+// lies that far above).  Where it does not, or where there is a NaN, the row is taken
+// again, `careful`: with a reference that rises with the maximum and NaNs read as -inf,
+// as the row's ends are always taken.  An entropy's E / S is a mean of exponents and
+// loses digits to a distant reference (1.4e-6 of H in 1024 x 262144 fp32 with a head at
+// 20, 1e-7 with the maximum; 149.6 and 150.2 us): there the reference follows the
+// maximum.
+constexpr float kMostSum = 1.0995116e12f;    // 2^40
+constexpr float kThreadSum = 4.6116860e18f;  // 2^62: with 2^40, 2048 x 128256 at T = 0.3 took 88 us instead of 76
+constexpr float kLeastSum = 0.5f;            // below any sum that holds its reference's own 1
 
 template <int kHow, bool kKeep, bool kEntropy, typename TIn, int T>
 __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn, T>& st, typename Run<TIn, T>::Stage& a,
@@ -413,7 +416,7 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
   if (!kEntropy) {  // each thread's: another warp's reference may hide what is past it
     float lo, hi;
     unpack2(acc.s0, lo, hi);
-    most = lo + hi < kMostSum;
+    most = lo + hi < kThreadSum;
   }
   if (!fast || !most) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
 }
