@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs
     RowSum<kEntropy> acc;
     sum_run<LOAD_KEEP, true>(run, st, first, acc, c, careful, kept);
     r = block_moments<T / 32, kEntropy>(acc.moments(), c, red);
-    if (careful || sum_ok(r.s)) break;  // the same in every thread
+    if (careful || sum_ok(r)) break;  // the same in every thread
     careful = true;
     __syncthreads();  // red is read
   }

@@ -420,7 +420,10 @@ __device__ __forceinline__ void sum_run(const Run<TIn, T>& run, const Stages<TIn
   }
   if (!fast || !most) acc.s0 = pack2(quiet_nan(), quiet_nan());  // asks for a careful pass
 }
-__device__ __forceinline__ bool sum_ok(float s) { return s < kMostSum && s > kLeastSum; }  // NaN compares false
+// Whether a share's sum stands (NaN compares false); one of nothing but -inf does.
+__device__ __forceinline__ bool sum_ok(const Moments& r) {
+  return (r.s < kMostSum && r.s > kLeastSum) || (r.m == kNegInf && r.s == 0.f);
+}
 
 // The block's moments from each warp's maximum and thread's sums, in every
 // thread; the order of the sums is fixed.  `red` holds one per warp.

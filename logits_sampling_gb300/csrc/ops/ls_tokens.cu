@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, i
     RowSum<kEntropy> acc;
     sum_run<LOAD_ONCE, false>(run, st, first, acc, c, careful, Kept<T>{nullptr, 0});
     r = block_moments<T / 32, kEntropy>(acc.moments(), c, red);
-    if (careful || sum_ok(r.s)) break;  // the same in every thread
+    if (careful || sum_ok(r)) break;  // the same in every thread
     careful = true;
     __syncthreads();  // red is read
   }
