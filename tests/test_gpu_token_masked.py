@@ -157,3 +157,29 @@ def test_entropy_gradients_of_masked_entries(dtype, T, g_H, level):
             fused = _f64(fused[:6])
             for got, sign in ((grad, 1.0), (fused, -1.0)):
                 _check_gradient(got, rows, np.zeros(n), sign * up, dtype, f"{n} rows of {fill}")
+
+
+@pytest.mark.parametrize("n,V", [(8, 9001), (8, 70001), (140, 70001), (320, 33001), (620, 70001), (1300, 20011)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_nan_among_masked_entries(dtype, n, V):
+    """Rows of -inf but for one allowed id and one NaN, at their ends, next to each other and in shares of their own: the
+    NaN has gradient 0, the allowed id log-prob 0 and entropy 0."""
+    import logits_sampling_gb300 as ls
+    import torch
+    rng = np.random.default_rng(V)
+    x = np.full((n, V), -np.inf, np.float32)
+    ids = np.full(n, -1)
+    places = [(0, V - 1), (V - 1, 0), (V // 2, V // 2 + 1), (700, V - 700), (V - 700, 700), (V - 3, V - 2), (1, 0),
+              tuple(rng.choice(V, 2, replace=False))]
+    for i, (one, nan) in enumerate(places):
+        x[i, one], x[i, nan], ids[i] = -12.0, np.nan, one
+    dev, _ = _logits(x, dtype, 3, 5)
+    idd, g = _dev(ids, np.int32), _dev(rng.standard_normal(n))
+    for entropy in (False, True):
+        lp, h, stats = ls.token_log_probs(dev, idd, entropy=entropy)
+        assert float(lp[:8].abs().max()) <= 2 * R.EXP and (not entropy or float(h[:8].abs().max()) <= 2 * R.EXP)
+        back = ls.token_log_probs_backward(dev, idd, stats, g, g if entropy else None)
+        _, fused, _ = ls.policy_loss_grad(dev, idd, g, entropy_coef=0.1 * entropy)
+        for grad in (back, fused):  # 1 - q of the only entry
+            assert torch.isfinite(grad).all() and float(grad.abs().max()) <= float(g.abs().max()) * 8 * R.EXP
+            assert not grad.scatter(1, idd.clamp(0).long()[:, None], 0.0).any()
