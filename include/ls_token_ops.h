@@ -107,8 +107,9 @@ typedef struct {
  * The gradient goes through u where u <= v and the bound of dual_clip does not
  * hold, through KL and through H.  A = 0 gives s = 0 whatever r is.  A log-ratio
  * of two log-probs of -inf (a token that both sides exclude) is 0.  Ratio and KL
- * are those of lp as it is returned in fp32: where old and ref are what the same
- * rows gave before, they are 1 and 0.  Where the loss is infinite (a token that one
+ * are those of lp as it is returned in fp32: where old and ref are what this call gave
+ * for the same rows before, they are 1 and 0 (another call may add a row up in another
+ * order: within a rounding).  Where the loss is infinite (a token that one
  * side alone excludes) its gradient is not finite.
  *
  *   out_loss     device float[n]

@@ -10,10 +10,10 @@ namespace lsg {
 namespace ops {
 
 // Bound by DRAM and by what does not overlap on an SM with two rows: 2048 x 128256
-// bf16 180 us (5.8 TB/s on one read and one write; 13 % of the second reads miss L2,
-// which makes 6.2), 1024 x 262144 fp32 with entropies 393 (5.5 TB/s; the exchange of
-// a row's CTAs and its scalars are a quarter of the stalls). The two calls take 230
-// and 459.
+// bf16 181 us (5.8 TB/s on one read and one write; 15 % of the second reads miss L2,
+// which makes 6.2), 1024 x 262144 fp32 with entropies 397 (5.4 TB/s; 18 % miss L2, and
+// the exchange of a row's CTAs and its scalars, barrier and membar, are a quarter of the
+// stalls of its eight CTAs of 256 threads). The two calls take 232 and 461.
 template <typename TIn, bool kEntropy, int T>
 __global__ void __launch_bounds__(T, 1024 / T) token_grad_kernel(const TokenArgs a, int upc, int keep) {
   using E = Elem<TIn>;

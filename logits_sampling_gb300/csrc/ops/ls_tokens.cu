@@ -12,10 +12,10 @@
 namespace lsg {
 namespace ops {
 
-// Bound by DRAM where there are rows enough: 2048 x 128256 bf16 76 us (6.9 TB/s, the
-// measured copy rate), with entropies 84 (each stage's maximum is looked for), 1024 x
-// 262144 fp32 with entropies 150 (7.2 TB/s). Fewer rows by what is in flight: 672 x
-// 151936 31.3 us (6.5 TB/s), 64 x 128256 6.8, one row of 32000 3.5 (launch, two reads
+// Bound by DRAM where there are rows enough (a kernel that only reads reaches 7.7 TB/s):
+// 2048 x 128256 bf16 78 us (6.7 TB/s), with entropies 84 (each stage's maximum is looked
+// for), 1024 x 262144 fp32 with entropies 150 (7.2). Fewer rows by what is in flight: 672 x
+// 151936 32.6 us (6.3 TB/s), 64 x 128256 7.1, one row of 32000 3.6 (launch, two reads
 // one after the other, barrier, scalars).
 template <typename TIn, bool kEntropy, int T>
 __global__ void __launch_bounds__(T, 1024 / T) token_kernel(const TokenArgs a, int upc) {
